@@ -1,0 +1,471 @@
+// gvr_cache.cu -- block tables and slot maps, and the 4-bit cache's writes and reads (declared in
+// include/gvr_cache.h).
+#include <cuda_bf16.h>
+
+#include <mutex>
+
+#include "gvr_cache_common.cuh"
+
+namespace gvrc {
+
+namespace {
+struct Device {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  int sms = 0;
+};
+Device g_devices[kMaxDevices];
+}  // namespace
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  Device& d = g_devices[dev];
+  std::call_once(d.once, [&d, dev]() {
+    d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+  });
+  *sms = d.sms;
+  return d.err;
+}
+
+namespace {
+
+// ------------------------------------------------------------------------------------- tables
+constexpr int TABLE_THREADS = 512;
+constexpr int TABLE_WARPS = TABLE_THREADS / 32;
+
+struct TableParams {
+  const int32_t* cached;
+  const int32_t* lens;
+  const int32_t* free_pages;
+  int32_t* table;
+  int32_t* slots;
+  int32_t* counts;
+  int64_t table_stride;
+  int64_t num_slots;
+  int32_t requests, ratio, page_shift, num_free, width;
+};
+
+// a + b for 0 <= a, b <= 2^31 - 1, at most 2^31 - 1: associative, so any order of summing gives
+// the same result.
+__device__ __forceinline__ int sat_add(int a, int b) { return int(min(uint32_t(a) + uint32_t(b), 0x7fffffffu)); }
+
+struct Growth {
+  int entries;     // e0: entries held before
+  int new_entries; // max(e1 - e0, 0)
+  int have;        // pages held before
+  int new_pages;
+  int missing;     // pages beyond the table's width
+};
+
+__device__ __forceinline__ Growth growth(const TableParams& p, int r) {
+  const int e0 = max(p.cached[r], 0) / p.ratio, e1 = max(p.lens[r], 0) / p.ratio;
+  Growth g;
+  g.entries = e0;
+  g.new_entries = max(e1 - e0, 0);
+  g.have = pages_of(e0, p.page_shift);
+  const int want = pages_of(e1, p.page_shift), need = min(want, p.width);
+  g.new_pages = max(need - g.have, 0);
+  g.missing = want - need;
+  return g;
+}
+
+// The last r with first[r] <= x (first is non-decreasing, first[0] = 0 <= x): the request that
+// element x of the concatenated lists belongs to, x being below their total.
+__device__ __forceinline__ int owner(const int* first, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Every CTA reads all lengths and scans them (8 bytes a request, from L2 after the first), then
+// takes its share of the two concatenated lists: new pages and new entries.  One launch, no
+// exchange between CTAs.  The smallest call is a chain of two global round trips (lengths, then a
+// page number) around the scan; the largest is bound by the 4 bytes written per slot.
+__global__ void __launch_bounds__(TABLE_THREADS) cache_tables_kernel(TableParams p) {
+  extern __shared__ int table_smem[];
+  int* page_first = table_smem;             // exclusive sums of new pages
+  int* entry_first = page_first + p.requests;  // exclusive sums of new entries
+  int* held = entry_first + p.requests;     // e0
+  __shared__ int warp_pages[TABLE_WARPS], warp_entries[TABLE_WARPS], warp_missing[TABLE_WARPS];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.requests + TABLE_THREADS - 1) / TABLE_THREADS;
+  const int r0 = min(tid * per, p.requests), r1 = min(r0 + per, p.requests);
+  int pages = 0, entries = 0, missing = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Growth g = growth(p, r);
+    page_first[r] = pages;
+    entry_first[r] = entries;
+    held[r] = g.entries;
+    pages = sat_add(pages, g.new_pages);
+    entries = sat_add(entries, g.new_entries);
+    missing = sat_add(missing, g.missing);
+  }
+  // inclusive scan over the threads' sums
+  int in_pages = pages, in_entries = entries;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, in_pages, d), b = __shfl_up_sync(0xffffffffu, in_entries, d);
+    if (lane >= d) {
+      in_pages = sat_add(in_pages, a);
+      in_entries = sat_add(in_entries, b);
+    }
+    missing = sat_add(missing, __shfl_xor_sync(0xffffffffu, missing, d));
+  }
+  int before_pages = __shfl_up_sync(0xffffffffu, in_pages, 1), before_entries = __shfl_up_sync(0xffffffffu, in_entries, 1);
+  if (lane == 0) before_pages = before_entries = 0;
+  if (lane == 31) {
+    warp_pages[warp] = in_pages;
+    warp_entries[warp] = in_entries;
+    warp_missing[warp] = missing;
+  }
+  __syncthreads();
+  int total_pages = 0, total_entries = 0, total_missing = 0;
+#pragma unroll
+  for (int w = 0; w < TABLE_WARPS; ++w) {
+    if (w == warp) {
+      before_pages = sat_add(before_pages, total_pages);
+      before_entries = sat_add(before_entries, total_entries);
+    }
+    total_pages = sat_add(total_pages, warp_pages[w]);
+    total_entries = sat_add(total_entries, warp_entries[w]);
+    total_missing = sat_add(total_missing, warp_missing[w]);
+  }
+  for (int r = r0; r < r1; ++r) {
+    page_first[r] = sat_add(page_first[r], before_pages);
+    entry_first[r] = sat_add(entry_first[r], before_entries);
+  }
+  __syncthreads();
+
+  if (blockIdx.x == 0 && tid == 0) {
+    const int taken = min(total_pages, p.num_free);
+    p.counts[0] = total_entries;
+    p.counts[1] = taken;
+    p.counts[2] = sat_add(total_missing, total_pages - taken);
+  }
+  const int64_t stride = int64_t(gridDim.x) * TABLE_THREADS, at = int64_t(blockIdx.x) * TABLE_THREADS + tid;
+  for (int64_t j = at; j < total_pages; j += stride) {
+    const int r = owner(page_first, p.requests, int(j));
+    const int block = pages_of(held[r], p.page_shift) + (int(j) - page_first[r]);
+    p.table[r * p.table_stride + block] = j < p.num_free ? p.free_pages[j] : -1;
+  }
+  // Four consecutive slots a thread: one search, one 16-byte store (where slots is aligned for it).
+  const bool wide = (reinterpret_cast<uintptr_t>(p.slots) & 15) == 0;
+  for (int64_t t4 = at * 4; t4 < p.num_slots; t4 += stride * 4) {
+    int slot[4] = {-1, -1, -1, -1};
+    if (t4 < total_entries) {
+      int r = owner(entry_first, p.requests, int(t4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t t = t4 + i;
+        if (t >= total_entries) break;
+        while (r + 1 < p.requests && entry_first[r + 1] <= t) ++r;
+        const int64_t entry = int64_t(held[r]) + (t - entry_first[r]);
+        const int64_t block = entry >> p.page_shift;
+        if (block >= p.width) continue;
+        const int64_t j = block - pages_of(held[r], p.page_shift) + page_first[r];  // place among the new pages
+        int page;
+        if (block < pages_of(held[r], p.page_shift)) page = p.table[r * p.table_stride + block];
+        else page = j < p.num_free ? p.free_pages[j] : -1;
+        slot[i] = slot_of(page, int(entry), p.page_shift);
+      }
+    }
+    if (wide && t4 + 4 <= p.num_slots) {
+      *reinterpret_cast<int4*>(p.slots + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t4 + i < p.num_slots) p.slots[t4 + i] = slot[i];
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ append and read
+constexpr int COPY_THREADS = 256;
+
+struct CopyParams {
+  uint8_t* data;
+  const int32_t* slots;
+  const void* k;
+  const void* v;
+  int64_t k_token, k_head, v_token, v_head;  // strides in elements
+  int64_t page_stride, work;                 // work: tokens * heads * blocks of a head
+  int32_t num_pages, heads, page_shift;
+  float k_scale, v_scale;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float2 to_f32(uint32_t two) {
+  if (BF16) return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+  return f16x2_to_f32(two);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t from_f32(float lo, float hi) {
+  uint32_t r;
+  if (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Largest magnitude of two 16-bit pairs, a NaN winning (maxima of the types' own bits).
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (BF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// One block of 16 values: scale (8 bits) and codes (16 x 4 bits).
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[8], float factor, uint2& codes) {
+  uint32_t m = x[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan<BF16>(m, x[i] & 0x7fff7fffu);
+  const float2 two = to_f32<BF16>(max_nan<BF16>(m, (m >> 16) | (m << 16)));
+  const uint32_t scale = f32_to_e4m3(two.x / (6.f * factor));
+  const float unit = f16x2_to_f32(e4m3x2_to_f16x2(scale)).x * factor;
+  uint32_t c[2] = {0, 0};
+  if (unit > 0.f) {  // neither 0 nor NaN
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = to_f32<BF16>(x[i]);
+      c[i >> 2] |= f32x2_to_e2m1(v.x / unit, v.y / unit) << (8 * (i & 3));
+    }
+  }
+  codes = make_uint2(c[0], c[1]);
+  return scale;
+}
+
+// Sixteen values as two 16-byte loads.
+__device__ __forceinline__ void load16(const uint4* src, uint32_t (&x)[8]) {
+  const uint4 a = __ldg(src), b = __ldg(src + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// Address of a slot's row of one head, or nullptr for a slot that names no entry.
+__device__ __forceinline__ uint8_t* row_of(const CopyParams& p, int slot, int head, int bytes) {
+  const int64_t off = slot_offset(slot, p.num_pages, p.page_shift, p.page_stride, p.heads, head, bytes);
+  return off < 0 ? nullptr : p.data + off;
+}
+
+// A thread takes one block of 16 values of K and the same block of V: neighbouring threads read
+// neighbouring 32-byte pieces and write neighbouring 8-byte pieces of one row.  Bound by the
+// bytes of K and V.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(COPY_THREADS) cache_append_kernel(CopyParams p) {
+  constexpr int BLOCKS = D / 16;
+  const int64_t i = int64_t(blockIdx.x) * COPY_THREADS + threadIdx.x;
+  if (i >= p.work) return;
+  const int b = int(i % BLOCKS);
+  const int64_t th = i / BLOCKS, t = th / p.heads;
+  const int h = int(th - t * p.heads);
+  uint8_t* row = row_of(p, p.slots[t], h, row_bytes(D));
+  if (!row) return;
+  uint32_t k[8], v[8];
+  load16(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k) + t * p.k_token + h * p.k_head + b * 16), k);
+  load16(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + t * p.v_token + h * p.v_head + b * 16), v);
+  uint2 kc, vc;
+  const uint32_t ks = quantise<BF16>(k, p.k_scale, kc), vs = quantise<BF16>(v, p.v_scale, vc);
+  *reinterpret_cast<uint2*>(row + b * 8) = kc;
+  *reinterpret_cast<uint2*>(row + D / 2 + b * 8) = vc;
+  row[D + b] = uint8_t(ks);
+  row[D + BLOCKS + b] = uint8_t(vs);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void dequantise(uint2 codes, uint32_t scale, float factor, uint4* dst) {
+  const float unit = f16x2_to_f32(e4m3x2_to_f16x2(scale)).x;
+  uint32_t out[8];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t h[4];
+    e2m1_to_f16x2(j ? codes.y : codes.x, h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 c = f16x2_to_f32(h[i]);
+      out[4 * j + i] = from_f32<BF16>(c.x * unit * factor, c.y * unit * factor);
+    }
+  }
+  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(COPY_THREADS) cache_read_kernel(CopyParams p) {
+  constexpr int BLOCKS = D / 16;
+  const int64_t i = int64_t(blockIdx.x) * COPY_THREADS + threadIdx.x;
+  if (i >= p.work) return;
+  const int b = int(i % BLOCKS);
+  const int64_t th = i / BLOCKS, t = th / p.heads;
+  const uint8_t* row = row_of(p, p.slots[t], int(th - t * p.heads), row_bytes(D));
+  uint2 kc = make_uint2(0, 0), vc = kc;
+  uint32_t ks = 0, vs = 0;
+  if (row) {
+    if (p.k) kc = *reinterpret_cast<const uint2*>(row + b * 8), ks = row[D + b];
+    if (p.v) vc = *reinterpret_cast<const uint2*>(row + D / 2 + b * 8), vs = row[D + BLOCKS + b];
+  }
+  if (p.k) dequantise<BF16>(kc, ks, p.k_scale, static_cast<uint4*>(const_cast<void*>(p.k)) + i * 2);
+  if (p.v) dequantise<BF16>(vc, vs, p.v_scale, static_cast<uint4*>(const_cast<void*>(p.v)) + i * 2);
+}
+
+using CopyKernel = void (*)(CopyParams);
+
+template <bool BF16>
+CopyKernel copy_kernel(int dim, bool append) {
+  if (dim == 64) return append ? cache_append_kernel<64, BF16> : cache_read_kernel<64, BF16>;
+  if (dim == 128) return append ? cache_append_kernel<128, BF16> : cache_read_kernel<128, BF16>;
+  return append ? cache_append_kernel<256, BF16> : cache_read_kernel<256, BF16>;
+}
+
+gvr_status launch_copy(const gvr_cache* c, CopyParams& p, int32_t dtype, int64_t tokens, bool append, void* stream) {
+  const int64_t blocks = c->head_dim / 16;
+  if (tokens > INT64_MAX / 4096 / c->num_kv_heads) return GVR_ERR_ARG;
+  p.data = static_cast<uint8_t*>(c->data);
+  p.page_stride = c->page_stride;
+  p.num_pages = int32_t(c->num_pages);
+  p.work = tokens * c->num_kv_heads * blocks;
+  p.heads = c->num_kv_heads;
+  p.page_shift = log2_of(c->page_size);
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  const int64_t grid = (p.work + COPY_THREADS - 1) / COPY_THREADS;
+  if (grid > kIntMax) return GVR_ERR_ARG;
+  const CopyKernel kernel = dtype == GVR_BF16 ? copy_kernel<true>(c->head_dim, append) : copy_kernel<false>(c->head_dim, append);
+  void* args[] = {&p};
+  if (cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(uint32_t(grid)), dim3(COPY_THREADS), args, 0,
+                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return GVR_ERR_LAUNCH;
+  return GVR_OK;
+}
+
+// Attributes of the tables kernel, set once per device: its largest shared memory.
+struct TableDevice {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+TableDevice g_table_devices[kMaxDevices];
+
+}  // namespace
+}  // namespace gvrc
+
+extern "C" {
+
+gvr_status cache_row_bytes(int32_t head_dim, int32_t* bytes) {
+  if (!bytes) return GVR_ERR_NULL;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return GVR_ERR_ARG;
+  *bytes = gvrc::row_bytes(head_dim);
+  return GVR_OK;
+}
+
+gvr_status cache_tables(const int32_t* cached_lens, const int32_t* kv_lens, int64_t num_requests,
+                        int32_t compress_ratio, int32_t page_size, const int32_t* free_pages,
+                        int64_t num_free, int32_t* block_table, int64_t table_stride,
+                        int64_t table_width, int32_t* slots, int64_t num_slots, int32_t* counts,
+                        void* stream) {
+  using namespace gvrc;
+  if (num_requests < 0 || num_requests > GVR_CACHE_MAX_REQUESTS || compress_ratio < 1 || !page_size_ok(page_size) ||
+      num_free < 0 || num_free > kIntMax || num_slots < 0 || num_slots > kIntMax || table_width < 0 ||
+      table_width > kIntMax / page_size)
+    return GVR_ERR_ARG;
+  if (table_stride < table_width || table_stride > kIntMax) return GVR_ERR_STRIDE;
+  if (!counts || (num_requests > 0 && (!cached_lens || !kv_lens)) || (num_requests > 0 && table_width > 0 && !block_table) ||
+      (num_free > 0 && !free_pages) || (num_slots > 0 && !slots))
+    return GVR_ERR_NULL;
+  if (!aligned(cached_lens, 4) || !aligned(kv_lens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) ||
+      !aligned(slots, 4) || !aligned(counts, 4))
+    return GVR_ERR_ALIGN;
+  int sms = 0, dev = 0;
+  if (sm_count(&sms) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return GVR_ERR_LAUNCH;
+  TableDevice& td = g_table_devices[dev];  // sm_count has checked dev
+  std::call_once(td.once, [&td]() {
+    td.err = cudaFuncSetAttribute(cache_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  GVR_CACHE_MAX_REQUESTS * 3 * int(sizeof(int)));
+  });
+  if (td.err != cudaSuccess) return GVR_ERR_LAUNCH;
+  TableParams p = {};
+  p.cached = cached_lens;
+  p.lens = kv_lens;
+  p.free_pages = free_pages;
+  p.table = block_table;
+  p.slots = slots;
+  p.counts = counts;
+  p.table_stride = table_stride;
+  p.num_slots = num_slots;
+  p.requests = int32_t(num_requests);
+  p.ratio = compress_ratio;
+  p.page_shift = log2_of(page_size);
+  p.num_free = int32_t(num_free);
+  p.width = int32_t(table_width);
+  // Enough CTAs for one 16-byte store a thread, at most two per SM: the scan is repeated by each.
+  const int64_t want = (num_slots + 4 * TABLE_THREADS - 1) / (4 * TABLE_THREADS);
+  const int grid = int(want < 1 ? 1 : want > 2 * sms ? 2 * sms : want);
+  void* args[] = {&p};
+  if (cudaLaunchKernel(reinterpret_cast<const void*>(cache_tables_kernel), dim3(grid), dim3(TABLE_THREADS), args,
+                       size_t(num_requests) * 3 * sizeof(int), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return GVR_ERR_LAUNCH;
+  return GVR_OK;
+}
+
+gvr_status cache_append(const gvr_cache* cache, const void* k, int64_t k_token_stride,
+                        int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                        int64_t v_head_stride, int32_t dtype, const int32_t* slots,
+                        int64_t num_tokens, void* stream) {
+  using namespace gvrc;
+  const gvr_status s = check_cache(cache);
+  if (s != GVR_OK) return s;
+  if (num_tokens < 0 || (dtype != GVR_BF16 && dtype != GVR_F16)) return GVR_ERR_ARG;
+  if (num_tokens == 0) return GVR_OK;
+  if (!k || !v || !slots) return GVR_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return GVR_ERR_ALIGN;
+  for (int64_t stride : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+    if (stride < 0 || stride % 8 != 0 || stride > kIntMax) return GVR_ERR_STRIDE;
+  CopyParams p = {};
+  p.k = k;
+  p.v = v;
+  p.slots = slots;
+  p.k_token = k_token_stride;
+  p.k_head = k_head_stride;
+  p.v_token = v_token_stride;
+  p.v_head = v_head_stride;
+  return launch_copy(cache, p, dtype, num_tokens, true, stream);
+}
+
+gvr_status cache_read(const gvr_cache* cache, const int32_t* slots, int64_t num_tokens, int32_t dtype, void* k, void* v,
+                      void* stream) {
+  using namespace gvrc;
+  const gvr_status s = check_cache(cache);
+  if (s != GVR_OK) return s;
+  if (num_tokens < 0 || (dtype != GVR_BF16 && dtype != GVR_F16)) return GVR_ERR_ARG;
+  if (num_tokens == 0 || (!k && !v)) return GVR_OK;
+  if (!slots) return GVR_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return GVR_ERR_ALIGN;
+  CopyParams p = {};
+  p.k = k;
+  p.v = v;
+  p.slots = slots;
+  return launch_copy(cache, p, dtype, num_tokens, false, stream);
+}
+
+const char* gvr_cache_status_string(gvr_status status) {
+  switch (status) {
+    case GVR_OK: return "ok";
+    case GVR_ERR_NULL: return "a required pointer is NULL";
+    case GVR_ERR_ALIGN: return "cache data, q, k, v and out must be 16-byte aligned, int32 and fp32 buffers 4-byte aligned";
+    case GVR_ERR_STRIDE:
+      return "a stride is out of range: page strides a multiple of 16 bytes that holds a page, q, k and v strides "
+             "multiples of 8 elements, table strides at least the table's width";
+    case GVR_ERR_ARG: return "invalid argument (head_dim 64, 128 or 256; page_size a power of two; counts, ratios, scales, heads, k or dtype)";
+    case GVR_ERR_LAUNCH: return "kernel launch failed";
+    default: return "unknown status";
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,99 @@
+// gvr_cache_common.cuh -- what the cache kernels share: the argument checks of a gvr_cache, its
+// row layout, and the conversions between 16-bit values, e2m1 codes and e4m3 scales.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "gvr_cache.h"
+#include "gvr_cache_index.h"
+
+namespace gvrc {
+
+constexpr int64_t kIntMax = 2147483647;
+constexpr int kMaxDevices = 64;
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+inline int log2_of(int32_t pow2) {
+  int s = 0;
+  while ((int32_t(1) << s) < pow2) ++s;
+  return s;
+}
+
+inline bool page_size_ok(int32_t ps) { return ps >= 1 && ps <= GVR_CACHE_MAX_PAGE_SIZE && (ps & (ps - 1)) == 0; }
+
+inline gvr_status check_cache(const gvr_cache* c) {
+  if (!c) return GVR_ERR_NULL;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return GVR_ERR_ARG;
+  if (!page_size_ok(c->page_size) || c->num_kv_heads < 1 || c->num_kv_heads > 65535 || c->reserved != 0)
+    return GVR_ERR_ARG;
+  if (c->num_pages < 0 || c->num_pages > kIntMax / c->page_size) return GVR_ERR_ARG;
+  if (!std::isfinite(c->k_scale) || !std::isfinite(c->v_scale) || !(c->k_scale > 0) || !(c->v_scale > 0))
+    return GVR_ERR_ARG;
+  if (c->page_stride % 16 != 0 ||
+      c->page_stride < int64_t(c->page_size) * c->num_kv_heads * row_bytes(c->head_dim))
+    return GVR_ERR_STRIDE;
+  // an address is page * page_stride + ... in 64 bits
+  if (c->num_pages > 0 && c->page_stride > INT64_MAX / 2 / c->num_pages) return GVR_ERR_STRIDE;
+  if (c->num_pages > 0 && !c->data) return GVR_ERR_NULL;
+  if (!aligned(c->data, 16)) return GVR_ERR_ALIGN;
+  return GVR_OK;
+}
+
+// The current device's number of SMs (looked up once per device).
+cudaError_t sm_count(int* sms);
+
+// ------------------------------------------------------------------------------- conversions
+// Four bytes of two e2m1 codes each -> four f16x2, low half from the low four bits.  Exact.
+__device__ __forceinline__ void e2m1_to_f16x2(uint32_t codes, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+}
+
+// Two e4m3 in the low 16 bits -> f16x2.  Exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+
+// Nearest e4m3 (ties to even, saturating at 448, NaN kept) in the low 8 bits.
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\tcvt.u32.u16 %0, t;\n\t}"
+      : "=r"(r)
+      : "f"(0.f), "f"(x));
+  return r;
+}
+
+// Nearest e2m1 codes (ties to even, saturating at 6) of lo and hi in one byte.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t, z;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b32 %0, {t, 0, 0, 0};\n\t}"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
+  const __half2 v = *reinterpret_cast<const __half2*>(&h);
+  return __half22float2(v);
+}
+
+}  // namespace gvrc

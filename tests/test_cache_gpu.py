@@ -1,0 +1,466 @@
+"""The 4-bit cache's operators on the GPU against the plain 64-bit implementation of cachecheck."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+import cachecheck as cc
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def gvr():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_attention_indexer_exact_gb300 import _build
+    _build.build_library()
+    import sparse_attention_indexer_exact_gb300 as mod
+    mod.load_library()
+    torch.cuda.set_device(0)
+    return mod
+
+
+def dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x)).to(dtype).to(DEV)
+
+
+def host(t):
+    return t.detach().float().cpu().numpy() if t.dtype in (torch.bfloat16, torch.float16) else t.detach().cpu().numpy()
+
+
+# ------------------------------------------------------------------------------------- tables
+def check_tables(gvr, cached, lens, free, table, max_new, ps, cr, offset=0):
+    want = cc.tables(cached, lens, free, table, max_new, ps, cr)
+    t = dev(table)
+    room = torch.full((max_new + offset + 3,), -77, dtype=torch.int32, device=DEV)
+    slots, counts = gvr.cache_tables(dev(cached), dev(lens), dev(free), t, max_new, ps, cr, slots=room[offset:offset + max_new])
+    assert np.array_equal(host(t), want[0])
+    assert np.array_equal(host(slots), want[1])
+    assert np.array_equal(host(counts), want[2])
+    r = host(room)
+    assert (r[:offset] == -77).all() and (r[offset + max_new:] == -77).all()
+
+
+@pytest.mark.parametrize("requests,ps,cr", [(1, 1, 1), (1, 64, 4), (3, 16, 1), (31, 2, 3), (64, 64, 4), (513, 16, 1), (1025, 8, 2)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_tables(gvr, requests, ps, cr, seed):
+    g = np.random.default_rng(100 * requests + seed)
+    cached = g.integers(0, 300, requests)
+    lens = cached + g.integers(0, [5, 400][seed], requests)
+    lens[g.random(requests) < 0.2] = 0  # finished requests: no growth
+    width = int(max(cached.max(), lens.max()) // cr // ps) + 2
+    need = -(-(cached // cr) // ps)
+    order = g.permutation(int(need.sum()) + requests * width)
+    table = np.full((requests, width), -1)
+    at = 0
+    for q in range(requests):
+        table[q, :need[q]] = order[at:at + need[q]]
+        at += need[q]
+    new = int(np.maximum(lens // cr - cached // cr, 0).sum())
+    for extra, offset in ((0, 0), (37, 1), (-min(new, 5), 2)):
+        check_tables(gvr, cached, lens, order[at:], table, new + extra, ps, cr, offset)
+
+
+def test_tables_borders(gvr):
+    """Empty pool, pool that ends inside a request, table too narrow, negative lengths, rollback, no
+    requests, requests that already overflow their table, unused slots."""
+    table = np.arange(12).reshape(3, 4) + 100
+    for free in ([], [7], [7, 8, 9]):
+        check_tables(gvr, [0, 5, 60], [40, 70, 64], free, table, 120, 16, 1)
+    check_tables(gvr, [-5, 8, 30], [10, -1, 7], [1, 2, 3], table, 20, 16, 1)
+    check_tables(gvr, [100, 100, 0], [140, 100, 1], [1, 2, 3], table, 50, 16, 1)  # 4 x 16 < 100
+    check_tables(gvr, [0, 0, 0], [0, 0, 0], [1], table, 0, 16, 1)
+    check_tables(gvr, [], [], [1], np.zeros((0, 4)), 9, 16, 1)
+    t = np.full((2, 4), -1)
+    t[0, 0] = 2 ** 31 - 1  # a page whose slots do not fit 31 bits: no slot
+    check_tables(gvr, [3, 0], [5, 2], [1], t, 4, 16, 1)
+
+
+def test_tables_most_requests(gvr):
+    n = gvr.MAX_CACHE_REQUESTS
+    g = np.random.default_rng(5)
+    cached, width = g.integers(0, 60, n), 9
+    lens = cached + g.integers(0, 12, n)
+    check_tables(gvr, cached, lens, np.arange(3 * n), np.full((n, width), 5), 6 * n, 8, 1)
+    with pytest.raises(gvr.GvrError):
+        check_tables(gvr, np.zeros(n + 1), np.zeros(n + 1), [1], np.zeros((n + 1, 1)), 1, 8, 1)
+
+
+def test_tables_wide_stride_keeps_what_lies_between(gvr):
+    whole = torch.full((5, 20), -9, dtype=torch.int32, device=DEV)
+    t = whole[:, 3:9]
+    gvr.cache_tables(dev([0] * 5), dev([33] * 5), dev(np.arange(50)), t, 200, 8, 1)
+    want = np.full((5, 20), -9)
+    want[:, 3:8] = np.arange(25).reshape(5, 5)
+    assert np.array_equal(host(whole), want)
+
+
+# ----------------------------------------------------------------------------- append and read
+def check_append(gvr, k, v, cache, slots, ks=1.0, vs=1.0):
+    """Appends and compares every byte of the cache; values back in both types."""
+    before = host(cache).copy()
+    flat = before.reshape(-1, *before.shape[2:]) if before.size else before
+    rows = cc.pack(host(k), host(v), ks, vs)
+    sl = host(slots)
+    ps, n = cache.shape[1], cache.shape[0] * cache.shape[1]
+    for t in range(len(sl)):
+        if 0 <= sl[t] < n:
+            flat[sl[t], :, :k.shape[2] * 9 // 8] = rows[t][:, :k.shape[2] * 9 // 8]  # the unused bytes stay
+    gvr.cache_append(k, v, cache, slots, k_scale=ks, v_scale=vs)
+    dim = k.shape[2]
+    used = dim + dim // 8
+    got = host(cache)
+    gc, wc = cc.unpack(got, dim, ks, vs), cc.unpack(flat.reshape(got.shape), dim, ks, vs)
+    for a, b in zip(gc, wc):
+        assert np.array_equal(a, b, equal_nan=True)
+    # bytes too, but for the sign of zeros (value-equal)
+    same = got[..., dim:used] == flat.reshape(got.shape)[..., dim:used]
+    assert same.all()
+    assert np.array_equal(got[..., used:], flat.reshape(got.shape)[..., used:])
+    for dt in (torch.bfloat16, torch.float16):
+        rk, rv = gvr.cache_read(cache, slots, dim, dt, k_scale=ks, v_scale=vs)
+        for r, w, f in ((rk, wc[0], ks), (rv, wc[1], vs)):
+            w = w.reshape(-1, *w.shape[2:])
+            want = np.stack([w[s] if 0 <= s < n else np.zeros(w.shape[1:]) for s in sl]) if len(sl) else np.zeros(r.shape)
+            want = torch.as_tensor(want.astype(np.float32)).to(dt).float().numpy()
+            assert np.array_equal(host(r), want, equal_nan=True)
+    assert ps > 0
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens,heads,ps", [(1, 1, 16), (5, 3, 1), (67, 2, 16), (130, 8, 64)])
+def test_append_and_read(gvr, dim, dtype, tokens, heads, ps):
+    g = torch.Generator().manual_seed(dim + tokens)
+    x = torch.randn(tokens, 2, heads, dim, generator=g) * torch.exp(2 * torch.randn(tokens, 2, heads, 1, generator=g))
+    x[0, 0, 0, 16:32] = 0
+    if tokens > 3:
+        x[1, 0, 0, :16] = torch.tensor([6, .25, .75, -1.25, 1.75, 2.5, 3.5, -5, -.25, -.75, 1.25, 5, -6, 3, -2, 0.5])  # ties
+        x[2, 1, 0, 3] = float("nan")
+        x[3, 0, 0, 5] = float("inf")
+        x[3, 1, 0, 5] = -float("inf")
+        x[3, 1, 0, 16:32] *= 1e-6 / 50  # scales that underflow
+    x = x.to(DT[dtype]).to(DEV)
+    pages = tokens // ps + 2
+    order = torch.randperm(pages * ps, generator=g)[:tokens].to(torch.int32)
+    if tokens > 3:
+        order[-1] = -1
+        order[-2] = pages * ps
+    cache = torch.randint(0, 120, (pages, ps, heads, cc.ROW_BYTES[dim]), generator=g, dtype=torch.uint8).to(DEV)
+    for ks, vs in ((1.0, 1.0), (0.25, 8.0)):
+        check_append(gvr, x[:, 0], x[:, 1], cache, order.to(DEV), ks, vs)
+
+
+def test_append_strides_and_pages_apart(gvr):
+    """K and V as slices of one projection, head-major K, pages with a gap between them."""
+    g = torch.Generator().manual_seed(9)
+    n, h, d, ps = 33, 4, 64, 8
+    qkv = torch.randn(n, 5 * h * d, generator=g).to(torch.bfloat16).to(DEV)
+    k, v = qkv[:, 3 * h * d:4 * h * d].view(n, h, d), qkv[:, 4 * h * d:].view(n, h, d)
+    slots = torch.randperm(6 * ps, generator=g)[:n].to(torch.int32).to(DEV)
+    whole = torch.full((6, 3, ps, h, 80), 7, dtype=torch.uint8, device=DEV)
+    check_append(gvr, k, v, whole[:, 1], slots)
+    assert (whole[:, 0] == 7).all() and (whole[:, 2] == 7).all()
+    hm = torch.randn(h, n, d, generator=g).to(torch.bfloat16).to(DEV).transpose(0, 1)
+    check_append(gvr, hm, v, whole[:, 2], slots)
+    check_append(gvr, hm[:1].expand(n, h, d), v, whole[:, 2], slots)  # a token stride of 0
+
+
+def test_append_nothing(gvr):
+    cache = gvr.cache_alloc(2, 16, 2, 64, DEV)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    gvr.cache_append(none, none, cache, dev([]))
+    k, v = gvr.cache_read(cache, dev([]), 64)
+    assert k.shape == v.shape == (0, 2, 64) and int(cache.sum()) == 0
+
+
+# ----------------------------------------------------------------------------------- attention
+def random_cache(g, pages, ps, heads, dim, spread=1.0):
+    kv = g.standard_normal((2, pages, ps, heads, dim)) * np.exp(spread * g.standard_normal((2, 1, 1, heads, dim)))
+    return cc.pack(kv[0].astype(np.float32), kv[1].astype(np.float32))
+
+
+def compare(out, lse, ref, cache, dim, vs=1.0):
+    v = cc.unpack(host(cache), dim, 1.0, vs)[1]
+    v_max = np.nanmax(np.abs(v)) if v.size else 0
+    tol, tol_lse = cc.attend_tolerance(ref, torch.finfo(out.dtype).eps, v_max)
+    o, l = host(out).astype(np.float64), host(lse).astype(np.float64)
+    assert np.isfinite(o).all()
+    worst = np.abs(o - ref[0]) / tol
+    assert worst.max(initial=0) <= 1, f"out: {worst.max()} of the bound at {np.unravel_index(worst.argmax(), worst.shape)}"
+    fin = np.isfinite(ref[1])
+    assert np.array_equal(l[~fin], ref[1][~fin])
+    worst = np.abs(l - ref[1])[fin] / tol_lse[fin]
+    assert worst.max(initial=0) <= 1, f"lse: {worst.max()} of the bound"
+
+
+def decode_case(gvr, seed, dim, dtype, kv_heads, group, ps, next_n, cr, lens, k, ks=1.0, vs=1.0, scale=None, qsize=1.0,
+                spoil=True, spread=0.5):
+    g = np.random.default_rng(seed)
+    lens = np.asarray(lens)
+    requests, rows = len(lens), len(lens) * next_n
+    width = max(1, -(-(int(lens.max()) // cr) // ps))
+    pages = requests * width + 2
+    cache = random_cache(g, pages, ps, kv_heads, dim, spread)
+    table = g.permutation(pages)[:requests * width].reshape(requests, width)
+    entries = cc.row_entries(lens, next_n, cr, rows, width * ps)
+    if spoil and width > 1:
+        table[0, 0], table[-1, -1] = -1, pages
+        table[requests // 2, 1] = 2 ** 31 - 1
+    idx = None
+    if k:
+        idx = np.full((rows, k), -1)
+        for r in range(rows):
+            n = entries[r]
+            m = min(n, k)
+            idx[r, :m] = g.permutation(n)[:m] if n > k else np.arange(m)
+        if spoil and k >= 4:
+            for r in range(0, rows, 2):
+                idx[r, 0], idx[r, k // 2], idx[r, k - 1] = -2, entries[r], idx[r, 1]  # failed, beyond, twice
+            if rows > 2:
+                idx[1] = -1
+    q = torch.as_tensor(g.standard_normal((rows, kv_heads * group, dim)) * qsize).to(DT[dtype]).to(DEV)
+    out, lse = gvr.attend_decode(q, dev(cache, torch.uint8), dev(table), dev(lens), next_n, cr,
+                                 None if idx is None else dev(idx), scale=scale, k_scale=ks, v_scale=vs, want_lse=True)
+    s = 1 / math.sqrt(dim) if scale is None else scale
+    ref = cc.attend(host(q), cache, table, entries, [r // next_n for r in range(rows)], idx, s, ks, vs)
+    compare(out, lse, ref, torch.as_tensor(cache), dim, vs)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,kv_heads,dtype", [(1, 1, "bf16"), (4, 3, "f16"), (8, 2, "bf16"), (9, 1, "f16"), (40, 1, "bf16")])
+@pytest.mark.parametrize("k", [1, 31, 33, 512])
+def test_decode_selected(gvr, dim, group, kv_heads, dtype, k):
+    decode_case(gvr, dim + group + k, dim, dtype, kv_heads, group, 16, 2, 1, [700, 40, 33, 1, 513], k)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,kv_heads,next_n,dtype", [(1, 2, 1, "bf16"), (3, 2, 2, "f16"), (8, 1, 1, "f16"), (5, 1, 4, "bf16"),
+                                                         (16, 1, 3, "f16")])
+@pytest.mark.parametrize("ps,cr", [(16, 1), (4, 3), (1, 1)])
+def test_decode_whole(gvr, dim, group, kv_heads, next_n, dtype, ps, cr):
+    decode_case(gvr, dim + group + ps, dim, dtype, kv_heads, group, ps, next_n, cr, [cr * 161, 0, cr * 31 + next_n, 5, cr * 64], 0)
+
+
+@pytest.mark.parametrize("k", [0, 2048])
+@pytest.mark.parametrize("requests,length", [(1, 5000), (9, 2500), (300, 40)])
+def test_decode_splits(gvr, k, requests, length):
+    """One item over a whole cluster, several clusters, more items than the device holds."""
+    g = np.random.default_rng(requests)
+    lens = g.integers(max(1, length // 2), length + 1, requests)
+    decode_case(gvr, requests + k, 128, "bf16", 2, 4, 64, 1, 1, lens, k)
+
+
+@pytest.mark.parametrize("qsize,scale,ks,vs", [(1e-4, None, 1.0, 1.0), (300.0, 1e-3, 1.0, 0.25), (3.0, -0.2, 4.0, 3.0),
+                                               (1.0, 0.0, 1.0, 1.0), (8.0, None, 1.0, 1.0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_decode_scales(gvr, qsize, scale, ks, vs, dtype):
+    """Tiny and large queries, negative and zero factors, peaked and flat rows, cache factors."""
+    decode_case(gvr, 77, 128, dtype, 2, 4, 16, 1, 1, [300, 90], 64, ks, vs, scale, qsize)
+    decode_case(gvr, 78, 64, dtype, 2, 4, 16, 2, 1, [300, 90], 0, ks, vs, scale, qsize)
+
+
+def test_decode_query_range_of_bf16(gvr):
+    """bf16 queries far outside f16's range: 2^100 with a scale that brings the scores back."""
+    decode_case(gvr, 5, 128, "bf16", 1, 4, 16, 1, 1, [200], 64, 1.0, 1.0, 2.0 ** -102, 2.0 ** 100)
+    decode_case(gvr, 6, 128, "bf16", 1, 4, 16, 1, 1, [200], 64, 1.0, 1.0, 2.0 ** 88, 2.0 ** -90)
+
+
+def test_decode_growing_scores(gvr):
+    """Scores that climb along the row, so that the running maximum grows at every step."""
+    g = np.random.default_rng(3)
+    n, d = 640, 64
+    base = g.standard_normal(d)
+    k = base * np.linspace(0, 12, n)[:, None] + 0.3 * g.standard_normal((n, d))
+    cache = cc.pack(k.astype(np.float32)[:, None], g.standard_normal((n, 1, d)).astype(np.float32)).reshape(40, 16, 1, 80)
+    table = np.arange(40)[None]
+    q = torch.as_tensor(np.stack([base, -base, 0.1 * base, 0 * base])[None]).to(torch.bfloat16).to(DEV)
+    out, lse = gvr.attend_decode(q, dev(cache, torch.uint8), dev(table), dev([n]), 1, 1, want_lse=True)
+    compare(out, lse, cc.attend(host(q), cache, table, [n], [0], None, 1 / 8), torch.as_tensor(cache), d)
+
+
+def test_decode_idle_and_strided(gvr):
+    """q as a slice of a projection, pages that lie apart, given outputs, requests without entries,
+    a batch of only such requests."""
+    g = np.random.default_rng(8)
+    cache = random_cache(g, 12, 16, 2, 128)
+    whole = torch.full((12, 2, 16, 2, 144), 255, dtype=torch.uint8, device=DEV)
+    whole[:, 1] = dev(cache, torch.uint8)
+    x = torch.as_tensor(g.standard_normal((3, 12, 128))).to(torch.float16).to(DEV)
+    q = x[:, 2:10]
+    lens = np.array([50, 0, 90])
+    table = torch.full((3, 11), -3, dtype=torch.int32, device=DEV)
+    table[:, 2:8] = dev(g.permutation(12)[:6])
+    t = table[:, 2:8]
+    out = torch.full((3, 8, 128), 7, dtype=torch.float16, device=DEV)
+    lse = torch.zeros(3, 8, device=DEV)
+    got = gvr.attend_decode(q, whole[:, 1], t, dev(lens), 1, 1, out=out, lse=lse)
+    assert got[0] is out and got[1] is lse
+    ref = cc.attend(host(q), cache, host(t), lens, [0, 1, 2], None, 1 / math.sqrt(128))
+    compare(out, lse, ref, torch.as_tensor(cache), 128)
+    assert (host(out)[1] == 0).all() and (host(lse)[1] == -np.inf).all()
+    out, lse = gvr.attend_decode(q, whole[:, 1], t, dev([0, -4, 0]), 1, 1, want_lse=True)
+    assert (host(out) == 0).all() and (host(lse) == -np.inf).all()
+    out, _ = gvr.attend_decode(q[:0], whole[:, 1], t, dev(lens), 1, 1)
+    assert out.shape == (0, 8, 128)
+    empty = torch.empty(0, 16, 2, 144, dtype=torch.uint8, device=DEV)  # a cache without pages
+    out, lse = gvr.attend_decode(q, empty, t, dev(lens), 1, 1, want_lse=True)
+    assert (host(out) == 0).all() and (host(lse) == -np.inf).all()
+
+
+def test_decode_masked_nan_stays_out(gvr):
+    """NaN scales and codes at their largest in entries that a row does not see leave it untouched;
+    in an entry that it sees they make that KV head NaN."""
+    g = np.random.default_rng(4)
+    cache = random_cache(g, 8, 16, 2, 64)
+    lens, table = np.array([70]), np.arange(8)[None]
+    clean = cache.copy()
+    cache[70 // 16, 70 % 16:] = 0xff
+    cache[70 // 16 + 1:] = 0x7f
+    q = torch.as_tensor(g.standard_normal((1, 4, 64))).to(torch.bfloat16).to(DEV)
+    idx = np.full((1, 100), -1)
+    idx[0, :70] = g.permutation(70)
+    idx[0, 70:80] = np.arange(70, 80)
+    for i in (None, idx):
+        out, lse = gvr.attend_decode(q, dev(cache, torch.uint8), dev(table), dev(lens), 1, 1, None if i is None else dev(i), want_lse=True)
+        ref = cc.attend(host(q), clean, table, lens, [0], i, 1 / 8)
+        compare(out, lse, ref, torch.as_tensor(clean), 64)
+    cache[0, 3, 1, 64] = 0x7f  # K scale of entry 3, KV head 1
+    out, lse = gvr.attend_decode(q, dev(cache, torch.uint8), dev(table), dev(lens), 1, 1, want_lse=True)
+    assert np.isfinite(host(out)[0, :2]).all() and np.isnan(host(out)[0, 2:]).all() and np.isnan(host(lse)[0, 2:]).all()
+
+
+@pytest.mark.parametrize("dim,dtype,group,kv_heads,k", [(64, "f16", 8, 2, 40), (128, "bf16", 8, 1, 512), (256, "bf16", 3, 2, 100)])
+def test_prefill_selected(gvr, dim, dtype, group, kv_heads, k):
+    g = np.random.default_rng(dim)
+    lengths, ps = [37, 300, 64], 16
+    start = np.array([0, 37, 337])
+    req = np.concatenate([np.full(n, i) for i, n in enumerate(lengths)])[::7]
+    pos = np.concatenate([np.arange(n) for n in lengths])[::7]
+    starts, ends = start[req], start[req] + pos + 1
+    req, starts, ends = (np.append(x, y) for x, y in ((req, [-1, 3, 1, 0]), (starts, [0, 0, 50, -9]), (ends, [9, 9, 50, 20])))
+    width = 19
+    cache = random_cache(g, 3 * width, ps, kv_heads, dim)
+    table = g.permutation(3 * width).reshape(3, width)
+    rows = len(req)
+    n = [min(max(int(e) - max(int(s), 0), 0), width * ps) for s, e in zip(starts, ends)]
+    idx = np.full((rows, k), -1)
+    for r in range(rows):
+        m = min(n[r], k)
+        idx[r, :m] = g.permutation(n[r])[:m] if n[r] > k else np.arange(m)
+    q = torch.as_tensor(g.standard_normal((rows, kv_heads * group, dim))).to(DT[dtype]).to(DEV)
+    out, lse = gvr.attend_prefill(q, dev(cache, torch.uint8), dev(table), dev(req), dev(starts), dev(ends), dev(idx), want_lse=True)
+    ref = cc.attend(host(q), cache, table, n, req, idx, 1 / math.sqrt(dim))
+    compare(out, lse, ref, torch.as_tensor(cache), dim)
+
+
+def test_same_result_every_time(gvr):
+    """No atomics, a fixed order of sums: the same bits again, alone or beside other calls."""
+    g = np.random.default_rng(1)
+    cache, table = dev(random_cache(g, 64, 16, 2, 128), torch.uint8), dev(g.permutation(64).reshape(2, 32))
+    q = torch.as_tensor(g.standard_normal((2, 8, 128))).to(torch.bfloat16).to(DEV)
+    lens = dev([500, 300])
+    first = [host(x) for x in gvr.attend_decode(q, cache, table, lens, 1, 1, want_lse=True)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 3]):
+            got.append(gvr.attend_decode(q, cache, table, lens, 1, 1, want_lse=True))
+    torch.cuda.synchronize()
+    for out, lse in got:
+        assert np.array_equal(host(out), first[0]) and np.array_equal(host(lse), first[1])
+
+
+# ----------------------------------------------------------------------------- a step together
+def step_inputs(g, gvr, lens, next_n, heads, kv_heads, dim, ps, stride):
+    rows = len(lens) * next_n
+    return dict(k=torch.as_tensor(g.standard_normal((rows, kv_heads, dim))).to(torch.bfloat16).to(DEV),
+                v=torch.as_tensor(g.standard_normal((rows, kv_heads, dim))).to(torch.bfloat16).to(DEV),
+                q=torch.as_tensor(g.standard_normal((rows, heads, dim))).to(torch.bfloat16).to(DEV),
+                logits=torch.as_tensor(g.standard_normal((rows, stride))).to(torch.float32).to(DEV))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_decode_steps_together(gvr, captured):
+    """Prompts written, then decode steps: tables, append, top-K, attention over the selection and over
+    everything, eagerly or as one captured graph replayed while the lengths grow."""
+    g = np.random.default_rng(12)
+    heads, kv_heads, dim, ps, next_n, k, stride = 8, 2, 64, 16, 2, 512, 1024
+    lens = np.array([600, 40, 701, 5])
+    n, width, pages = len(lens), 60, 200
+    cache = gvr.cache_alloc(pages, ps, kv_heads, dim, DEV)
+    table = torch.full((n, width), -1, dtype=torch.int32, device=DEV)
+    free = dev(g.permutation(pages))
+    # the prompts
+    total = int(lens.sum())
+    kv = torch.as_tensor(g.standard_normal((2, total, kv_heads, dim))).to(torch.bfloat16).to(DEV)
+    slots, counts = gvr.cache_tables(dev([0] * n), dev(lens), free, table, total + 9, ps)
+    gvr.cache_append(kv[0], kv[1], cache, slots)
+    used = int(counts[1])
+    assert counts.tolist() == [total, int((-(-lens // ps)).sum()), 0]
+    # mirror on the host
+    mirror = [cc.pack(host(kv[0][a:a + m]), host(kv[1][a:a + m])) for a, m in zip(np.cumsum(lens) - lens, lens)]
+    cached, now = dev(lens), dev(lens + next_n)
+    buf = step_inputs(g, gvr, lens, next_n, heads, kv_heads, dim, ps, stride)
+    pool = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+
+    def step():
+        slots, counts = gvr.cache_tables(cached, now, pool, table, n * next_n, ps)
+        gvr.cache_append(buf["k"], buf["v"], cache, slots)
+        idx, _ = gvr.topk_decode(buf["logits"], now, next_n, 1, k)
+        sel = gvr.attend_decode(buf["q"], cache, table, now, next_n, 1, idx, want_lse=True)
+        return slots, counts, idx, sel, gvr.attend_decode(buf["q"], cache, table, now, next_n, 1, want_lse=True)
+
+    graph = None
+    for i in range(4):
+        new = step_inputs(g, gvr, lens, next_n, heads, kv_heads, dim, ps, stride)
+        for name in buf:
+            buf[name].copy_(new[name])
+        cached.copy_(dev(lens))
+        lens = lens + next_n
+        now.copy_(dev(lens))
+        pool.copy_(free[used:used + n])
+        if captured and graph is None:
+            warm = torch.cuda.Stream()
+            warm.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(warm):
+                gvr.topk_decode(buf["logits"], now, next_n, 1, k)
+            torch.cuda.current_stream().wait_stream(warm)
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got = step()
+        if captured:
+            graph.replay()
+        else:
+            got = step()
+        torch.cuda.synchronize()
+        slots, counts, idx, sel, every = got
+        used += int(counts[1])
+        assert int(counts[0]) == n * next_n and int(counts[2]) == 0
+        for q in range(n):
+            rows = slice(q * next_n, (q + 1) * next_n)
+            mirror[q] = np.concatenate([mirror[q], cc.pack(host(buf["k"][rows]), host(buf["v"][rows]))])
+        # the plain form over the mirror: one request after the other as its own pages
+        flat = np.concatenate(mirror)
+        base = np.cumsum([len(m) for m in mirror]) - [len(m) for m in mirror]
+        rows = n * next_n
+        entries = cc.row_entries(lens, next_n, 1, rows, width * ps)
+        for chosen, (out, lse) in ((host(idx), sel), (None, every)):
+            parts = []
+            for q in range(n):
+                one = mirror[q][:, None]  # pages of one entry
+                r = slice(q * next_n, (q + 1) * next_n)
+                parts.append(cc.attend(host(buf["q"][r]), one, np.arange(len(one))[None], entries[r], [0] * next_n,
+                                       None if chosen is None else chosen[r], 1 / 8))
+            ref = [np.concatenate(x) for x in zip(*parts)]
+            compare(out, lse, ref, torch.as_tensor(flat[:, None]), dim)
+        assert base[0] == 0
