@@ -33,9 +33,9 @@
  *
  * Conventions.  As in gvr_topk.h: all pointers but the gvr_cache itself are device pointers to
  * memory that the caller owns; every call checks its arguments on the host, allocates nothing,
- * needs no workspace, reads no device memory on the host, does not synchronise, and enqueues ONE
- * kernel on `stream` of the current device, so it can be captured in a graph; calls share no
- * state, on any streams.  Counts of 0 are no-ops that return GVR_OK.  Statuses are those of
+ * reads no device memory on the host, does not synchronise, and enqueues one kernel (attention
+ * with a workspace: one or two) on `stream` of the current device, so it can be captured in a
+ * graph; calls share no state, on any streams.  Counts of 0 are no-ops that return GVR_OK.  Statuses are those of
  * gvr_topk.h; gvr_cache_status_string says what each means here.
  */
 #ifndef GVR_CACHE_H
@@ -52,6 +52,7 @@ enum { GVR_BF16 = 0, GVR_F16 = 1 };
 
 #define GVR_CACHE_MAX_REQUESTS 8192   /* cache_tables */
 #define GVR_CACHE_MAX_PAGE_SIZE 4096
+#define GVR_ATTEND_WORKSPACE (1 << 20) /* bytes */
 
 typedef struct gvr_cache {
   void* data;           /* device, 16-byte aligned */
@@ -126,6 +127,12 @@ gvr_status cache_read(const gvr_cache* cache, const int32_t* slots, int64_t num_
  *           row's entries times V.  A row without entries gets zeros.
  *   lse     optional fp32 [num_rows][num_heads]: log of the sum of exp(scale * q . k); -infinity
  *           for a row without entries.  (Merges this with attention over other entries.)
+ *   workspace  optional device memory, 16-byte aligned, of any content and size: rows of very many
+ *           entries in a small batch are then split over more of the device, as far as
+ *           workspace_bytes goes (GVR_ATTEND_WORKSPACE is always enough).  Its content is not kept:
+ *           calls that can overlap on the GPU, or graphs whose replays can, need one each.
+ * Every wait for the kernel's own copies is bounded (0.5 s).  If one gives up -- not expected on a
+ * healthy GPU -- the outputs of the query heads concerned are NaN.
  * Scores, softmax and sums are fp32; K and V values are exact; probabilities are rounded to
  * 11-bit significands before they multiply V.
  */
@@ -134,7 +141,7 @@ gvr_status attend_decode(const gvr_cache* cache, const void* q, int64_t q_row_st
                          const int32_t* block_table, int64_t table_stride, int64_t table_width,
                          const int32_t* kv_lens, int32_t next_n, int32_t compress_ratio,
                          const int32_t* indices, int64_t k, float scale, void* out, float* lse,
-                         void* stream);
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Attention of prefill rows over their selection.  Row r belongs to request row_requests[r] and
@@ -150,7 +157,7 @@ gvr_status attend_prefill(const gvr_cache* cache, const void* q, int64_t q_row_s
                           int64_t num_requests, const int32_t* row_requests,
                           const int32_t* row_starts, const int32_t* row_ends,
                           const int32_t* indices, int64_t k, float scale, void* out, float* lse,
-                          void* stream);
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static English text for a status returned by the functions of this header; never NULL. */
 const char* gvr_cache_status_string(gvr_status status);

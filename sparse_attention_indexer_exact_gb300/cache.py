@@ -1,8 +1,9 @@
 """The 4-bit paged cache and the attention that reads it at the selected entries.
 
 Bindings of ``include/gvr_cache.h``, in the manner of the package's top-K calls: tensors are
-checked and turned into addresses here, everything else happens in one kernel per call on the
-current stream (or on ``stream``) of the tensors' device.  A decode step, in call order::
+checked and turned into addresses here, everything else happens in one kernel per call (two for few
+rows of very many entries) on the current stream of the tensors' device, or on the one given as
+``stream=`` to any of the calls.  A decode step, in call order::
 
     slots, counts = cache_tables(cached_lens, kv_lens, free_pages, block_table, new, page_size, cr)
     cache_append(k, v, cache, slots)                       # cache = cache_alloc(pages, page_size, heads, dim)
@@ -15,6 +16,7 @@ layout of a row, the quantiser and what every call does at its borders.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 __all__ = ["cache_alloc", "cache_row_bytes", "cache_tables", "cache_append", "cache_read", "attend_decode",
@@ -43,17 +45,27 @@ def _declare(lib):
     lib.cache_tables.argtypes = [p, p, i64, i32, i32, p, i64, p, i64, i64, p, i64, p, p]
     lib.cache_append.argtypes = [cache, p, i64, i64, p, i64, i64, i32, p, i64, p]
     lib.cache_read.argtypes = [cache, p, i64, i32, p, p, p]
-    lib.attend_decode.argtypes = [cache, p, i64, i64, i32, i64, i32, p, i64, i64, p, i32, i32, p, i64, f32, p, p, p]
-    lib.attend_prefill.argtypes = [cache, p, i64, i64, i32, i64, i32, p, i64, i64, i64, p, p, p, p, i64, f32, p, p, p]
+    sz = ctypes.c_size_t
+    lib.attend_decode.argtypes = [cache, p, i64, i64, i32, i64, i32, p, i64, i64, p, i32, i32, p, i64, f32, p, p, p, sz, p]
+    lib.attend_prefill.argtypes = [cache, p, i64, i64, i32, i64, i32, p, i64, i64, i64, p, p, p, p, i64, f32, p, p, p, sz, p]
     for name in EXPORTED_SYMBOLS[:-1]:
         getattr(lib, name).restype = ctypes.c_int
     lib.gvr_cache_status_string.argtypes = [ctypes.c_int]
     lib.gvr_cache_status_string.restype = ctypes.c_char_p
 
 
-def _lib():
-    from . import load_library
-    return load_library()
+_WORKSPACE = 1 << 20  # GVR_ATTEND_WORKSPACE
+_LONG = 8192  # selections over this many entries a row get a workspace, as whole caches do
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        from . import load_library
+        _lib = load_library()
+    return _lib
 
 
 def _check(lib, status: int):
@@ -62,41 +74,63 @@ def _check(lib, status: int):
         raise GvrError(status, lib.gvr_cache_status_string(status).decode())
 
 
-def _on_device(lib, device, stream, call, *args):
-    """``call(*args, stream)`` with the tensors' device current."""
+def _launch(device: int, call, *args):
+    """``call(*args, stream)`` on the current stream of the tensors' device, with that device current."""
     import torch
-    from . import _stream_handle
-    if device.index == torch.cuda.current_device():
-        _check(lib, call(*args, _stream_handle(stream, device)))
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if device == torch._C._cuda_getDevice():
+        status = call(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(lib, call(*args, _stream_handle(stream, device)))
+            status = call(*args, stream)
+    if status != 0:
+        _check(_library(), status)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}: all tensors must share one device")
+def _on_stream(call):
+    """``call`` with a ``stream`` argument: a torch stream or a handle, made current around the call, so
+    that what the call allocates belongs to the stream that uses it."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        import torch
+        if not isinstance(stream, torch.cuda.Stream):
+            device = next((a.device for a in args if isinstance(a, torch.Tensor)), None)
+            stream = torch.cuda.ExternalStream(stream, device)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return wrapped
 
 
-def _cuda(t, name):
+# The checks of one tensor: its device's number, or an error that names it.
+def _device(t, name) -> int:
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    return t
+    return t.get_device()
 
 
-def _int32(t, name, least=0):
+def _on(t, device: int, name):
+    if _device(t, name) != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}: all tensors must share one device")
+
+
+def _int32(t, device: int, name, least=0) -> int:
+    """Address of a contiguous 1-D int32 tensor of at least ``least`` entries."""
     import torch
-    if _cuda(t, name).dtype != torch.int32:
+    _on(t, device, name)
+    if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
-    if t.dim() != 1 or t.shape[0] < least or (t.shape[0] > 1 and t.stride(0) != 1):
+    shape = t.shape
+    if len(shape) != 1 or shape[0] < least or (shape[0] > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be 1-D contiguous with at least {least} entries")
+    return t.data_ptr()
 
 
-def _dtype(t, name):
+def _dtype(t, name) -> int:
     import torch
-    if _cuda(t, name).dtype == torch.bfloat16:
+    if t.dtype == torch.bfloat16:
         return 0
     if t.dtype == torch.float16:
         return 1
@@ -105,35 +139,44 @@ def _dtype(t, name):
 
 def _heads_3d(t, name, dim):
     """(row stride, head stride) of [rows, heads, dim] with unit inner stride."""
-    if t.dim() != 3 or t.shape[2] != dim:
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"{name} must be [rows, heads, {dim}]")
-    rows, head, inner = t.stride()
     if t.numel() == 0:
         return 0, 0
+    row, head, inner = t.stride()
     if inner != 1:
         raise ValueError(f"{name} must have unit inner stride")
     # a dimension of one element is never stepped over
-    return (rows if t.shape[0] > 1 else 0), (head if t.shape[1] > 1 else 0)
+    return (row if shape[0] > 1 else 0), (head if shape[1] > 1 else 0)
 
 
-def _table_2d(t, requests):
+def _table_2d(t, device: int, requests):
     """(address, stride, width) of an int32 block table [>= requests, width]."""
     import torch
-    if _cuda(t, "block_table").dtype != torch.int32:
+    _on(t, device, "block_table")
+    if t.dtype != torch.int32:
         raise TypeError("block_table must be int32")
-    if t.dim() != 2 or t.shape[0] < requests or (t.shape[0] > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < requests:
         raise ValueError(f"block_table must be [>= {requests}, pages] with unit inner stride")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1]), t.shape[1]
+    width = shape[1]
+    row, inner = t.stride()
+    if shape[0] > 0 and width > 1 and inner != 1:
+        raise ValueError(f"block_table must be [>= {requests}, pages] with unit inner stride")
+    return t.data_ptr(), (row if shape[0] > 1 else width), width
 
 
 def _cache_struct(cache, k_scale, v_scale):
     import torch
-    if _cuda(cache, "cache").dtype != torch.uint8:
+    _device(cache, "cache")
+    if cache.dtype != torch.uint8:
         raise TypeError("cache must be uint8")
-    dim = _HEAD_DIM.get(cache.shape[3]) if cache.dim() == 4 else None
+    shape = cache.shape
+    dim = _HEAD_DIM.get(shape[3]) if len(shape) == 4 else None
     if dim is None:
         raise ValueError("cache must be [pages, page_size, kv_heads, row] with row 80, 144 or 288 (cache_alloc)")
-    pages, size, heads, row = cache.shape
+    pages, size, heads, row = shape
     page, entry, head, inner = cache.stride()
     if pages and (inner != 1 or (heads > 1 and head != row) or (size > 1 and entry != heads * row)):
         raise ValueError("the rows of a page of the cache must be packed; only its pages may lie apart")
@@ -142,7 +185,7 @@ def _cache_struct(cache, k_scale, v_scale):
 
 def cache_row_bytes(head_dim: int) -> int:
     """Bytes of one entry of one KV head: K and V codes and scales of ``head_dim`` values."""
-    lib = _lib()
+    lib = _library()
     out = ctypes.c_int32(0)
     _check(lib, lib.cache_row_bytes(head_dim, ctypes.byref(out)))
     return out.value
@@ -154,8 +197,9 @@ def cache_alloc(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int
     return torch.zeros((num_pages, page_size, num_kv_heads, cache_row_bytes(head_dim)), dtype=torch.uint8, device=device)
 
 
+@_on_stream
 def cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new: int, page_size: int, compress_ratio: int = 1,
-                 slots=None, counts=None, *, stream=None):
+                 slots=None, counts=None):
     """Give each request the pages that its new entries need, and map those entries to slots.
 
     ``cached_lens`` and ``kv_lens`` (int32 [requests]) are each request's uncompressed length before
@@ -165,61 +209,62 @@ def cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new: int, pa
     taken, pages missing).
     """
     import torch
-    requests = _cuda(kv_lens, "kv_lens").shape[0] if kv_lens.dim() == 1 else -1
-    _int32(kv_lens, "kv_lens")
-    _int32(cached_lens, "cached_lens", requests)
-    _int32(free_pages, "free_pages")
-    table, table_stride, width = _table_2d(block_table, requests)
-    device = kv_lens.device
+    device = _device(kv_lens, "kv_lens")
+    requests = kv_lens.shape[0] if kv_lens.dim() == 1 else 0
+    lens = _int32(kv_lens, device, "kv_lens")
+    cached = _int32(cached_lens, device, "cached_lens", requests)
+    free = _int32(free_pages, device, "free_pages")
+    table, table_stride, width = _table_2d(block_table, device, requests)
     if slots is None:
-        slots = torch.empty(max_new, dtype=torch.int32, device=device)
+        slots = torch.empty(max_new, dtype=torch.int32, device=kv_lens.device)
+        to = slots.data_ptr()
     else:
-        _int32(slots, "slots", max_new)
+        to = _int32(slots, device, "slots", max_new)
     if counts is None:
-        counts = torch.empty(3, dtype=torch.int32, device=device)
+        counts = torch.empty(3, dtype=torch.int32, device=kv_lens.device)
+        sums = counts.data_ptr()
     else:
-        _int32(counts, "counts", 3)
-    _same_device(device, cached_lens=cached_lens, free_pages=free_pages, block_table=block_table, slots=slots, counts=counts)
-    lib = _lib()
-    _on_device(lib, device, stream, lib.cache_tables, cached_lens.data_ptr(), kv_lens.data_ptr(), requests, compress_ratio,
-               page_size, free_pages.data_ptr(), free_pages.shape[0], table, table_stride, width, slots.data_ptr(), max_new,
-               counts.data_ptr())
+        sums = _int32(counts, device, "counts", 3)
+    _launch(device, _library().cache_tables, cached, lens, requests, compress_ratio, page_size, free,
+            free_pages.shape[0], table, table_stride, width, to, max_new, sums)
     return slots, counts
 
 
-def cache_append(k, v, cache, slots, *, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+@_on_stream
+def cache_append(k, v, cache, slots, *, k_scale: float = 1.0, v_scale: float = 1.0) -> None:
     """Quantise ``k`` and ``v`` [tokens, kv_heads, head_dim] (bfloat16 or float16, strides in multiples
     of 8) into ``cache`` at ``slots`` (int32 [tokens]; -1 skips the token)."""
     c = _cache_struct(cache, k_scale, v_scale)
+    device = cache.get_device()
+    _on(k, device, "k")
+    _on(v, device, "v")
     kind = _dtype(k, "k")
-    if _dtype(v, "v") != kind or v.shape != k.shape:
+    if v.dtype != k.dtype or v.shape != k.shape:
         raise ValueError("k and v must have one shape and dtype")
     k_token, k_head = _heads_3d(k, "k", c.head_dim)
     v_token, v_head = _heads_3d(v, "v", c.head_dim)
-    if k.shape[1] != c.num_kv_heads:
-        raise ValueError(f"k has {k.shape[1]} heads, the cache {c.num_kv_heads}")
-    _int32(slots, "slots", k.shape[0])
-    _same_device(cache.device, k=k, v=v, slots=slots)
-    lib = _lib()
-    _on_device(lib, cache.device, stream, lib.cache_append, ctypes.byref(c), k.data_ptr(), k_token, k_head, v.data_ptr(),
-               v_token, v_head, kind, slots.data_ptr(), k.shape[0])
+    tokens, heads, _ = k.shape
+    if heads != c.num_kv_heads:
+        raise ValueError(f"k has {heads} heads, the cache {c.num_kv_heads}")
+    at = _int32(slots, device, "slots", tokens)
+    _launch(device, _library().cache_append, c, k.data_ptr(), k_token, k_head, v.data_ptr(), v_token, v_head, kind,
+            at, tokens)
 
 
-def cache_read(cache, slots, head_dim: int, dtype=None, *, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
+@_on_stream
+def cache_read(cache, slots, head_dim: int, dtype=None, *, k_scale: float = 1.0, v_scale: float = 1.0):
     """The values held at ``slots`` (int32 [n]): K and V, each [n, kv_heads, head_dim] of ``dtype``
     (bfloat16 by default, or float16); zeros for a slot that names no entry."""
     import torch
     c = _cache_struct(cache, k_scale, v_scale)
+    device = cache.get_device()
     if c.head_dim != head_dim:
         raise ValueError(f"the cache holds heads of {c.head_dim}, not {head_dim}")
-    _int32(slots, "slots")
-    _same_device(cache.device, slots=slots)
+    at = _int32(slots, device, "slots")
     n = slots.shape[0]
-    k = torch.empty((n, c.num_kv_heads, head_dim), dtype=dtype or torch.bfloat16, device=cache.device)
-    v = torch.empty_like(k)
-    kind = _dtype(k, "dtype")
-    lib = _lib()
-    _on_device(lib, cache.device, stream, lib.cache_read, ctypes.byref(c), slots.data_ptr(), n, kind, k.data_ptr(), v.data_ptr())
+    kv = torch.empty((2, n, c.num_kv_heads, head_dim), dtype=dtype or torch.bfloat16, device=cache.device)
+    k, v = kv.unbind(0)
+    _launch(device, _library().cache_read, c, at, n, _dtype(kv, "dtype"), k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -227,6 +272,8 @@ def _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse):
     """What both attention calls check: the arguments up to the block table, and the outputs."""
     import torch
     c = _cache_struct(cache, k_scale, v_scale)
+    device = cache.get_device()
+    _on(q, device, "q")
     kind = _dtype(q, "q")
     row, head = _heads_3d(q, "q", c.head_dim)
     rows, heads, dim = q.shape
@@ -234,29 +281,42 @@ def _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse):
         raise ValueError(f"q has {heads} heads, no multiple of the cache's {c.num_kv_heads}")
     if out is None:
         out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)}")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({rows}, {heads})")
+    else:
+        _on(out, device, "out")
+        if out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)}")
+    if lse is not None:
+        _on(lse, device, "lse")
+        if lse.dtype != torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape ({rows}, {heads})")
+    elif want_lse:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
     if scale is None:
         scale = 1.0 / math.sqrt(dim)
-    return (ctypes.byref(c), q.data_ptr(), row, head, kind, rows, heads), scale, out, lse
+    return device, (c, q.data_ptr(), row, head, kind, rows, heads), scale, out, lse
 
 
-def _indices_2d(indices, rows):
+def _workspace(device):
+    """Scratch of one call: from torch's allocator, so each call on each stream has its own, and a
+    captured graph keeps its own."""
     import torch
-    if _cuda(indices, "indices").dtype != torch.int32:
+    return torch.empty(_WORKSPACE, dtype=torch.uint8, device=device)
+
+
+def _indices_2d(t, device: int, rows):
+    import torch
+    _on(t, device, "indices")
+    if t.dtype != torch.int32:
         raise TypeError("indices must be int32")
-    if indices.dim() != 2 or indices.shape[0] != rows or indices.shape[1] < 1 or not indices.is_contiguous():
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < 1 or not t.is_contiguous():
         raise ValueError(f"indices must be contiguous [{rows}, >= 1]")
-    return indices.data_ptr(), indices.shape[1]
+    return t.data_ptr(), shape[1]
 
 
+@_on_stream
 def attend_decode(q, cache, block_table, kv_lens, next_n: int, compress_ratio: int, indices=None, *, scale=None,
-                  k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False, stream=None):
+                  k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False):
     """Attention of decode rows over the 4-bit cache; returns (out, lse or None).
 
     ``q`` is [rows, heads, head_dim] (bfloat16 or float16, strides in multiples of 8); row r belongs to
@@ -265,37 +325,37 @@ def attend_decode(q, cache, block_table, kv_lens, next_n: int, compress_ratio: i
     ``topk_decode`` returns them) lists, or all where it is None.  ``scale`` defaults to
     1 / sqrt(head_dim).  ``lse`` (fp32 [rows, heads]) is the log of each row's sum of exponentials.
     """
-    head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
-    rows = q.shape[0]
+    device, head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
+    rows = head[5]
     requests = (rows + next_n - 1) // max(next_n, 1)
-    table, table_stride, width = _table_2d(block_table, requests)
-    _int32(kv_lens, "kv_lens", requests)
-    listed, k = _indices_2d(indices, rows) if indices is not None else (None, 0)
-    _same_device(q.device, cache=cache, block_table=block_table, kv_lens=kv_lens, indices=indices, out=out, lse=lse)
-    lib = _lib()
-    _on_device(lib, q.device, stream, lib.attend_decode, *head, table, table_stride, width, kv_lens.data_ptr(), next_n,
-               compress_ratio, listed, k, scale, out.data_ptr(), None if lse is None else lse.data_ptr())
+    table, table_stride, width = _table_2d(block_table, device, requests)
+    lens = _int32(kv_lens, device, "kv_lens", requests)
+    listed, k = (None, 0) if indices is None else _indices_2d(indices, device, rows)
+    space = _workspace(q.device) if k == 0 or k > _LONG else None
+    _launch(device, _library().attend_decode, *head, table, table_stride, width, lens, next_n, compress_ratio,
+            listed, k, scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+            None if space is None else space.data_ptr(), _WORKSPACE)
     return out, lse
 
 
+@_on_stream
 def attend_prefill(q, cache, block_table, row_requests, row_starts, row_ends, indices, *, scale=None,
-                   k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False, stream=None):
+                   k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False):
     """Attention of prefill rows over their selection in the 4-bit cache; returns (out, lse or None).
 
     Row r belongs to request ``row_requests[r]`` (int32; outside the block table: no entries) and sees
     its first ``row_ends[r] - row_starts[r]`` entries, the window given to ``topk_prefill``, whose
     ``indices`` (int32 [rows, k]) it attends to.  The rest is as in :func:`attend_decode`.
     """
-    head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
-    rows = q.shape[0]
-    table, table_stride, width = _table_2d(block_table, 0)
-    for t, name in ((row_requests, "row_requests"), (row_starts, "row_starts"), (row_ends, "row_ends")):
-        _int32(t, name, rows)
-    listed, k = _indices_2d(indices, rows)
-    _same_device(q.device, cache=cache, block_table=block_table, row_requests=row_requests, row_starts=row_starts,
-                 row_ends=row_ends, indices=indices, out=out, lse=lse)
-    lib = _lib()
-    _on_device(lib, q.device, stream, lib.attend_prefill, *head, table, table_stride, width, block_table.shape[0],
-               row_requests.data_ptr(), row_starts.data_ptr(), row_ends.data_ptr(), listed, k, scale, out.data_ptr(),
-               None if lse is None else lse.data_ptr())
+    device, head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
+    rows = head[5]
+    table, table_stride, width = _table_2d(block_table, device, 0)
+    requests = _int32(row_requests, device, "row_requests", rows)
+    starts = _int32(row_starts, device, "row_starts", rows)
+    ends = _int32(row_ends, device, "row_ends", rows)
+    listed, k = _indices_2d(indices, device, rows)
+    space = _workspace(q.device) if k > _LONG else None
+    _launch(device, _library().attend_prefill, *head, table, table_stride, width, block_table.shape[0], requests,
+            starts, ends, listed, k, scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+            None if space is None else space.data_ptr(), _WORKSPACE)
     return out, lse

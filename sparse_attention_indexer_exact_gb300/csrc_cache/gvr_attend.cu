@@ -6,21 +6,28 @@
 // in one pass over the entries with a running maximum m and running sums that are rescaled when m
 // grows, in any grouping of the entries: groups join by the same rescaling.
 //
-// Work split.  An item is one KV head and up to 8 NT query vectors that read the same entries: the
-// query heads of the group (for whole-cache decode, those of all next_n rows of the request).  A
-// cluster of CTAs takes an item; each of its warps walks over its own steps of 32 entries with its
-// own running state, without any CTA barrier; warps join through shared memory, CTAs through
-// distributed shared memory.  So a call is one launch with no workspace and a fixed order of sums.
+// Work split.  A unit is a set of rows that read the same entries: one row, or (whole-cache decode)
+// the next_n rows of a request.  Its queries fall into jobs of one KV head and 8 NT query vectors
+// each.  A CTA takes one to eight jobs of a unit -- as many KV heads and query tiles as fit its
+// warps, so that an entry's rows of neighbouring heads are fetched together, and once -- and where
+// that leaves warps over, SPLIT warps share a job, each taking every SPLIT-th run of 32 entries.
+// A cluster of up to eight CTAs (and, given a workspace, several clusters) divide the entries.
+// Warps join through shared memory, CTAs through distributed shared memory, clusters through the
+// workspace and a second kernel.  Every sum has a fixed order.
 //
-// A step.  32 rows (codes and scales of K and V, 144 bytes at head_dim 128) arrive in the warp's
-// ring by 16-byte asynchronous copies, STAGES - 1 steps ahead; rows of skipped entries are filled
-// with zeros.  S^T = K Q^T and O^T += V^T P^T run on m16n8k16 matrix instructions with entries
-// (for S) and head dimensions (for O) on the 16-row side: these have the 4-bit operand, expanded
-// in registers straight into the instruction's operand layout, so nothing expanded is ever stored.
-// e2m1 * e4m3 has at most 5 significant bits and an exponent within f16's, so K and V are exact
-// in f16.  Queries are brought to f16 exactly, too: a power of two per query puts its largest
-// element at 2^14, and what f16 cannot hold below that is under 2^-39 of it.  P is rounded to f16
-// (11 bits): eight times finer than the 16-bit outputs' bf16 and averaged over the entries.
+// A step.  32 SPLIT entries (codes and scales of K and V, 144 bytes a head at head_dim 128) arrive in
+// a ring of STAGES stages by 16-byte asynchronous copies, STAGES - 1 steps ahead, each warp fetching
+// its share of the entries; one CTA barrier a step.  (Bulk copies of single rows measured slower: 20
+// to 48 clocks each on an SM whatever their size up to 320 bytes.)  The pitch of an entry in shared
+// memory is an odd multiple of 16 bytes, which with tile_entry's order spreads the operand reads over
+// all banks.  S^T = K Q^T and O^T += V^T P^T run on m16n8k16 matrix instructions with entries (for S)
+// and head dimensions (for O) on the 16-row side: these have the 4-bit operand, expanded in registers
+// straight into the instruction's operand layout, so nothing expanded is ever stored.  e2m1 * e4m3
+// has at most 5 significant bits and an exponent within f16's, so K and V are exact in f16.  Queries
+// are brought to f16 exactly, too: a power of two per query puts its largest element at 2^14, and
+// what f16 cannot hold below that is under 2^-39 of it.  P is rounded to f16 (11 bits): eight times
+// finer than bf16 outputs, and averaged over the entries.
+#include <algorithm>
 #include <mutex>
 
 #include "gvr_cache_common.cuh"
@@ -29,10 +36,14 @@
 namespace gvrc {
 namespace {
 
-constexpr int WARPS = 4;
-constexpr int THREADS = WARPS * 32;
-constexpr int STEP = 32;  // entries per step: one per lane
+constexpr int STEP = 32;  // entries a warp takes at a time: one per lane
+constexpr int STAGES = 3;
+constexpr int MAX_TURNS = 3;  // 512-byte pieces of an entry's rows in a CTA: eight heads of 144 bytes, four of 288
+constexpr int MAX_WARPS = 8;
 constexpr int MAX_CLUSTER = 8;
+constexpr int CTA_STEPS = 3;
+constexpr int PART_STEPS = 4;
+constexpr int JOIN_THREADS = 128;
 
 struct AttendParams {
   const uint8_t* data;
@@ -45,23 +56,31 @@ struct AttendParams {
   const int32_t* indices;   // nullptr: all entries
   void* out;
   float* lse;
+  float* parts_out;  // parts > 1: [item][part][Q * (D + 2)] partial results
   int64_t page_stride, q_row, q_head, table_stride, num_rows, k;
-  int32_t num_pages, page_shift, kv_heads, group, fold, tiles, capacity, next_n, ratio, num_requests, bf16;
-  float scale_log2;  // scale * k_scale * log2(e)
+  int32_t num_pages, page_shift, kv_heads, group, fold, capacity, next_n, ratio, num_requests, bf16;
+  int32_t tiles;            // query tiles of a KV head in a unit
+  int32_t heads_in, tiles_in, split, split_log2;  // a CTA's jobs: heads_in x tiles_in, SPLIT warps each
+  int32_t share;            // entries of a run that each of its warps fetches
+  int32_t head_groups, tile_groups;   // CTAs side by side for the jobs of a unit
+  int32_t items, parts;     // units x head_groups x tile_groups; clusters of CTAs an item
+  int32_t pitch;            // bytes between entries in shared memory
+  float scale_log2;  // |scale| * k_scale * log2(e); 1 for a scale of 0
+  float q_sign;      // the scale's sign, which the queries take on (0 for a scale of 0)
   float v_scale;
 };
 
 // Row r of a 16-entry matrix tile <-> entry of the 16 (a permutation).  Even and odd entries
-// separate, and neighbouring rows four apart modulo 8: with row pitches of 80, 144 and 288 bytes
-// the operand reads of K (two neighbouring tile rows a phase) and of V (every other tile row)
-// then fall on different shared-memory banks.
+// separate, and neighbouring rows four apart modulo 8: with an odd pitch (in 16 bytes) the operand
+// reads of K (two neighbouring tile rows a phase) and of V (every other tile row) then fall on
+// different shared-memory banks.
 __device__ __forceinline__ int tile_entry(int r) {
   const int x = r & 7, e = (x & 1) ? 8 + ((x + 3) & 7) : x;
   return e + (r >> 3);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -74,6 +93,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float4 dsmem_ld_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -113,36 +141,72 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 template <int D, int NT>
 struct Shape {
   static constexpr int RB = row_bytes(D);
-  static constexpr int CHUNKS = RB / 16;  // 16-byte pieces of a row
-  static constexpr int STAGES = D == 256 ? 3 : 4;
-  static constexpr int STAGE_BYTES = STEP * RB;
-  static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
-  static constexpr int Q = 8 * NT;  // query vectors of an item
-  static constexpr int JOIN = (WARPS * Q * D + 3 * WARPS * Q) * int(sizeof(float));
-  static constexpr int OFFSETS = WARPS * STEP * 8;
-  static constexpr int SMEM = (RING > JOIN ? RING : JOIN) + OFFSETS;
+  static constexpr int Q = 8 * NT;  // query vectors of a job
+  // accumulators and queries take 3 D / 8 NT registers: that leaves room for 16, 12 or 8 warps on an SM
+  static constexpr int WARPS = D <= 128 && NT == 1 ? 8 : 4;
+  static constexpr int BLOCKS = D * NT == 128 && NT == 2 ? 3 : 2;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int JOIN = (WARPS * Q * D + 4 * WARPS * Q) * int(sizeof(float));
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
+// Eight finished values of a head: sums over exp2(score - all) v, their sum `sum`.
+template <int D>
+__device__ __forceinline__ void write_out(const AttendParams& p, int64_t row, int head, int d, float all, float sum,
+                                          const float (&acc)[8]) {
+  const float norm = sum == 0.f ? 0.f : p.v_scale / sum;
+  uint32_t packed[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float lo = acc[2 * j] * norm, hi = acc[2 * j + 1] * norm;
+    if (p.bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed[j]) : "f"(hi), "f"(lo));
+    else packed[j] = pack_f16(lo, hi);
+  }
+  const int64_t at = row * (int64_t(p.kv_heads) * p.group) + head;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + d) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+  if (p.lse && d == 0) p.lse[at] = sum == 0.f ? -INFINITY : (all + log2f(sum)) * 0.69314718055994531f;
+}
+
+// FOLD: the unit is the next_n rows of a request (whole-cache decode with next_n > 1).
+template <int D, int NT, bool FOLD>
+__global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) attend_kernel(AttendParams p) {
   using S = Shape<D, NT>;
-  constexpr int STAGES = S::STAGES;
   constexpr int KSTEPS = D / 16;       // 16-wide steps of the head dimension
   constexpr int KW = D / 32;           // 32-bit words of K codes per lane and entry
   constexpr int VW = D / 64;           // the same of V codes
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t exists[4][MAX_WARPS];  // by step modulo 4 and run: which of its entries are there
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in every lane, and known to be
+  const int warps = blockDim.x >> 5;
   const uint32_t rank = gvr::cluster_rank(), cs = gvr::cluster_size();
-  int64_t item = blockIdx.x / cs;
-  const int h = int(item % p.kv_heads);
-  item /= p.kv_heads;
-  const int tile = int(item % p.tiles);
-  const int64_t unit = item / p.tiles;  // a row, or (whole-cache decode) a request's next_n rows
+  const int unit = int(cs == 1 ? blockIdx.x : gvr::cluster_id_x()), part = blockIdx.z;
+  const int tile_group = p.head_groups == 1 ? blockIdx.y : blockIdx.y / p.head_groups;
+  const int head0 = (int(blockIdx.y) - tile_group * p.head_groups) * p.heads_in, tile0 = tile_group * p.tiles_in;
+  const int job = warp >> p.split_log2, sub = warp & (p.split - 1);
+  const int tile_in = p.tiles_in == 1 ? 0 : job / p.heads_in;
+  const int h = head0 + job - tile_in * p.heads_in, tile = tile0 + tile_in;
 
-  // ---- the item's entries: request and number of valid ones
+  // ---- the job's queries, on their way: lane (g, c) holds query 8 t + g at D/4 c + [0, D/4)
+  const int m0 = tile * S::Q;
+  const int members = tile < p.tiles ? (FOLD ? p.fold * p.group : p.group) : 0;
+  uint32_t raw[NT][D / 8];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int m = m0 + 8 * t + g;
+    const int64_t row = FOLD ? int64_t(unit) * p.fold + m / p.group : unit;
+    const bool live = m < members && row < p.num_rows;
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + int64_t(h * p.group + (FOLD ? m % p.group : m)) * p.q_head + c * (D / 4);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+      raw[t][4 * i] = v.x, raw[t][4 * i + 1] = v.y, raw[t][4 * i + 2] = v.z, raw[t][4 * i + 3] = v.w;
+    }
+  }
+
+  // ---- the unit's entries: request and number of valid ones
   int64_t request;
-  int n = 0;        // entries that some row of the item sees
+  int n = 0;        // entries that some row of the unit sees
   int kv = 0;
   if (p.requests) {
     request = p.requests[unit];
@@ -152,104 +216,138 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
       request = 0;
     }
   } else {
-    request = p.fold > 1 ? unit : unit / p.next_n;
+    request = FOLD || p.next_n == 1 ? unit : unit / p.next_n;
     kv = p.lens[request];
-    const int last = p.fold > 1 ? p.next_n - 1 : int(unit % p.next_n);
+    const int last = FOLD ? p.next_n - 1 : unit - int(request) * p.next_n;
     n = decode_entries(kv, p.next_n, last, p.ratio, p.capacity);
   }
   const int32_t* table = p.table + request * p.table_stride;
-  const int32_t* indices = p.indices ? p.indices + unit * p.k : nullptr;
+  const int32_t* indices = p.indices ? p.indices + int64_t(unit) * p.k : nullptr;
   const int64_t listed = indices ? (n > 0 ? p.k : 0) : n;  // positions to walk over
-  const int steps = int((listed + STEP - 1) / STEP);
-  const int walkers = int(cs) * WARPS, me = int(rank) * WARPS + warp;
-  const int mine = steps > me ? (steps - me + walkers - 1) / walkers : 0;
+  const int stage_entries = STEP * p.split;
+  const int steps = int((listed + stage_entries - 1) >> (5 + p.split_log2));
+  const int walkers = p.parts * int(cs), me = part * int(cs) + int(rank);
+  const int mine = walkers == 1 ? steps : steps > me ? (steps - me + walkers - 1) / walkers : 0;
 
-  // ---- the item's queries as operands: lane (g, c) holds query 8 t + g at D/4 c + [0, D/4)
-  const int m0 = tile * S::Q;
-  const int members = p.fold * p.group;
-  uint32_t qb[NT][KSTEPS][2];
-  float factor[NT][2];  // of the scores of queries 8 t + 2 c, 8 t + 2 c + 1: to log2 units
-  int limit[NT][2];     // entries that these queries see
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int m = m0 + 8 * t + g;
-    const int64_t row = unit * p.fold + m / p.group;
-    const bool live = m < members && row < p.num_rows;
-    uint32_t raw[D / 8];
-    if (live) {
-      const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + int64_t(h * p.group + m % p.group) * p.q_head + c * (D / 4);
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) raw[i] = 0;
-    }
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const float2 v = p.bf16 ? make_float2(__uint_as_float(raw[i] << 16), __uint_as_float(raw[i] & 0xffff0000u))
-                              : f16x2_to_f32(raw[i]);
-      big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
-    }
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    // 2^up with up = 14 - exponent(big); no scaling of zero or infinite queries
-    int up = 14 - (int(__float_as_uint(big) >> 23) - 127);
-    up = big == 0.f || up < -113 ? 0 : min(up, 126);
-    const float mul = __uint_as_float(uint32_t(127 + up) << 23), back = __uint_as_float(uint32_t(127 - up) << 23);
-#pragma unroll
-    for (int s = 0; s < KSTEPS; ++s)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t w = raw[2 * s + j];
-        const float2 v = p.bf16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : f16x2_to_f32(w);
-        qb[t][s][j] = pack_f16(v.x * mul, v.y * mul);
-      }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      factor[t][j] = __shfl_sync(0xffffffffu, back, (2 * c + j) * 4) * p.scale_log2;
-      const int mm = m0 + 8 * t + 2 * c + j;
-      limit[t][j] = p.fold > 1 ? decode_entries(kv, p.next_n, min(mm / p.group, p.fold - 1), p.ratio, p.capacity) : n;
-    }
-  }
-  // entries below this are seen by every query of the item
-  const int sure = p.fold > 1 ? decode_entries(kv, p.next_n, 0, p.ratio, p.capacity) : n;
+  // ---- fetching.  The warps that share run `sub` of the steps (one per job) take turns at working
+  // out where its entries lie, three steps before they are fetched: an entry number, a page, and an
+  // address, a step apart (of step i the warp of job i modulo jobs).  Then each fetches its share of
+  // the run.
+  const int jobs = warps >> p.split_log2;
+  const int stage_bytes = stage_entries * p.pitch;
+  const uint32_t ring = gvr::smem_u32(smem);
+  const uint8_t** places = reinterpret_cast<const uint8_t**>(smem + STAGES * stage_bytes) + sub * STEP;  // [2][stage_entries]
+  const int chunks = p.heads_in * (S::RB / 16);
+  const int share = p.share, first_own = job * share, count = min(share, STEP - first_own);
+  const int lanes_log2 = chunks > 16 ? 5 : chunks > 8 ? 4 : 3, lanes = 1 << lanes_log2;  // that copy one entry together
+  const int per_turn = 32 >> lanes_log2, piece = lane & (lanes - 1), of_turn = lane >> lanes_log2;
+  const int step_stride = walkers * stage_entries;
 
-  // ---- the walk
-  uint8_t* ring = smem + warp * STAGES * S::STAGE_BYTES;
-  int64_t* offsets = reinterpret_cast<int64_t*>(smem + S::SMEM - S::OFFSETS) + warp * STEP;
-
-  auto load_entry = [&](int i) -> int {  // this lane's entry in my i-th step (-1: none)
+  auto load_entry = [&](int i) -> int {  // this lane's entry of step i of mine (-1: none)
     if (i >= mine) return -1;
-    const int64_t pos = int64_t(me + i * walkers) * STEP + lane;
+    const int64_t pos = int64_t(me) * stage_entries + int64_t(i) * step_stride + sub * STEP + lane;
     if (pos >= listed) return -1;
     const int e = indices ? __ldg(indices + pos) : int(pos);
     return e < n ? e : -1;
   };
   auto load_page = [&](int e) -> int { return e >= 0 ? __ldg(table + (e >> p.page_shift)) : -1; };
-  // issue the copies of a step; returns which lanes' entries exist
-  auto issue = [&](int i, int e, int page) -> uint32_t {
-    const int64_t off = row_offset(page, p.num_pages, e, p.page_shift, p.page_stride, p.kv_heads, h, S::RB);
-    offsets[lane] = off;
-    const uint32_t mask = __ballot_sync(0xffffffffu, off >= 0);
-    __syncwarp();
-    if (i < mine) {
-      const uint32_t dst = gvr::smem_u32(ring + (i % STAGES) * S::STAGE_BYTES);
+  auto place = [&](int i, int e, int page) {
+    const int64_t off = row_offset(page, p.num_pages, e, p.page_shift, p.page_stride, p.kv_heads, head0, S::RB);
+    const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
+    // a missing entry beside others is fetched from where one of them lies, and not looked at
+    const int64_t some = __shfl_sync(0xffffffffu, off, there ? __ffs(there) - 1 : 0);
+    places[(i & 1) * stage_entries + lane] = p.data + (off < 0 ? some : off);
+    if (lane == 0) exists[i & 3][sub] = there;
+  };
+  bool whole[MAX_TURNS];  // whether this lane has a piece in each 512 bytes of an entry's rows
 #pragma unroll
-      for (int j = 0; j < S::CHUNKS; ++j) {
-        const int id = j * 32 + lane, row = id / S::CHUNKS, part = id % S::CHUNKS;
-        const int64_t o = offsets[row];
-        copy16(dst + id * 16, p.data + (o < 0 ? 0 : o + part * 16), o < 0 ? 0 : 16);
+  for (int x = 0; x < MAX_TURNS; ++x) whole[x] = piece + 32 * x < chunks;
+  auto fetch = [&](int i, uint32_t stage_at) {
+    if (i < mine && exists[i & 3][sub]) {
+      const uint8_t** from = places + (i & 1) * stage_entries + first_own;
+      uint32_t dst = stage_at + (sub * STEP + first_own) * p.pitch + piece * 16;
+      if (lanes == 32) {
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) {
+          const uint8_t* at = from[j] + piece * 16;
+#pragma unroll
+          for (int x = 0; x < MAX_TURNS; ++x)
+            if (whole[x]) copy16(dst + 512 * x, at + 512 * x);
+          dst += p.pitch;
+        }
+      } else {
+        dst += of_turn * p.pitch;
+#pragma unroll 4
+        for (int j = of_turn; j < count; j += per_turn) {
+          if (whole[0]) copy16(dst, from[j] + piece * 16);
+          dst += per_turn * p.pitch;
+        }
       }
     }
     copy_commit();
-    __syncwarp();
-    return mask;
   };
+  // The next of the own steps (job, job + jobs, ...) to place, to load pages and entries of.
+  int to_place = job, to_page = 0, to_enter = 0, e_next = -1, e_page = -1, page = -1;
+  {
+    int e[5], pg[4];
+    uint32_t own = 0;  // which of the first five steps
+    for (int j = job; j < 5; j += jobs) own |= 1u << j;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) e[i] = (own >> i) & 1 ? load_entry(i) : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pg[i] = load_page(e[i]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if ((own >> i) & 1) place(i, e[i], pg[i]);
+    __syncthreads();
+    fetch(0, ring);
+    fetch(1, ring + stage_bytes);
+    __syncthreads();
+    if ((own >> 2) & 1) place(2, e[2], pg[2]);
+    if ((own >> 3) & 1) e_page = e[3], page = pg[3];
+    if ((own >> 4) & 1) e_next = e[4];
+    while (to_place < 3) to_place += jobs;
+    for (to_page = to_place; to_page < 4;) to_page += jobs;
+    for (to_enter = to_page; to_enter < 5;) to_enter += jobs;
+  }
 
+  // ---- the queries as operands
+  uint32_t qb[NT][KSTEPS][2];
+  float factor[NT][2];  // of the scores of queries 8 t + 2 c, 8 t + 2 c + 1: to log2 units
+  int limit[NT][2];     // entries that these queries see
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float back = 1.f;
+    if (p.bf16) {
+      // 2^up with up = 14 - exponent of the largest; none of zero or infinite queries
+      uint32_t big = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, raw[t][i] & 0x7fff7fffu);
+      big = max(big & 0xffffu, big >> 16);
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int exponent = int(big >> 7), up = big == 0 || exponent == 255 ? 0 : min(14 - (exponent - 127), 126);
+      const float mul = p.q_sign * __uint_as_float(uint32_t(127 + up) << 23);
+      back = __uint_as_float(uint32_t(127 - up) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        qb[t][i / 2][i % 2] = pack_f16(__uint_as_float(raw[t][i] << 16) * mul, __uint_as_float(raw[t][i] & 0xffff0000u) * mul);
+    } else {
+      const uint32_t sign = pack_f16(p.q_sign, p.q_sign);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) qb[t][i / 2][i % 2] = hmul2(raw[t][i], sign);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      factor[t][j] = fmaxf(__shfl_sync(0xffffffffu, back, (2 * c + j) * 4) * p.scale_log2, 1.17549435e-38f);  // never 0
+      const int mm = m0 + 8 * t + 2 * c + j;
+      if (FOLD) limit[t][j] = decode_entries(kv, p.next_n, min(mm / p.group, p.fold - 1), p.ratio, p.capacity);
+    }
+  }
+  // entries below this are seen by every query of the unit
+  const int sure = FOLD ? decode_entries(kv, p.next_n, 0, p.ratio, p.capacity) : n;
+
+  // ---- the walk
   float o[NT][KSTEPS][4];
   float top[NT][2], total[NT][2];
 #pragma unroll
@@ -261,41 +359,33 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
     top[t][0] = top[t][1] = -INFINITY;
     total[t][0] = total[t][1] = 0.f;
   }
-
-  uint32_t masks[STAGES];
-  {
-    int e[STAGES + 1];
-#pragma unroll
-    for (int i = 0; i < STAGES + 1; ++i) e[i] = load_entry(i);
-    int pg[STAGES - 1];
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) pg[i] = load_page(e[i]);
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) masks[i] = issue(i, e[i], pg[i]);
-    masks[STAGES - 1] = 0;
-    // carried: entry and page of step STAGES - 1, entry of step STAGES
-    int e_next = e[STAGES - 1], e_after = e[STAGES];
-    int pg_next = load_page(e_next);
-
-    for (int i = 0; i < mine; ++i) {
+  // where this lane's operand rows start in a stage: of K, tile rows g and g + 8 (the next entry); of V,
+  // columns 2 c and 2 c + 1 (and 8 behind them, the next entries)
+  const int run = sub * STEP * p.pitch + (h - head0) * S::RB;
+  const int k_at = run + tile_entry(g) * p.pitch;
+  const int v_at0 = run + tile_entry(2 * c) * p.pitch, v_at1 = run + tile_entry(2 * c + 1) * p.pitch;
+  int now = 0, before = (STAGES - 1) * stage_bytes;  // bytes of this step's stage and of the one before
+  for (int i = 0; i < mine; ++i) {
+    {
       copy_wait<STAGES - 2>();
-      __syncwarp();
-      masks[STAGES - 1] = issue(i + STAGES - 1, e_next, pg_next);
-      e_next = e_after;
-      pg_next = load_page(e_next);
-      e_after = load_entry(i + STAGES + 1);
+      __syncthreads();  // the step's entries are here, and the stage before it is free
+      fetch(i + STAGES - 1, ring + before);
+      if (i + 3 == to_place) place(i + 3, e_page, page), to_place += jobs;
+      if (i + 4 == to_page) e_page = e_next, page = load_page(e_next), to_page += jobs;
+      if (i + 5 == to_enter) e_next = load_entry(i + 5), to_enter += jobs;
 
-      const uint8_t* st = ring + (i % STAGES) * S::STAGE_BYTES;
-      const uint32_t mask = masks[0];
-#pragma unroll
-      for (int j = 0; j < STAGES - 1; ++j) masks[j] = masks[j + 1];
+      const uint8_t* st = smem + now;
+      before = now;
+      now = now == (STAGES - 1) * stage_bytes ? 0 : now + stage_bytes;
+      const uint32_t mask = exists[i & 3][sub];
+      if (mask == 0) continue;
 
       // S^T: two tiles of 16 entries
       float s[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const uint8_t* r0 = st + (16 * mt + tile_entry(g)) * S::RB;
-        const uint8_t* r1 = st + (16 * mt + tile_entry(g + 8)) * S::RB;
+        const uint8_t* r0 = st + k_at + 16 * mt * p.pitch;
+        const uint8_t* r1 = r0 + p.pitch;
         uint32_t k0[KW], k1[KW];
         load_words<KW>(r0 + c * (D / 8), k0);
         load_words<KW>(r1 + c * (D / 8), k1);
@@ -325,15 +415,11 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
         }
       }
 
-      // to log2 units; entries that are skipped or beyond a query's limit leave the sums
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[mt][t][j] *= factor[t][j & 1];
-      const int first = (me + i * walkers) * STEP;
-      if (mask != 0xffffffffu || (p.fold > 1 && first > sure - STEP)) {
+      // entries that are skipped or beyond a query's limit leave the sums
+      // entries that only some rows of the unit see (at most at its end)
+      const int64_t first = int64_t(me) * stage_entries + int64_t(i) * step_stride + sub * STEP;
+      const bool border = FOLD && first + STEP > sure;
+      if (mask != 0xffffffffu || border) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -342,7 +428,7 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
             const bool there = (mask >> at) & 1;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-              if (!there || (p.fold > 1 && first + at >= limit[t][j & 1])) s[mt][t][j] = -INFINITY;
+              if (!there || (border && first + at >= limit[t][j & 1])) s[mt][t][j] = -INFINITY;
           }
       }
 
@@ -357,8 +443,8 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          high[t][j] = v;
-          grow |= v > top[t][j] + 8.f;
+          high[t][j] = v * factor[t][j];  // in log2 units; factors are positive
+          grow |= high[t][j] > top[t][j] + 8.f;
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -384,8 +470,8 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
         const float base0 = top[t][0] == -INFINITY ? 0.f : top[t][0], base1 = top[t][1] == -INFINITY ? 0.f : top[t][1];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const float e0 = exp2_fast(s[mt][t][0] - base0), e1 = exp2_fast(s[mt][t][1] - base1);
-          const float e2 = exp2_fast(s[mt][t][2] - base0), e3 = exp2_fast(s[mt][t][3] - base1);
+          const float e0 = exp2_fast(fmaf(s[mt][t][0], factor[t][0], -base0)), e1 = exp2_fast(fmaf(s[mt][t][1], factor[t][1], -base1));
+          const float e2 = exp2_fast(fmaf(s[mt][t][2], factor[t][0], -base0)), e3 = exp2_fast(fmaf(s[mt][t][3], factor[t][1], -base1));
           total[t][0] += e0 + e2;
           total[t][1] += e1 + e3;
           pb[mt][t][0] = transpose8x8(pack_f16(e0, e1));
@@ -393,52 +479,71 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
         }
       }
 
-      // O^T += V^T P^T: lane (g, c) expands V at D/8 g + [0, D/8) of four entries of each tile
+      // O^T += V^T P^T: lane (g, c) expands V at D/8 g + [0, D/8) of four entries of each tile.  An
+      // entry that is left out has P = 0 and, as 0 x NaN is NaN, a V scale of 0.  At the border that
+      // differs from row to row, so each row of the job takes a pass with its own entries.
+      int j = border ? m0 / p.group : 0;
+      const int j_end = border ? min((m0 + S::Q - 1) / p.group, p.fold - 1) : 0;
+      do {
+        uint32_t there = mask, pj[2][NT][2];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t v[4][VW], vs[4];
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint8_t* r = st + (16 * mt + tile_entry(2 * c + (x & 1) + 8 * (x >> 1))) * S::RB;
-          load_words<VW>(r + D / 2 + g * (D / 16), v[x]);
-          if (D == 64) vs[x] = r[D + D / 16 + (g >> 1)];
-          else if (D == 128) vs[x] = r[D + D / 16 + g];
-          else vs[x] = *reinterpret_cast<const uint16_t*>(r + D + D / 16 + 2 * g);
+          for (int t = 0; t < NT; ++t) pj[mt][t][0] = pb[mt][t][0], pj[mt][t][1] = pb[mt][t][1];
+        if (border) {
+          const int64_t seen = decode_entries(kv, p.next_n, j, p.ratio, p.capacity) - first;
+          there &= seen <= 0 ? 0u : seen >= 32 ? 0xffffffffu : (1u << int(seen)) - 1;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if ((m0 + 8 * t + g) / p.group != j) pj[0][t][0] = pj[0][t][1] = pj[1][t][0] = pj[1][t][1] = 0;
         }
-        uint32_t x01[VW > 2 ? 2 : 1], x23[VW > 2 ? 2 : 1];  // scales of the entry pairs
 #pragma unroll
-        for (int b = 0; b < (VW > 2 ? 2 : 1); ++b) {
-          x01[b] = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], b ? 0x0051 : 0x0040));
-          x23[b] = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], b ? 0x0051 : 0x0040));
-        }
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t v[4][VW], vs[4];
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-          // bytes of (entry 0, entry 1) codes: of the even values, of the odd values
-          uint32_t lo01[4], hi01[4], lo23[4], hi23[4];
-          e2m1_to_f16x2((v[0][w] & 0x0f0f0f0fu) | ((v[1][w] << 4) & 0xf0f0f0f0u), lo01);
-          e2m1_to_f16x2(((v[0][w] >> 4) & 0x0f0f0f0fu) | (v[1][w] & 0xf0f0f0f0u), hi01);
-          e2m1_to_f16x2((v[2][w] & 0x0f0f0f0fu) | ((v[3][w] << 4) & 0xf0f0f0f0u), lo23);
-          e2m1_to_f16x2(((v[2][w] >> 4) & 0x0f0f0f0fu) | (v[3][w] & 0xf0f0f0f0u), hi23);
-          const uint32_t y01 = x01[w / 2], y23 = x23[w / 2];
+          for (int x = 0; x < 4; ++x) {
+            const uint8_t* r = st + (x & 1 ? v_at1 : v_at0) + (16 * mt + (x >> 1)) * p.pitch;
+            load_words<VW>(r + D / 2 + g * (D / 16), v[x]);
+            if (D == 64) vs[x] = r[D + D / 16 + (g >> 1)];
+            else if (D == 128) vs[x] = r[D + D / 16 + g];
+            else vs[x] = *reinterpret_cast<const uint16_t*>(r + D + D / 16 + 2 * g);
+          }
+          if (there != 0xffffffffu) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t a0 = hmul2(lo01[b], y01), a1 = hmul2(hi01[b], y01);
-            const uint32_t a2 = hmul2(lo23[b], y23), a3 = hmul2(hi23[b], y23);
+            for (int x = 0; x < 4; ++x)
+              if (!((there >> (16 * mt + tile_entry(2 * c + (x & 1) + 8 * (x >> 1)))) & 1)) vs[x] = 0;
+          }
+          uint32_t x01[VW > 2 ? 2 : 1], x23[VW > 2 ? 2 : 1];  // scales of the entry pairs
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma(o[t][4 * w + b], a0, a1, a2, a3, pb[mt][t][0], pb[mt][t][1]);
+          for (int b = 0; b < (VW > 2 ? 2 : 1); ++b) {
+            x01[b] = e4m3x2_to_f16x2(__byte_perm(vs[0], vs[1], b ? 0x0051 : 0x0040));
+            x23[b] = e4m3x2_to_f16x2(__byte_perm(vs[2], vs[3], b ? 0x0051 : 0x0040));
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            // bytes of (entry 0, entry 1) codes: of the even values, of the odd values
+            uint32_t lo01[4], hi01[4], lo23[4], hi23[4];
+            e2m1_to_f16x2((v[0][w] & 0x0f0f0f0fu) | ((v[1][w] << 4) & 0xf0f0f0f0u), lo01);
+            e2m1_to_f16x2(((v[0][w] >> 4) & 0x0f0f0f0fu) | (v[1][w] & 0xf0f0f0f0u), hi01);
+            e2m1_to_f16x2((v[2][w] & 0x0f0f0f0fu) | ((v[3][w] << 4) & 0xf0f0f0f0u), lo23);
+            e2m1_to_f16x2(((v[2][w] >> 4) & 0x0f0f0f0fu) | (v[3][w] & 0xf0f0f0f0u), hi23);
+            const uint32_t y01 = x01[w / 2], y23 = x23[w / 2];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const uint32_t a0 = hmul2(lo01[b], y01), a1 = hmul2(hi01[b], y01);
+              const uint32_t a2 = hmul2(lo23[b], y23), a3 = hmul2(hi23[b], y23);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma(o[t][4 * w + b], a0, a1, a2, a3, pj[mt][t][0], pj[mt][t][1]);
+            }
           }
         }
-      }
+      } while (++j <= j_end);
     }
   }
   copy_wait<0>();
-  __syncthreads();  // the ring becomes the warps' partial results
+  __syncthreads();  // every copy has landed, every stage is read: the ring becomes the partial results
 
-  // ---- join the warps, then the CTAs
-  float* part = reinterpret_cast<float*>(smem);           // [WARPS][Q][D]
-  float* tops = part + WARPS * S::Q * D;                  // [WARPS][Q]
-  float* sums = tops + WARPS * S::Q;                      // [WARPS][Q]
-  float* joined = sums + WARPS * S::Q;                    // [2][Q]: the CTA's maximum and sum
+  // ---- the lanes' sums of each query
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -447,11 +552,41 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
       v += __shfl_xor_sync(0xffffffffu, v, 4);
       v += __shfl_xor_sync(0xffffffffu, v, 8);
       v += __shfl_xor_sync(0xffffffffu, v, 16);
-      if (g == 0) {
-        tops[warp * S::Q + 8 * t + 2 * c + j] = top[t][j];
-        sums[warp * S::Q + 8 * t + 2 * c + j] = v;
-      }
+      total[t][j] = v;
     }
+  if (p.split == 1 && walkers == 1) {  // the warp has its job's whole sums: lane (g, c) writes D/8 values
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int m = m0 + 8 * t + 2 * c + j;
+        const int64_t row = FOLD ? int64_t(unit) * p.fold + m / p.group : unit;
+        if (m >= members || row >= p.num_rows) continue;
+#pragma unroll
+        for (int x = 0; x < KSTEPS; x += 4) {
+          float acc[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) acc[2 * y] = o[t][x + y][j], acc[2 * y + 1] = o[t][x + y][j + 2];
+          write_out<D>(p, row, h * p.group + (FOLD ? m % p.group : m), g * (D / 8) + 2 * x, top[t][j], total[t][j], acc);
+        }
+      }
+    return;
+  }
+
+  // ---- join the warps of a job, then the CTAs
+  float* partial = reinterpret_cast<float*>(smem);   // [warps][Q][D]
+  float* tops = partial + warps * S::Q * D;          // [warps][Q]
+  float* sums = tops + warps * S::Q;                 // [warps][Q]
+  float* joined = sums + warps * S::Q;               // [jobs][2][Q]: maximum and sum of a job in this CTA
+  if (g == 0) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        tops[warp * S::Q + 8 * t + 2 * c + j] = top[t][j];
+        sums[warp * S::Q + 8 * t + 2 * c + j] = total[t][j];
+      }
+  }
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -459,95 +594,118 @@ __global__ void __launch_bounds__(THREADS) attend_kernel(AttendParams p) {
     for (int j = 0; j < 2; ++j) {
       const int qi = 8 * t + 2 * c + j;
       float all = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) all = fmaxf(all, tops[w * S::Q + qi]);
+      for (int w = job * p.split; w < (job + 1) * p.split; ++w) all = fmaxf(all, tops[w * S::Q + qi]);
       const float down = top[t][j] == -INFINITY ? 1.f : exp2_fast(top[t][j] - all);
-      float* dst = part + (warp * S::Q + qi) * D + g * (D / 8);
+      float* dst = partial + (warp * S::Q + qi) * D + g * (D / 8);
 #pragma unroll
       for (int x = 0; x < KSTEPS; ++x)
         *reinterpret_cast<float2*>(dst + 2 * x) = make_float2(o[t][x][j] * down, o[t][x][j + 2] * down);
-      if (warp == 0 && g == 0) {
+      if (sub == 0 && g == 0) {
         float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = job * p.split; w < (job + 1) * p.split; ++w) {
           const float tw = tops[w * S::Q + qi];
           sum += sums[w * S::Q + qi] * (tw == -INFINITY ? 1.f : exp2_fast(tw - all));
         }
-        joined[qi] = all;
-        joined[S::Q + qi] = sum;
+        joined[job * 2 * S::Q + qi] = all;
+        joined[job * 2 * S::Q + S::Q + qi] = sum;
       }
     }
   __syncthreads();
-  if (cs > 1) {
-    // the CTA's own sum over its warps, in place of warp 0's part, for the other CTAs to read
-    for (int i = tid; i < S::Q * D / 4; i += THREADS) {
-      float4* at = reinterpret_cast<float4*>(part) + i;
+  constexpr int EIGHTS = D / 8;
+  if (p.split > 1) {
+    // the job's sum over its warps, in place of its first warp's
+    for (int i = tid; i < jobs * S::Q * D / 4; i += blockDim.x) {
+      float4* at = reinterpret_cast<float4*>(partial) + i / (S::Q * D / 4) * p.split * (S::Q * D / 4) + i % (S::Q * D / 4);
       float4 sum = *at;
-#pragma unroll
-      for (int w = 1; w < WARPS; ++w) {
+      for (int w = 1; w < p.split; ++w) {
         const float4 v = at[w * S::Q * D / 4];
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
       }
       *at = sum;
     }
-    gvr::cluster_sync();
   }
-  const uint32_t part_addr = gvr::smem_u32(part), joined_addr = gvr::smem_u32(joined);
-  // each CTA of the cluster finishes its share of the queries x head dimension, eight values a thread
-  constexpr int EIGHTS = D / 8;
-  for (int i = int(rank) * THREADS + tid; i < S::Q * EIGHTS; i += int(cs) * THREADS) {
-    const int qi = i / EIGHTS, d = (i % EIGHTS) * 8;
-    const int m = m0 + qi;
-    const int64_t row = unit * p.fold + m / p.group;
-    if (m >= members || row >= p.num_rows) continue;
-    float all, sum = 0.f, acc[8];
+  if (cs > 1) gvr::cluster_sync();
+  else __syncthreads();
+  const uint32_t partial_addr = gvr::smem_u32(partial), joined_addr = gvr::smem_u32(joined);
+  // each CTA of the cluster finishes its share of jobs x queries x head dimension, eight values a thread
+  for (int i = int(rank) * blockDim.x + tid; i < jobs * S::Q * EIGHTS; i += int(cs) * blockDim.x) {
+    const int jb = i / (S::Q * EIGHTS), qi = i / EIGHTS % S::Q, d = i % EIGHTS * 8;
+    const int m = (tile0 + jb / p.heads_in) * S::Q + qi, hj = head0 + jb % p.heads_in;
+    const int64_t row = FOLD ? int64_t(unit) * p.fold + m / p.group : unit;
+    if (m >= p.fold * p.group || row >= p.num_rows) continue;
+    const uint32_t top_at = joined_addr + (jb * 2 * S::Q + qi) * 4, sum_at = top_at + S::Q * 4;
+    const uint32_t at = partial_addr + (jb * p.split * S::Q * D + qi * D + d) * 4;
+    float all = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-    if (cs == 1) {
-      all = joined[qi], sum = joined[S::Q + qi];
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float4* src = reinterpret_cast<const float4*>(part + (w * S::Q + qi) * D + d);
-        const float4 a = src[0], b = src[1];
-        acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w, acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
-      }
+    for (int y = 0; y < 8; ++y) acc[y] = 0.f;
+    for (uint32_t r = 0; r < cs; ++r) all = fmaxf(all, __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(top_at, r))));
+    for (uint32_t r = 0; r < cs; ++r) {
+      const float tr = __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(top_at, r)));
+      const float down = tr == -INFINITY ? 1.f : exp2_fast(tr - all);
+      sum += down * __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(sum_at, r)));
+      const float4 a = dsmem_ld_f32x4(gvr::dsmem_map(at, r)), b = dsmem_ld_f32x4(gvr::dsmem_map(at + 16, r));
+      acc[0] += down * a.x, acc[1] += down * a.y, acc[2] += down * a.z, acc[3] += down * a.w;
+      acc[4] += down * b.x, acc[5] += down * b.y, acc[6] += down * b.z, acc[7] += down * b.w;
+    }
+    if (p.parts > 1) {
+      float* dst = p.parts_out + (((int64_t(unit) * gridDim.y + blockIdx.y) * jobs + jb) * p.parts + part) * (S::Q * (D + 2));
+      *reinterpret_cast<float4*>(dst + qi * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      *reinterpret_cast<float4*>(dst + qi * D + d + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (d == 0) dst[S::Q * D + qi] = all, dst[S::Q * (D + 1) + qi] = sum;
     } else {
-      all = -INFINITY;
-      for (uint32_t r = 0; r < cs; ++r) all = fmaxf(all, __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(joined_addr + qi * 4, r))));
-      for (uint32_t r = 0; r < cs; ++r) {
-        const float tr = __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(joined_addr + qi * 4, r)));
-        const float down = tr == -INFINITY ? 1.f : exp2_fast(tr - all);
-        sum += down * __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(joined_addr + (S::Q + qi) * 4, r)));
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          acc[j] += down * __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(part_addr + ((qi * D) + d + j) * 4, r)));
-      }
+      write_out<D>(p, row, hj * p.group + (FOLD ? m % p.group : m), d, all, sum, acc);
     }
-    const float norm = sum == 0.f ? 0.f : p.v_scale / sum;
-    uint32_t packed[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float lo = acc[2 * j] * norm, hi = acc[2 * j + 1] * norm;
-      if (p.bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed[j]) : "f"(hi), "f"(lo));
-      else packed[j] = pack_f16(lo, hi);
-    }
-    const int64_t head = row * (int64_t(p.kv_heads) * p.group) + h * p.group + m % p.group;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + head * D + d) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-    if (p.lse && d == 0) p.lse[head] = sum == 0.f ? -INFINITY : (all + log2f(sum)) * 0.69314718055994531f;
   }
   if (cs > 1) gvr::cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
+// Joins the parts of a job that was split over several clusters: one CTA a job, eight values a
+// thread, parts in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(AttendParams p) {
+  using S = Shape<D, NT>;
+  const int jobs = p.heads_in * p.tiles_in, item = blockIdx.x / jobs, jb = blockIdx.x % jobs;
+  const int groups = p.head_groups * p.tile_groups, group = item % groups;
+  const int h = group % p.head_groups * p.heads_in + jb % p.heads_in;
+  const int tile = group / p.head_groups * p.tiles_in + jb / p.heads_in;
+  const int64_t unit = item / groups;
+  const float* src = p.parts_out + int64_t(blockIdx.x) * p.parts * (S::Q * (D + 2));
+  constexpr int EIGHTS = D / 8;
+  for (int i = threadIdx.x; i < S::Q * EIGHTS; i += JOIN_THREADS) {
+    const int qi = i / EIGHTS, d = (i % EIGHTS) * 8, m = tile * S::Q + qi;
+    const int64_t row = unit * p.fold + m / p.group;
+    if (m >= p.fold * p.group || row >= p.num_rows) continue;
+    float all = -INFINITY, sum = 0.f, acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    for (int r = 0; r < p.parts; ++r) all = fmaxf(all, src[int64_t(r) * (S::Q * (D + 2)) + S::Q * D + qi]);
+    for (int r = 0; r < p.parts; ++r) {
+      const float* from = src + int64_t(r) * (S::Q * (D + 2));
+      const float tr = from[S::Q * D + qi], down = tr == -INFINITY ? 1.f : exp2_fast(tr - all);
+      sum += down * from[S::Q * (D + 1) + qi];
+      const float4 a = *reinterpret_cast<const float4*>(from + qi * D + d), b = *reinterpret_cast<const float4*>(from + qi * D + d + 4);
+      acc[0] += down * a.x, acc[1] += down * a.y, acc[2] += down * a.z, acc[3] += down * a.w;
+      acc[4] += down * b.x, acc[5] += down * b.y, acc[6] += down * b.z, acc[7] += down * b.w;
+    }
+    write_out<D>(p, row, h * p.group + m % p.group, d, all, sum, acc);
+  }
+}
+
 // ------------------------------------------------------------------------------------- host
 struct KernelInfo {
-  const void* kernel;
-  int smem;
-  int queries;
+  const void* kernel[2];  // by FOLD
+  const void* join;
+  int queries, warps;
+  int part_bytes;  // of one job's results
+  int join_bytes;  // shared memory of a CTA's join
 };
 
 template <int D, int NT>
 KernelInfo info() {
-  return {reinterpret_cast<const void*>(attend_kernel<D, NT>), Shape<D, NT>::SMEM, 8 * NT};
+  using S = Shape<D, NT>;
+  return {{reinterpret_cast<const void*>(attend_kernel<D, NT, false>), reinterpret_cast<const void*>(attend_kernel<D, NT, true>)},
+          reinterpret_cast<const void*>(join_kernel<D, NT>), S::Q,
+          S::WARPS, S::Q * (D + 2) * int(sizeof(float)), S::JOIN};
 }
 
 constexpr int KERNELS = 6;
@@ -556,9 +714,9 @@ const KernelInfo& kernel_info(int i) {
   return all[i];
 }
 
-// Fewest passes over the entries, then fewest query vectors: 8, 16 or 32 of them a pass, as far as
-// the accumulators (head_dim / 16 x 4 registers for each 8) leave room.
-int choose_kernel(int dim, int members) {
+// 8, 16 or 32 query vectors a job, as far as the accumulators (head_dim / 16 x 4 registers for each
+// 8) leave room.
+int choose_kernel(int dim, int64_t members) {
   if (dim == 64) return members <= 8 ? 0 : members <= 16 ? 1 : 2;
   if (dim == 128) return members <= 8 ? 3 : 4;
   return 5;
@@ -567,34 +725,44 @@ int choose_kernel(int dim, int members) {
 struct Device {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
-  int resident[KERNELS] = {};  // CTAs on the whole device
+  int sms = 0, smem_per_sm = 0, smem_reserved = 0;
+  int ctas_by_registers[KERNELS][2] = {};  // of the kernel's full size, per SM
 };
 Device g_devices[kMaxDevices];
 
-cudaError_t resident_ctas(int kernel, int* ctas) {
+cudaError_t device_info(Device** out) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   Device& d = g_devices[dev];  // sm_count has checked dev
-  std::call_once(d.once, [&d, sms]() {
+  std::call_once(d.once, [&d, sms, dev]() {
+    d.sms = sms;
+    int most = 0;
+    d.err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&d.smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+    if (d.err == cudaSuccess) d.err = cudaDeviceGetAttribute(&d.smem_reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
     for (int i = 0; i < KERNELS && d.err == cudaSuccess; ++i) {
       const KernelInfo& k = kernel_info(i);
-      d.err = cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-      if (d.err == cudaSuccess) d.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.resident[i], k.kernel, THREADS, k.smem);
-      d.resident[i] *= sms;
+      for (int f = 0; f < 2; ++f) {
+        cudaFuncAttributes a;
+        if (d.err == cudaSuccess) d.err = cudaFuncGetAttributes(&a, k.kernel[f]);
+        if (d.err == cudaSuccess)
+          d.err = cudaFuncSetAttribute(k.kernel[f], cudaFuncAttributeMaxDynamicSharedMemorySize, most - int(a.sharedSizeBytes));
+        if (d.err == cudaSuccess)
+          d.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.ctas_by_registers[i][f], k.kernel[f], 32 * k.warps, 0);
+      }
     }
   });
-  *ctas = d.resident[kernel];
+  *out = &d;
   return d.err;
 }
 
 gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride, int64_t q_head_stride, int32_t dtype,
                   int64_t num_rows, int32_t num_heads, int64_t table_stride, int64_t table_width, int64_t k, float scale,
-                  void* stream) {
+                  void* workspace, size_t workspace_bytes, void* stream) {
   const int group = num_heads / cache->num_kv_heads;
-  // with no pages every copy is of 0 bytes: from any valid address
-  p.data = static_cast<const uint8_t*>(cache->num_pages > 0 ? cache->data : p.q);
+  p.data = static_cast<const uint8_t*>(cache->data);
   p.page_stride = cache->page_stride;
   p.q_row = q_row_stride;
   p.q_head = q_head_stride;
@@ -605,39 +773,81 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
   p.page_shift = log2_of(cache->page_size);
   p.kv_heads = cache->num_kv_heads;
   p.group = group;
-  p.capacity = int32_t(table_width * cache->page_size);
+  p.capacity = cache->num_pages > 0 ? int32_t(table_width * cache->page_size) : 0;  // no pages: no entries
   p.bf16 = dtype == GVR_BF16;
-  p.scale_log2 = float(double(scale) * cache->k_scale * 1.4426950408889634);
+  p.scale_log2 = scale == 0.f ? 1.f : float(std::fabs(double(scale)) * cache->k_scale * 1.4426950408889634);
+  p.q_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
   p.v_scale = cache->v_scale;
-  // whole-cache decode: the rows of a request read the same entries, so they share an item
+  // whole-cache decode: the rows of a request read the same entries, so they share a unit
   p.fold = p.indices ? 1 : p.next_n;
   const int64_t members = int64_t(p.fold) * group;
   if (members > kIntMax) return GVR_ERR_ARG;
-  const int kernel = choose_kernel(cache->head_dim, int(members > 64 ? 64 : members));
+  const int kernel = choose_kernel(cache->head_dim, members);
   const KernelInfo& info = kernel_info(kernel);
+  // a CTA's jobs: all query tiles of a KV head as far as its warps go, then neighbouring KV heads
+  // (a divisor of their number), then several warps a job
   p.tiles = int32_t((members + info.queries - 1) / info.queries);
+  p.tile_groups = (p.tiles + info.warps - 1) / info.warps;
+  p.tiles_in = (p.tiles + p.tile_groups - 1) / p.tile_groups;
+  p.heads_in = info.warps / p.tiles_in;
+  while (p.kv_heads % p.heads_in) --p.heads_in;
+  p.head_groups = p.kv_heads / p.heads_in;
+  const int jobs = p.heads_in * p.tiles_in;
+  p.split_log2 = jobs > info.warps / 2 ? 0 : jobs > info.warps / 4 ? 1 : jobs > info.warps / 8 ? 2 : 3;  // a power of two
+  p.split = 1 << p.split_log2;
+  p.share = (STEP + jobs - 1) / jobs;
+  const int threads = 32 * jobs * p.split;
+  const int chunks = p.heads_in * (row_bytes(cache->head_dim) / 16);
+  p.pitch = 16 * (chunks | 1);
+  const int smem = std::max(STEP * p.split * (STAGES * p.pitch + 2 * int(sizeof(int64_t))), info.join_bytes);
   const int64_t units = (num_rows + p.fold - 1) / p.fold;
-  if (units > kIntMax / p.tiles / p.kv_heads / MAX_CLUSTER) return GVR_ERR_ARG;
-  const int64_t items = units * p.tiles * p.kv_heads;
-  int resident = 0;
-  if (resident_ctas(kernel, &resident) != cudaSuccess) return GVR_ERR_LAUNCH;
-  // CTAs per item: until the device is full, while each warp keeps a step
-  const int64_t most = p.indices ? k : p.capacity;
+  const int64_t groups = int64_t(p.tile_groups) * p.head_groups;
+  if (groups > 65535 || units > kIntMax / groups / MAX_CLUSTER) return GVR_ERR_ARG;
+  p.items = int32_t(units * groups);
+  Device* d = nullptr;
+  if (device_info(&d) != cudaSuccess) return GVR_ERR_LAUNCH;
+  const int64_t resident = int64_t(d->sms) * std::max(1, std::min(d->ctas_by_registers[kernel][p.fold > 1], d->smem_per_sm / (smem + 256 + d->smem_reserved)));
+  // CTAs per item: the cluster size with the fewest rounds of steps, counting a CTA's start and end
+  // as CTA_STEPS steps
+  const int64_t steps = ((p.indices ? k : p.capacity) + STEP * p.split - 1) / (STEP * p.split);
   int cs = 1;
-  while (cs < MAX_CLUSTER && items * cs < resident && int64_t(cs) * 2 * WARPS * STEP <= most) cs *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(uint32_t(items * cs));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = size_t(info.smem);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = uint32_t(cs);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  int64_t least = INT64_MAX;
+  for (int x = 1; x <= MAX_CLUSTER && x <= std::max<int64_t>(1, steps); ++x) {
+    const int64_t cost = (p.items * int64_t(x) + resident - 1) / resident * ((steps + x - 1) / x + CTA_STEPS);
+    if (cost < least) least = cost, cs = x;
+  }
+  // few items of many entries: as many clusters an item as the device holds, while each keeps
+  // PART_STEPS steps a CTA, joined by a second kernel through the workspace
+  p.parts = 1;
+  if (workspace && cs == MAX_CLUSTER) {
+    const int64_t full = resident / (int64_t(p.items) * cs), worth = steps / (int64_t(cs) * PART_STEPS);
+    const int64_t room = int64_t(workspace_bytes) / info.part_bytes / (int64_t(p.items) * jobs);
+    p.parts = int32_t(std::max<int64_t>(1, std::min(full, std::min(worth, room))));
+    p.parts_out = static_cast<float*>(workspace);
+  }
   void* args[] = {&p};
-  return cudaLaunchKernelExC(&cfg, info.kernel, args) == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
+  const void* main_kernel = info.kernel[p.fold > 1];
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  const dim3 grid(uint32_t(units * cs), uint32_t(groups), uint32_t(p.parts));
+  cudaError_t e;
+  if (cs == 1) {
+    e = cudaLaunchKernel(main_kernel, grid, dim3(threads), args, size_t(smem), on);
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = on;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = uint32_t(cs);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelExC(&cfg, main_kernel, args);
+  }
+  if (e == cudaSuccess && p.parts > 1) e = cudaLaunchKernel(info.join, dim3(uint32_t(p.items * jobs)), dim3(JOIN_THREADS), args, 0, on);
+  return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
 }
 
 gvr_status check_attend(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t dtype,
@@ -665,7 +875,8 @@ extern "C" {
 gvr_status attend_decode(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t dtype,
                          int64_t num_rows, int32_t num_heads, const int32_t* block_table, int64_t table_stride,
                          int64_t table_width, const int32_t* kv_lens, int32_t next_n, int32_t compress_ratio,
-                         const int32_t* indices, int64_t k, float scale, void* out, float* lse, void* stream) {
+                         const int32_t* indices, int64_t k, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
   using namespace gvrc;
   const gvr_status s = check_attend(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table,
                                     table_stride, table_width, scale, out, lse);
@@ -673,7 +884,7 @@ gvr_status attend_decode(const gvr_cache* cache, const void* q, int64_t q_row_st
   if (next_n < 1 || next_n > 4096 || compress_ratio < 1 || (indices && (k < 1 || k > kIntMax))) return GVR_ERR_ARG;
   if (num_rows == 0) return GVR_OK;
   if (!kv_lens) return GVR_ERR_NULL;
-  if (!aligned(kv_lens, 4) || !aligned(indices, 4)) return GVR_ERR_ALIGN;
+  if (!aligned(kv_lens, 4) || !aligned(indices, 4) || !aligned(workspace, 16)) return GVR_ERR_ALIGN;
   AttendParams p = {};
   p.q = q;
   p.table = block_table;
@@ -683,14 +894,15 @@ gvr_status attend_decode(const gvr_cache* cache, const void* q, int64_t q_row_st
   p.lse = lse;
   p.next_n = next_n;
   p.ratio = compress_ratio;
-  return attend(cache, p, q_row_stride, q_head_stride, dtype, num_rows, num_heads, table_stride, table_width, k, scale, stream);
+  return attend(cache, p, q_row_stride, q_head_stride, dtype, num_rows, num_heads, table_stride, table_width, k, scale, workspace,
+                workspace_bytes, stream);
 }
 
 gvr_status attend_prefill(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t dtype,
                           int64_t num_rows, int32_t num_heads, const int32_t* block_table, int64_t table_stride,
                           int64_t table_width, int64_t num_requests, const int32_t* row_requests, const int32_t* row_starts,
                           const int32_t* row_ends, const int32_t* indices, int64_t k, float scale, void* out, float* lse,
-                          void* stream) {
+                          void* workspace, size_t workspace_bytes, void* stream) {
   using namespace gvrc;
   const gvr_status s = check_attend(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table,
                                     table_stride, table_width, scale, out, lse);
@@ -698,7 +910,7 @@ gvr_status attend_prefill(const gvr_cache* cache, const void* q, int64_t q_row_s
   if (num_requests < 0 || num_requests > kIntMax || k < 1 || k > kIntMax) return GVR_ERR_ARG;
   if (num_rows == 0) return GVR_OK;
   if (!row_requests || !row_starts || !row_ends || !indices) return GVR_ERR_NULL;
-  if (!aligned(row_requests, 4) || !aligned(row_starts, 4) || !aligned(row_ends, 4) || !aligned(indices, 4)) return GVR_ERR_ALIGN;
+  if (!aligned(row_requests, 4) || !aligned(row_starts, 4) || !aligned(row_ends, 4) || !aligned(indices, 4) || !aligned(workspace, 16)) return GVR_ERR_ALIGN;
   AttendParams p = {};
   p.q = q;
   p.table = block_table;
@@ -711,7 +923,8 @@ gvr_status attend_prefill(const gvr_cache* cache, const void* q, int64_t q_row_s
   p.next_n = 1;
   p.ratio = 1;
   p.num_requests = int32_t(num_requests);
-  return attend(cache, p, q_row_stride, q_head_stride, dtype, num_rows, num_heads, table_stride, table_width, k, scale, stream);
+  return attend(cache, p, q_row_stride, q_head_stride, dtype, num_rows, num_heads, table_stride, table_width, k, scale, workspace,
+                workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -139,9 +139,10 @@ def test_tables_refusals(lib):
 
 
 ATTEND = dict(q=A, qr=512, qh=128, dtype=0, rows=4, heads=4, table=A, stride=8, width=8, indices=A, k=32, scale=0.1, out=A,
-              lse=None, stream=None)
+              lse=None, ws=A, ws_bytes=1 << 20, stream=None)
 BAD_ATTEND = [(dict(q=None), NULL), (dict(out=None), NULL), (dict(table=None), NULL), (dict(q=A + 8), ALIGN),
               (dict(out=A + 2), ALIGN), (dict(lse=A + 2), ALIGN), (dict(table=A + 2), ALIGN), (dict(indices=A + 2), ALIGN),
+              (dict(ws=A + 8), ALIGN),
               (dict(qr=508), STRIDE), (dict(qh=-128), STRIDE), (dict(qh=1 << 33), STRIDE), (dict(stride=7), STRIDE),
               (dict(dtype=7), ARG), (dict(rows=-1), ARG), (dict(heads=3), ARG), (dict(heads=0), ARG), (dict(k=0), ARG),
               (dict(k=1 << 31), ARG), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
@@ -150,7 +151,7 @@ BAD_ATTEND = [(dict(q=None), NULL), (dict(out=None), NULL), (dict(table=None), N
 
 def test_attend_decode_refusals(lib):
     names = ["q", "qr", "qh", "dtype", "rows", "heads", "table", "stride", "width", "lens", "next_n", "cr", "indices", "k",
-             "scale", "out", "lse", "stream"]
+             "scale", "out", "lse", "ws", "ws_bytes", "stream"]
     call = caller(lib.attend_decode, names, dict(ATTEND, lens=A, next_n=2, cr=4))
     for kw, want in BAD_CACHES:
         assert call(cache=kw) == want, kw
@@ -163,7 +164,7 @@ def test_attend_decode_refusals(lib):
 
 def test_attend_prefill_refusals(lib):
     names = ["q", "qr", "qh", "dtype", "rows", "heads", "table", "stride", "width", "requests", "req", "starts", "ends",
-             "indices", "k", "scale", "out", "lse", "stream"]
+             "indices", "k", "scale", "out", "lse", "ws", "ws_bytes", "stream"]
     call = caller(lib.attend_prefill, names, dict(ATTEND, requests=2, req=A, starts=A, ends=A))
     for kw, want in BAD_CACHES:
         assert call(cache=kw) == want, kw
