@@ -58,7 +58,8 @@ typedef struct gvr_cache {
   void* data;           /* device, 16-byte aligned */
   int64_t num_pages;    /* num_pages * page_size < 2^31 */
   int64_t page_stride;  /* bytes between pages: a multiple of 16, at least
-                           page_size * num_kv_heads * row_bytes */
+                           page_size * num_kv_heads * row_bytes; the whole cache may span 2^32
+                           rows, or 64 GB where the stride is not a multiple of row_bytes */
   int32_t page_size;    /* entries per page: a power of two, 1 to GVR_CACHE_MAX_PAGE_SIZE */
   int32_t num_kv_heads; /* >= 1 */
   int32_t head_dim;     /* 64, 128 or 256 */

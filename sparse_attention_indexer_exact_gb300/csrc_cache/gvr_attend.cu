@@ -8,25 +8,24 @@
 //
 // Work split.  A unit is a set of rows that read the same entries: one row, or (whole-cache decode)
 // the next_n rows of a request.  Its queries fall into jobs of one KV head and 8 NT query vectors
-// each.  A CTA takes one to eight jobs of a unit -- as many KV heads and query tiles as fit its
-// warps, so that an entry's rows of neighbouring heads are fetched together, and once -- and where
-// that leaves warps over, SPLIT warps share a job, each taking every SPLIT-th run of 32 entries.
-// A cluster of up to eight CTAs (and, given a workspace, several clusters) divide the entries.
-// Warps join through shared memory, CTAs through distributed shared memory, clusters through the
-// workspace and a second kernel.  Every sum has a fixed order.
+// each.  A warp works on one job, alone: it fetches its own entries and keeps its own running state,
+// without any CTA barrier.  A CTA holds the warps of several jobs, or SPLIT warps a job; a cluster of
+// up to eight CTAs (and, given a workspace, several clusters) divide the entries further.  Warps join
+// through shared memory, CTAs through distributed shared memory, clusters through the workspace and a
+// second kernel.  Every sum has a fixed order.
 //
-// A step.  32 SPLIT entries (codes and scales of K and V, 144 bytes a head at head_dim 128) arrive in
-// a ring of STAGES stages by 16-byte asynchronous copies, STAGES - 1 steps ahead, each warp fetching
-// its share of the entries; one CTA barrier a step.  (Bulk copies of single rows measured slower: 20
-// to 48 clocks each on an SM whatever their size up to 320 bytes.)  The pitch of an entry in shared
-// memory is an odd multiple of 16 bytes, which with tile_entry's order spreads the operand reads over
-// all banks.  S^T = K Q^T and O^T += V^T P^T run on m16n8k16 matrix instructions with entries (for S)
-// and head dimensions (for O) on the 16-row side: these have the 4-bit operand, expanded in registers
-// straight into the instruction's operand layout, so nothing expanded is ever stored.  e2m1 * e4m3
-// has at most 5 significant bits and an exponent within f16's, so K and V are exact in f16.  Queries
-// are brought to f16 exactly, too: a power of two per query puts its largest element at 2^14, and
-// what f16 cannot hold below that is under 2^-39 of it.  P is rounded to f16 (11 bits): eight times
-// finer than bf16 outputs, and averaged over the entries.
+// A step.  32 entries (codes and scales of K and V, 144 bytes at head_dim 128) arrive in the warp's ring
+// of STAGES stages by 16-byte asynchronous copies, STAGES - 1 steps ahead; their numbers and pages are
+// loaded two and one steps before that.  (Bulk copies of single rows measured slower: 20 to 48 clocks
+// each on an SM whatever their size up to 320 bytes.)  The pitch of a row in shared memory is an odd
+// multiple of 16 bytes, which with tile_entry's order spreads the operand reads over all banks.
+// S^T = K Q^T and O^T += V^T P^T run on m16n8k16 matrix instructions with entries (for S) and head
+// dimensions (for O) on the 16-row side: these have the 4-bit operand, expanded in registers straight
+// into the instruction's operand layout, so nothing expanded is ever stored.  e2m1 * e4m3 has at most
+// 5 significant bits and an exponent within f16's, so K and V are exact in f16.  Queries are brought
+// to f16 exactly, too: a power of two per query puts a bf16 query's largest element at 2^14, and what
+// f16 cannot hold below that is under 2^-39 of it.  P is rounded to f16 (11 bits): eight times finer
+// than bf16 outputs, and averaged over the entries.
 #include <algorithm>
 #include <mutex>
 
@@ -38,8 +37,6 @@ namespace {
 
 constexpr int STEP = 32;  // entries a warp takes at a time: one per lane
 constexpr int STAGES = 3;
-constexpr int MAX_TURNS = 3;  // 512-byte pieces of an entry's rows in a CTA: eight heads of 144 bytes, four of 288
-constexpr int MAX_WARPS = 8;
 constexpr int MAX_CLUSTER = 8;
 constexpr int CTA_STEPS = 3;
 constexpr int PART_STEPS = 4;
@@ -57,14 +54,13 @@ struct AttendParams {
   void* out;
   float* lse;
   float* parts_out;  // parts > 1: [item][part][Q * (D + 2)] partial results
-  int64_t page_stride, q_row, q_head, table_stride, num_rows, k;
+  int64_t q_row, q_head, table_stride, num_rows, k;
+  uint32_t unit, page_units, entry_units, row_units;  // bytes of a unit; pages, entries and rows in units
   int32_t num_pages, page_shift, kv_heads, group, fold, capacity, next_n, ratio, num_requests, bf16;
   int32_t tiles;            // query tiles of a KV head in a unit
   int32_t heads_in, tiles_in, split, split_log2;  // a CTA's jobs: heads_in x tiles_in, SPLIT warps each
-  int32_t share;            // entries of a run that each of its warps fetches
   int32_t head_groups, tile_groups;   // CTAs side by side for the jobs of a unit
   int32_t items, parts;     // units x head_groups x tile_groups; clusters of CTAs an item
-  int32_t pitch;            // bytes between entries in shared memory
   float scale_log2;  // |scale| * k_scale * log2(e); 1 for a scale of 0
   float q_sign;      // the scale's sign, which the queries take on (0 for a scale of 0)
   float v_scale;
@@ -141,12 +137,16 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 template <int D, int NT>
 struct Shape {
   static constexpr int RB = row_bytes(D);
+  static constexpr int PITCH = 16 * (RB / 16 | 1);  // of a row in shared memory
   static constexpr int Q = 8 * NT;  // query vectors of a job
+  static constexpr int WARPS = 4, THREADS = 32 * WARPS;
   // accumulators and queries take 3 D / 8 NT registers: that leaves room for 16, 12 or 8 warps on an SM
-  static constexpr int WARPS = D <= 128 && NT == 1 ? 8 : 4;
-  static constexpr int BLOCKS = D * NT == 128 && NT == 2 ? 3 : 2;
-  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 4 : D * NT == 128 ? 3 : 2;
+  static constexpr int STAGE_BYTES = STEP * PITCH;
+  static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
+  static constexpr int PLACES = WARPS * STEP * 4;
   static constexpr int JOIN = (WARPS * Q * D + 4 * WARPS * Q) * int(sizeof(float));
+  static constexpr int SMEM = RING + PLACES > JOIN ? RING + PLACES : JOIN;
 };
 
 // Eight finished values of a head: sums over exp2(score - all) v, their sum `sum`.
@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
   constexpr int KW = D / 32;           // 32-bit words of K codes per lane and entry
   constexpr int VW = D / 64;           // the same of V codes
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint32_t exists[4][MAX_WARPS];  // by step modulo 4 and run: which of its entries are there
 
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in every lane, and known to be
@@ -224,91 +223,63 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
   const int32_t* table = p.table + request * p.table_stride;
   const int32_t* indices = p.indices ? p.indices + int64_t(unit) * p.k : nullptr;
   const int64_t listed = indices ? (n > 0 ? p.k : 0) : n;  // positions to walk over
-  const int stage_entries = STEP * p.split;
-  const int steps = int((listed + stage_entries - 1) >> (5 + p.split_log2));
-  const int walkers = p.parts * int(cs), me = part * int(cs) + int(rank);
+  const int steps = int((listed + STEP - 1) / STEP);
+  const int walkers = p.parts * int(cs) * p.split, me = (part * int(cs) + int(rank)) * p.split + sub;
   const int mine = walkers == 1 ? steps : steps > me ? (steps - me + walkers - 1) / walkers : 0;
 
-  // ---- fetching.  The warps that share run `sub` of the steps (one per job) take turns at working
-  // out where its entries lie, three steps before they are fetched: an entry number, a page, and an
-  // address, a step apart (of step i the warp of job i modulo jobs).  Then each fetches its share of
-  // the run.
-  const int jobs = warps >> p.split_log2;
-  const int stage_bytes = stage_entries * p.pitch;
-  const uint32_t ring = gvr::smem_u32(smem);
-  const uint8_t** places = reinterpret_cast<const uint8_t**>(smem + STAGES * stage_bytes) + sub * STEP;  // [2][stage_entries]
-  const int chunks = p.heads_in * (S::RB / 16);
-  const int share = p.share, first_own = job * share, count = min(share, STEP - first_own);
-  const int lanes_log2 = chunks > 16 ? 5 : chunks > 8 ? 4 : 3, lanes = 1 << lanes_log2;  // that copy one entry together
-  const int per_turn = 32 >> lanes_log2, piece = lane & (lanes - 1), of_turn = lane >> lanes_log2;
-  const int step_stride = walkers * stage_entries;
-
-  auto load_entry = [&](int i) -> int {  // this lane's entry of step i of mine (-1: none)
-    if (i >= mine) return -1;
-    const int64_t pos = int64_t(me) * stage_entries + int64_t(i) * step_stride + sub * STEP + lane;
-    if (pos >= listed) return -1;
-    const int e = indices ? __ldg(indices + pos) : int(pos);
-    return e < n ? e : -1;
+  // ---- fetching
+  uint8_t* ring = smem + warp * STAGES * S::STAGE_BYTES;
+  uint32_t* places = reinterpret_cast<uint32_t*>(smem + S::RING) + warp * STEP;
+  constexpr int CODES = D / 16, SCALES = S::RB / 16 - CODES;  // 16-byte pieces of a row: of codes, of scales
+  const uint32_t stride = walkers * STEP, end = uint32_t(listed);
+  uint32_t pos = me * STEP + lane;  // of the entry that this lane loads next; below 2^32 even behind the last
+  auto load_entry = [&]() -> int {  // -1: none
+    int e = -1;
+    if (pos < end) e = indices ? __ldg(indices + pos) : int(pos);
+    pos += stride;
+    return e;
   };
-  auto load_page = [&](int e) -> int { return e >= 0 ? __ldg(table + (e >> p.page_shift)) : -1; };
-  auto place = [&](int i, int e, int page) {
-    const int64_t off = row_offset(page, p.num_pages, e, p.page_shift, p.page_stride, p.kv_heads, head0, S::RB);
-    const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
-    // a missing entry beside others is fetched from where one of them lies, and not looked at
-    const int64_t some = __shfl_sync(0xffffffffu, off, there ? __ffs(there) - 1 : 0);
-    places[(i & 1) * stage_entries + lane] = p.data + (off < 0 ? some : off);
-    if (lane == 0) exists[i & 3][sub] = there;
-  };
-  bool whole[MAX_TURNS];  // whether this lane has a piece in each 512 bytes of an entry's rows
-#pragma unroll
-  for (int x = 0; x < MAX_TURNS; ++x) whole[x] = piece + 32 * x < chunks;
-  auto fetch = [&](int i, uint32_t stage_at) {
-    if (i < mine && exists[i & 3][sub]) {
-      const uint8_t** from = places + (i & 1) * stage_entries + first_own;
-      uint32_t dst = stage_at + (sub * STEP + first_own) * p.pitch + piece * 16;
-      if (lanes == 32) {
-#pragma unroll 4
-        for (int j = 0; j < count; ++j) {
-          const uint8_t* at = from[j] + piece * 16;
-#pragma unroll
-          for (int x = 0; x < MAX_TURNS; ++x)
-            if (whole[x]) copy16(dst + 512 * x, at + 512 * x);
-          dst += p.pitch;
-        }
-      } else {
-        dst += of_turn * p.pitch;
-#pragma unroll 4
-        for (int j = of_turn; j < count; j += per_turn) {
-          if (whole[0]) copy16(dst, from[j] + piece * 16);
-          dst += per_turn * p.pitch;
-        }
+  auto load_page = [&](int e) -> int { return uint32_t(e) < uint32_t(n) ? __ldg(table + (e >> p.page_shift)) : -1; };
+  // CODES neighbouring lanes copy a row's codes, every lane a row's scales
+  const uint8_t* codes_from = p.data + lane % CODES * 16;
+  const uint32_t codes_to = lane / CODES * S::PITCH + lane % CODES * 16, scales_to = lane * S::PITCH + D;
+  const uint32_t head_units = h * p.row_units;
+  // Starts the copies of a step; returns which lanes' entries exist.
+  auto fetch = [&](uint32_t to, int e, int page) -> uint32_t {
+    const bool is = uint32_t(page) < uint32_t(p.num_pages);
+    const uint32_t there = __ballot_sync(0xffffffffu, is);
+    if (there) {
+      uint32_t from = row_unit(page, e, p.page_shift, p.page_units, p.entry_units, head_units);
+      if (there != 0xffffffffu) {  // a missing entry is fetched from where another lies, and not looked at
+        const uint32_t some = __shfl_sync(0xffffffffu, from, __ffs(there) - 1);
+        if (!is) from = some;
       }
+      places[lane] = from;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < CODES; ++j)
+        copy16(to + codes_to + j * (32 / CODES) * S::PITCH, codes_from + uint64_t(places[j * (32 / CODES) + lane / CODES]) * p.unit);
+#pragma unroll
+      for (int j = 0; j < SCALES; ++j) copy16(to + scales_to + j * 16, p.data + uint64_t(from) * p.unit + D + j * 16);
     }
     copy_commit();
+    return there;
   };
-  // The next of the own steps (job, job + jobs, ...) to place, to load pages and entries of.
-  int to_place = job, to_page = 0, to_enter = 0, e_next = -1, e_page = -1, page = -1;
+  const uint32_t ring_at = gvr::smem_u32(ring);
+  uint32_t masks[STAGES];  // of the steps under way
+  int e_ahead, e_after, page_ahead;
   {
-    int e[5], pg[4];
-    uint32_t own = 0;  // which of the first five steps
-    for (int j = job; j < 5; j += jobs) own |= 1u << j;
+    int e[STAGES + 1], pg[STAGES];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) e[i] = (own >> i) & 1 ? load_entry(i) : -1;
+    for (int i = 0; i < STAGES + 1; ++i) e[i] = load_entry();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pg[i] = load_page(e[i]);
+    for (int i = 0; i < STAGES; ++i) pg[i] = load_page(e[i]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if ((own >> i) & 1) place(i, e[i], pg[i]);
-    __syncthreads();
-    fetch(0, ring);
-    fetch(1, ring + stage_bytes);
-    __syncthreads();
-    if ((own >> 2) & 1) place(2, e[2], pg[2]);
-    if ((own >> 3) & 1) e_page = e[3], page = pg[3];
-    if ((own >> 4) & 1) e_next = e[4];
-    while (to_place < 3) to_place += jobs;
-    for (to_page = to_place; to_page < 4;) to_page += jobs;
-    for (to_enter = to_page; to_enter < 5;) to_enter += jobs;
+    for (int i = 0; i < STAGES - 1; ++i) {
+      masks[i] = fetch(ring_at + i * S::STAGE_BYTES, e[i], pg[i]);
+      __syncwarp();
+    }
+    e_ahead = e[STAGES - 1], page_ahead = pg[STAGES - 1], e_after = e[STAGES];
   }
 
   // ---- the queries as operands
@@ -361,31 +332,31 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
   }
   // where this lane's operand rows start in a stage: of K, tile rows g and g + 8 (the next entry); of V,
   // columns 2 c and 2 c + 1 (and 8 behind them, the next entries)
-  const int run = sub * STEP * p.pitch + (h - head0) * S::RB;
-  const int k_at = run + tile_entry(g) * p.pitch;
-  const int v_at0 = run + tile_entry(2 * c) * p.pitch, v_at1 = run + tile_entry(2 * c + 1) * p.pitch;
-  int now = 0, before = (STAGES - 1) * stage_bytes;  // bytes of this step's stage and of the one before
+  const int k_at = tile_entry(g) * S::PITCH;
+  const int v_at0 = tile_entry(2 * c) * S::PITCH, v_at1 = tile_entry(2 * c + 1) * S::PITCH;
+  int now = 0;  // this step's stage in bytes
   for (int i = 0; i < mine; ++i) {
     {
       copy_wait<STAGES - 2>();
-      __syncthreads();  // the step's entries are here, and the stage before it is free
-      fetch(i + STAGES - 1, ring + before);
-      if (i + 3 == to_place) place(i + 3, e_page, page), to_place += jobs;
-      if (i + 4 == to_page) e_page = e_next, page = load_page(e_next), to_page += jobs;
-      if (i + 5 == to_enter) e_next = load_entry(i + 5), to_enter += jobs;
+      __syncwarp();  // the step's entries are here, and every lane is done with the stage before it
+      masks[STAGES - 1] = fetch(ring_at + (now == 0 ? (STAGES - 1) * S::STAGE_BYTES : now - S::STAGE_BYTES), e_ahead, page_ahead);
+      e_ahead = e_after;
+      page_ahead = load_page(e_ahead);
+      e_after = load_entry();
 
-      const uint8_t* st = smem + now;
-      before = now;
-      now = now == (STAGES - 1) * stage_bytes ? 0 : now + stage_bytes;
-      const uint32_t mask = exists[i & 3][sub];
+      const uint8_t* st = ring + now;
+      const uint32_t mask = masks[0];
+      now = now == (STAGES - 1) * S::STAGE_BYTES ? 0 : now + S::STAGE_BYTES;
+#pragma unroll
+      for (int j = 0; j < STAGES - 1; ++j) masks[j] = masks[j + 1];
       if (mask == 0) continue;
 
       // S^T: two tiles of 16 entries
       float s[2][NT][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-        const uint8_t* r0 = st + k_at + 16 * mt * p.pitch;
-        const uint8_t* r1 = r0 + p.pitch;
+        const uint8_t* r0 = st + k_at + 16 * mt * S::PITCH;
+        const uint8_t* r1 = r0 + S::PITCH;
         uint32_t k0[KW], k1[KW];
         load_words<KW>(r0 + c * (D / 8), k0);
         load_words<KW>(r1 + c * (D / 8), k1);
@@ -417,7 +388,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
 
       // entries that are skipped or beyond a query's limit leave the sums
       // entries that only some rows of the unit see (at most at its end)
-      const int64_t first = int64_t(me) * stage_entries + int64_t(i) * step_stride + sub * STEP;
+      const int64_t first = int64_t(me + i * walkers) * STEP;
       const bool border = FOLD && first + STEP > sure;
       if (mask != 0xffffffffu || border) {
 #pragma unroll
@@ -502,7 +473,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
           uint32_t v[4][VW], vs[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const uint8_t* r = st + (x & 1 ? v_at1 : v_at0) + (16 * mt + (x >> 1)) * p.pitch;
+            const uint8_t* r = st + (x & 1 ? v_at1 : v_at0) + (16 * mt + (x >> 1)) * S::PITCH;
             load_words<VW>(r + D / 2 + g * (D / 16), v[x]);
             if (D == 64) vs[x] = r[D + D / 16 + (g >> 1)];
             else if (D == 128) vs[x] = r[D + D / 16 + g];
@@ -554,7 +525,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
       v += __shfl_xor_sync(0xffffffffu, v, 16);
       total[t][j] = v;
     }
-  if (p.split == 1 && walkers == 1) {  // the warp has its job's whole sums: lane (g, c) writes D/8 values
+  const int jobs = warps >> p.split_log2;
+  if (walkers == 1) {  // the warp has its job's whole sums: lane (g, c) writes D/8 values
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -697,7 +669,7 @@ struct KernelInfo {
   const void* join;
   int queries, warps;
   int part_bytes;  // of one job's results
-  int join_bytes;  // shared memory of a CTA's join
+  int smem;
 };
 
 template <int D, int NT>
@@ -705,7 +677,7 @@ KernelInfo info() {
   using S = Shape<D, NT>;
   return {{reinterpret_cast<const void*>(attend_kernel<D, NT, false>), reinterpret_cast<const void*>(attend_kernel<D, NT, true>)},
           reinterpret_cast<const void*>(join_kernel<D, NT>), S::Q,
-          S::WARPS, S::Q * (D + 2) * int(sizeof(float)), S::JOIN};
+          S::WARPS, S::Q * (D + 2) * int(sizeof(float)), S::SMEM};
 }
 
 constexpr int KERNELS = 6;
@@ -763,7 +735,11 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
                   void* workspace, size_t workspace_bytes, void* stream) {
   const int group = num_heads / cache->num_kv_heads;
   p.data = static_cast<const uint8_t*>(cache->data);
-  p.page_stride = cache->page_stride;
+  const int row = row_bytes(cache->head_dim);
+  p.unit = unit_bytes(cache->page_stride, row);
+  p.page_units = uint32_t(cache->page_stride / p.unit);
+  p.row_units = row / p.unit;
+  p.entry_units = p.row_units * cache->num_kv_heads;
   p.q_row = q_row_stride;
   p.q_head = q_head_stride;
   p.table_stride = table_stride;
@@ -795,11 +771,7 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
   const int jobs = p.heads_in * p.tiles_in;
   p.split_log2 = jobs > info.warps / 2 ? 0 : jobs > info.warps / 4 ? 1 : jobs > info.warps / 8 ? 2 : 3;  // a power of two
   p.split = 1 << p.split_log2;
-  p.share = (STEP + jobs - 1) / jobs;
-  const int threads = 32 * jobs * p.split;
-  const int chunks = p.heads_in * (row_bytes(cache->head_dim) / 16);
-  p.pitch = 16 * (chunks | 1);
-  const int smem = std::max(STEP * p.split * (STAGES * p.pitch + 2 * int(sizeof(int64_t))), info.join_bytes);
+  const int threads = 32 * jobs * p.split, smem = info.smem;
   const int64_t units = (num_rows + p.fold - 1) / p.fold;
   const int64_t groups = int64_t(p.tile_groups) * p.head_groups;
   if (groups > 65535 || units > kIntMax / groups / MAX_CLUSTER) return GVR_ERR_ARG;
@@ -809,7 +781,7 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
   const int64_t resident = int64_t(d->sms) * std::max(1, std::min(d->ctas_by_registers[kernel][p.fold > 1], d->smem_per_sm / (smem + 256 + d->smem_reserved)));
   // CTAs per item: the cluster size with the fewest rounds of steps, counting a CTA's start and end
   // as CTA_STEPS steps
-  const int64_t steps = ((p.indices ? k : p.capacity) + STEP * p.split - 1) / (STEP * p.split);
+  const int64_t steps = ((p.indices ? k : p.capacity) + STEP * p.split - 1) / (STEP * p.split);  // of a warp
   int cs = 1;
   int64_t least = INT64_MAX;
   for (int x = 1; x <= MAX_CLUSTER && x <= std::max<int64_t>(1, steps); ++x) {

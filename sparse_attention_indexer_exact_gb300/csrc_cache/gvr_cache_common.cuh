@@ -39,6 +39,7 @@ inline gvr_status check_cache(const gvr_cache* c) {
     return GVR_ERR_STRIDE;
   // an address is page * page_stride + ... in 64 bits
   if (c->num_pages > 0 && c->page_stride > INT64_MAX / 2 / c->num_pages) return GVR_ERR_STRIDE;
+  if (!units_fit(c->num_pages, c->page_stride, row_bytes(c->head_dim))) return GVR_ERR_STRIDE;
   if (c->num_pages > 0 && !c->data) return GVR_ERR_NULL;
   if (!aligned(c->data, 16)) return GVR_ERR_ALIGN;
   return GVR_OK;

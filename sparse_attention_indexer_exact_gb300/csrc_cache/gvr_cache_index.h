@@ -35,6 +35,19 @@ GVRC_FN int64_t slot_offset(int slot, int num_pages, int page_shift, int64_t pag
   return row_offset(slot >> page_shift, num_pages, slot, page_shift, page_stride, heads, head, bytes);
 }
 
+// Number of an entry's row in units of `unit` bytes, given the page stride, the rows of one entry and
+// the head's row in the same units; the caller has checked `page`.  Fits 32 bits (units_fit).
+GVRC_FN uint32_t row_unit(int page, int entry, int page_shift, uint32_t page_units, uint32_t entry_units, uint32_t head_units) {
+  return uint32_t(page) * page_units + uint32_t(entry & ((1 << page_shift) - 1)) * entry_units + head_units;
+}
+
+// The unit: a row where the page stride is a multiple of it (caches of up to 2^32 rows, 320 GB and
+// more), else 16 bytes (up to 64 GB).
+GVRC_FN int unit_bytes(int64_t page_stride, int bytes) { return page_stride % bytes == 0 ? bytes : 16; }
+GVRC_FN bool units_fit(int64_t num_pages, int64_t page_stride, int bytes) {
+  return num_pages == 0 || page_stride / unit_bytes(page_stride, bytes) <= 4294967295ll / num_pages;
+}
+
 // Slot of an entry on `page`; -1 where there is no page or the slot would not fit 31 bits.
 GVRC_FN int slot_of(int page, int entry, int page_shift) {
   if (page < 0) return -1;

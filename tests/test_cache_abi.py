@@ -76,6 +76,7 @@ def struct(**kw):
 BAD_CACHES = [(dict(data=None), NULL), (dict(data=A + 8), ALIGN), (dict(num_pages=-1), ARG),
               (dict(num_pages=1 << 27), ARG), (dict(page_stride=16 * 2 * 144 - 16), STRIDE),
               (dict(page_stride=16 * 2 * 144 + 8), STRIDE), (dict(page_stride=1 << 62), STRIDE),
+              (dict(page_stride=1 << 33, num_pages=8), STRIDE), (dict(page_stride=144 << 25, num_pages=200), STRIDE),
               (dict(page_size=0), ARG), (dict(page_size=24), ARG), (dict(page_size=-16), ARG),
               (dict(page_size=8192, page_stride=8192 * 2 * 144), ARG), (dict(num_kv_heads=0), ARG), (dict(head_dim=96), ARG),
               (dict(reserved=1), ARG), (dict(k_scale=0.0), ARG), (dict(v_scale=-1.0), ARG),
@@ -207,6 +208,8 @@ int main() {
     if (f == 'w') r = window_entries(a[0], a[1], a[2]);
     if (f == 'p') r = pages_of(a[0], a[1]);
     if (f == 'b') r = row_bytes(a[0]);
+    if (f == 'u') r = row_unit(a[0], a[1], a[2], a[3], a[4], a[5]);
+    if (f == 'f') r = units_fit(a[0], a[1], a[2]) ? unit_bytes(a[1], a[2]) : 0;
     std::printf("%lld\n", r);
   }
 }
@@ -251,6 +254,19 @@ def test_index_arithmetic_on_the_host(tmp_path):
                 ask("o", (page, entry, shift), s if page >= 0 and s < top else -1)
         for n in (0, 1, ps, ps + 1, top):
             ask("p", (n, shift), -(-n // ps))
+    # attention's 32-bit units: the same places as the 64-bit offsets, up to the largest cache that fits
+    for shift, heads, row, gap in ((0, 1, 80, 0), (4, 8, 144, 0), (12, 3, 288, 0), (6, 2, 144, 16), (4, 8, 80, 48)):
+        stride = (1 << shift) * heads * row + gap
+        unit = row if stride % row == 0 else 16
+        most = min((2 ** 32 - 1) // (stride // unit), top >> shift)
+        for pages, fits in ((0, 1), (1, 1), (most, 1), ((2 ** 32 - 1) // (stride // unit) + 1, 0)):
+            ask("f", (pages, stride, row), unit if fits else 0)
+        for page in (0, 1, most - 1):
+            for entry in (0, (1 << shift) - 1, 5 * (1 << shift), top):
+                for head in (0, heads - 1):
+                    at = page * stride + ((entry % (1 << shift)) * heads + head) * row
+                    assert at % unit == 0 and at // unit < 2 ** 32
+                    ask("u", (page, entry, shift, stride // unit, row // unit * heads, head * row // unit), at // unit)
     for kv in (-3, 0, 1, 2, 3, 4, 100, top):
         for next_n in (1, 2, 4096):
             for j in (0, next_n - 1):
