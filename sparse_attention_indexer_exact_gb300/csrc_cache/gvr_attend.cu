@@ -38,6 +38,7 @@ namespace {
 constexpr int STEP = 32;  // entries a warp takes at a time: one per lane
 constexpr int STAGES = 3;
 constexpr int MAX_CLUSTER = 8;
+constexpr float NO_TOP = -3.4028235e38f;  // the maximum of no scores: finite, so that differences are
 constexpr int CTA_STEPS = 3;
 constexpr int PART_STEPS = 4;
 constexpr int JOIN_THREADS = 128;
@@ -118,6 +119,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// Both halves of an f16x2 from its low or high one.
+__device__ __forceinline__ uint32_t splat(uint32_t two, int high) {
+  const __half2 v = *reinterpret_cast<const __half2*>(&two);
+  const __half2 r = high ? __high2half2(v) : __low2half2(v);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if (N == 1) {
@@ -139,9 +147,9 @@ struct Shape {
   static constexpr int RB = row_bytes(D);
   static constexpr int PITCH = 16 * (RB / 16 | 1);  // of a row in shared memory
   static constexpr int Q = 8 * NT;  // query vectors of a job
-  static constexpr int WARPS = 4, THREADS = 32 * WARPS;
+  static constexpr int WARPS = D <= 128 && NT == 1 ? 8 : 4, THREADS = 32 * WARPS;
   // accumulators and queries take 3 D / 8 NT registers: that leaves room for 16, 12 or 8 warps on an SM
-  static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 4 : D * NT == 128 ? 3 : 2;
+  static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 2 : D * NT == 128 ? 3 : 2;
   static constexpr int STAGE_BYTES = STEP * PITCH;
   static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
   static constexpr int PLACES = WARPS * STEP * 4;
@@ -231,7 +239,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
   uint8_t* ring = smem + warp * STAGES * S::STAGE_BYTES;
   uint32_t* places = reinterpret_cast<uint32_t*>(smem + S::RING) + warp * STEP;
   constexpr int CODES = D / 16, SCALES = S::RB / 16 - CODES;  // 16-byte pieces of a row: of codes, of scales
-  const uint32_t stride = walkers * STEP, end = uint32_t(listed);
+  // (listed entries are loaded whatever the row's length, which may still be on its way)
+  const uint32_t stride = walkers * STEP, end = indices ? uint32_t(p.k) : uint32_t(n);
   uint32_t pos = me * STEP + lane;  // of the entry that this lane loads next; below 2^32 even behind the last
   auto load_entry = [&]() -> int {  // -1: none
     int e = -1;
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
     for (int i = 0; i < KSTEPS; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
-    top[t][0] = top[t][1] = -INFINITY;
+    top[t][0] = top[t][1] = NO_TOP;
     total[t][0] = total[t][1] = 0.f;
   }
   // where this lane's operand rows start in a stage: of K, tile rows g and g + 8 (the next entry); of V,
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
           e2m1_to_f16x2(k1[w], b);
           const int block = w / 2;  // 16 values a scale
           const uint32_t two0 = e4m3x2_to_f16x2(sc0 >> (16 * (block / 2))), two1 = e4m3x2_to_f16x2(sc1 >> (16 * (block / 2)));
-          const uint32_t x0 = __byte_perm(two0, two0, block & 1 ? 0x3232 : 0x1010), x1 = __byte_perm(two1, two1, block & 1 ? 0x3232 : 0x1010);
+          const uint32_t x0 = splat(two0, block & 1), x1 = splat(two1, block & 1);
 #pragma unroll
           for (int j = 0; j < 4; ++j) a[j] = hmul2(a[j], x0), b[j] = hmul2(b[j], x1);
 #pragma unroll
@@ -403,18 +412,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
           }
       }
 
-      // running maximum: kept while the step's maximum is at most 2^8 above it (P stays within f16)
+      // The base that scores are taken against: the maximum when it was last set, kept while no score is
+      // more than 2^8 above it (P stays within f16).
       bool grow = false;
-      float high[NT][2];
+      float high[NT][2];  // of this lane's scores, in log2 units; factors are positive
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float v = fmaxf(fmaxf(s[0][t][j], s[0][t][j + 2]), fmaxf(s[1][t][j], s[1][t][j + 2]));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          high[t][j] = v * factor[t][j];  // in log2 units; factors are positive
+          high[t][j] = fmaxf(fmaxf(s[0][t][j], s[0][t][j + 2]), fmaxf(s[1][t][j], s[1][t][j + 2])) * factor[t][j];
           grow |= high[t][j] > top[t][j] + 8.f;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -423,8 +429,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
           float down[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float next = fmaxf(top[t][j], high[t][j]);
-            down[j] = top[t][j] == -INFINITY ? 0.f : exp2_fast(top[t][j] - next);
+            float next = fmaxf(top[t][j], high[t][j]);
+            next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 4));
+            next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 8));
+            next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 16));
+            down[j] = exp2_fast(top[t][j] - next);
             top[t][j] = next;
             total[t][j] *= down[j];
           }
@@ -438,11 +447,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
       uint32_t pb[2][NT][2];  // P^T as operands
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float base0 = top[t][0] == -INFINITY ? 0.f : top[t][0], base1 = top[t][1] == -INFINITY ? 0.f : top[t][1];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const float e0 = exp2_fast(fmaf(s[mt][t][0], factor[t][0], -base0)), e1 = exp2_fast(fmaf(s[mt][t][1], factor[t][1], -base1));
-          const float e2 = exp2_fast(fmaf(s[mt][t][2], factor[t][0], -base0)), e3 = exp2_fast(fmaf(s[mt][t][3], factor[t][1], -base1));
+          const float e0 = exp2_fast(fmaf(s[mt][t][0], factor[t][0], -top[t][0])), e1 = exp2_fast(fmaf(s[mt][t][1], factor[t][1], -top[t][1]));
+          const float e2 = exp2_fast(fmaf(s[mt][t][2], factor[t][0], -top[t][0])), e3 = exp2_fast(fmaf(s[mt][t][3], factor[t][1], -top[t][1]));
           total[t][0] += e0 + e2;
           total[t][1] += e1 + e3;
           pb[mt][t][0] = transpose8x8(pack_f16(e0, e1));
@@ -565,9 +573,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int qi = 8 * t + 2 * c + j;
-      float all = -INFINITY;
+      float all = NO_TOP;
       for (int w = job * p.split; w < (job + 1) * p.split; ++w) all = fmaxf(all, tops[w * S::Q + qi]);
-      const float down = top[t][j] == -INFINITY ? 1.f : exp2_fast(top[t][j] - all);
+      const float down = exp2_fast(top[t][j] - all);
       float* dst = partial + (warp * S::Q + qi) * D + g * (D / 8);
 #pragma unroll
       for (int x = 0; x < KSTEPS; ++x)
@@ -576,7 +584,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
         float sum = 0.f;
         for (int w = job * p.split; w < (job + 1) * p.split; ++w) {
           const float tw = tops[w * S::Q + qi];
-          sum += sums[w * S::Q + qi] * (tw == -INFINITY ? 1.f : exp2_fast(tw - all));
+          sum += sums[w * S::Q + qi] * exp2_fast(tw - all);
         }
         joined[job * 2 * S::Q + qi] = all;
         joined[job * 2 * S::Q + S::Q + qi] = sum;
@@ -607,13 +615,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
     if (m >= p.fold * p.group || row >= p.num_rows) continue;
     const uint32_t top_at = joined_addr + (jb * 2 * S::Q + qi) * 4, sum_at = top_at + S::Q * 4;
     const uint32_t at = partial_addr + (jb * p.split * S::Q * D + qi * D + d) * 4;
-    float all = -INFINITY, sum = 0.f, acc[8];
+    float all = NO_TOP, sum = 0.f, acc[8];
 #pragma unroll
     for (int y = 0; y < 8; ++y) acc[y] = 0.f;
     for (uint32_t r = 0; r < cs; ++r) all = fmaxf(all, __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(top_at, r))));
     for (uint32_t r = 0; r < cs; ++r) {
       const float tr = __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(top_at, r)));
-      const float down = tr == -INFINITY ? 1.f : exp2_fast(tr - all);
+      const float down = exp2_fast(tr - all);
       sum += down * __uint_as_float(gvr::dsmem_ld_u32(gvr::dsmem_map(sum_at, r)));
       const float4 a = dsmem_ld_f32x4(gvr::dsmem_map(at, r)), b = dsmem_ld_f32x4(gvr::dsmem_map(at + 16, r));
       acc[0] += down * a.x, acc[1] += down * a.y, acc[2] += down * a.z, acc[3] += down * a.w;
@@ -647,13 +655,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(AttendParams p) {
     const int qi = i / EIGHTS, d = (i % EIGHTS) * 8, m = tile * S::Q + qi;
     const int64_t row = unit * p.fold + m / p.group;
     if (m >= p.fold * p.group || row >= p.num_rows) continue;
-    float all = -INFINITY, sum = 0.f, acc[8];
+    float all = NO_TOP, sum = 0.f, acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     for (int r = 0; r < p.parts; ++r) all = fmaxf(all, src[int64_t(r) * (S::Q * (D + 2)) + S::Q * D + qi]);
     for (int r = 0; r < p.parts; ++r) {
       const float* from = src + int64_t(r) * (S::Q * (D + 2));
-      const float tr = from[S::Q * D + qi], down = tr == -INFINITY ? 1.f : exp2_fast(tr - all);
+      const float tr = from[S::Q * D + qi], down = exp2_fast(tr - all);
       sum += down * from[S::Q * (D + 1) + qi];
       const float4 a = *reinterpret_cast<const float4*>(from + qi * D + d), b = *reinterpret_cast<const float4*>(from + qi * D + d + 4);
       acc[0] += down * a.x, acc[1] += down * a.y, acc[2] += down * a.z, acc[3] += down * a.w;
@@ -763,13 +771,14 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
   // a CTA's jobs: all query tiles of a KV head as far as its warps go, then neighbouring KV heads
   // (a divisor of their number), then several warps a job
   p.tiles = int32_t((members + info.queries - 1) / info.queries);
-  p.tile_groups = (p.tiles + info.warps - 1) / info.warps;
+  const int warps = info.warps;
+  p.tile_groups = (p.tiles + warps - 1) / warps;
   p.tiles_in = (p.tiles + p.tile_groups - 1) / p.tile_groups;
-  p.heads_in = info.warps / p.tiles_in;
+  p.heads_in = warps / p.tiles_in;
   while (p.kv_heads % p.heads_in) --p.heads_in;
   p.head_groups = p.kv_heads / p.heads_in;
   const int jobs = p.heads_in * p.tiles_in;
-  p.split_log2 = jobs > info.warps / 2 ? 0 : jobs > info.warps / 4 ? 1 : jobs > info.warps / 8 ? 2 : 3;  // a power of two
+  p.split_log2 = jobs > warps / 2 ? 0 : jobs > warps / 4 ? 1 : jobs > warps / 8 ? 2 : 3;  // a power of two
   p.split = 1 << p.split_log2;
   const int threads = 32 * jobs * p.split, smem = info.smem;
   const int64_t units = (num_rows + p.fold - 1) / p.fold;
