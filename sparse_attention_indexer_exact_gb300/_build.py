@@ -5,12 +5,16 @@
 beside this file; it rebuilds only when a source is newer than the library.  No
 CMake, no torch extension machinery: the library is a plain shared object with
 an ``extern "C"`` interface (``include/gvr_topk.h``, ``include/gvr_cache.h``).
+Beside it g++ builds ``_native.so`` (``_native.cpp``), the short way from torch
+tensors to the cache's calls, against the installed torch and the library.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
+import sysconfig
 import tempfile
 import threading
 from concurrent.futures import ThreadPoolExecutor
@@ -21,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 CSRC_CACHE = os.path.join(PKG, "csrc_cache")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgvrtopk.so")
+NATIVE_SOURCE = os.path.join(PKG, "_native.cpp")
+NATIVE_PATH = os.path.join(PKG, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()
 
@@ -58,22 +64,52 @@ def _run(cmd: list[str]) -> str:
     return r.stdout + r.stderr
 
 
-def stale(out: str = LIB_PATH) -> bool:
+def _torch_root() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch is needed to build _native.so")
+    return list(spec.submodule_search_locations)[0]
+
+
+def native_commands(obj: str, out: str = NATIVE_PATH) -> tuple[list[str], list[str]]:
+    """Compiling and linking the tensor binding (the link needs libgvrtopk.so)."""
+    torch = _torch_root()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include") if os.path.isabs(nvcc_path()) else \
+        "/usr/local/cuda/include"
+    include = [os.path.join(torch, "include"), sysconfig.get_paths()["include"], cuda, INCLUDE]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[x for d in include for x in ("-I", d)], "-c",
+                NATIVE_SOURCE, "-o", obj]
+    link = ["g++", "-shared", obj, "-o", out, "-L", PKG, "-l:libgvrtopk.so", "-L", os.path.join(torch, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
+def stale(out: str = LIB_PATH, of: list[str] | None = None) -> bool:
     if not os.path.exists(out):
         return True
     t = os.path.getmtime(out)
-    return any(os.path.getmtime(s) > t for s in sources())
+    return any(os.path.getmtime(s) > t for s in (of or sources()))
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile libgvrtopk.so for sm_103a if it is missing or older than its sources."""
+    """Compile libgvrtopk.so for sm_103a, and _native.so, where missing or older than their sources."""
     with _lock:
-        if force or stale():
+        library = force or stale()
+        native = force or library or stale(NATIVE_PATH, [NATIVE_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+        if library or native:
             extra = ["-Xptxas", "-v"] if verbose else []
             with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor() as pool:
-                jobs = [(u, os.path.join(tmp, os.path.basename(u) + ".o")) for u in units()]
-                said = list(pool.map(lambda j: _run(compile_command(*j, extra)), jobs))
-                said.append(_run(link_command([o for _, o in jobs])))
+                jobs = [(u, os.path.join(tmp, os.path.basename(u) + ".o")) for u in units()] if library else []
+                obj = os.path.join(tmp, "native.o")
+                commands = [compile_command(*j, extra) for j in jobs]
+                if native:
+                    native_compile, native_link = native_commands(obj)
+                    commands.append(native_compile)
+                said = list(pool.map(_run, commands))
+                if library:
+                    said.append(_run(link_command([o for _, o in jobs])))
+                if native:
+                    said.append(_run(native_link))
             if verbose:
                 print("".join(said))
     return LIB_PATH

@@ -16,7 +16,6 @@ layout of a row, the quantiser and what every call does at its borders.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 
 __all__ = ["cache_alloc", "cache_row_bytes", "cache_tables", "cache_append", "cache_read", "attend_decode",
@@ -87,20 +86,33 @@ def _launch(device: int, call, *args):
         _check(_library(), status)
 
 
-def _on_stream(call):
-    """``call`` with a ``stream`` argument: a torch stream or a handle, made current around the call, so
-    that what the call allocates belongs to the stream that uses it."""
-    @functools.wraps(call)
-    def wrapped(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        import torch
-        if not isinstance(stream, torch.cuda.Stream):
-            device = next((a.device for a in args if isinstance(a, torch.Tensor)), None)
-            stream = torch.cuda.ExternalStream(stream, device)
-        with torch.cuda.stream(stream):
-            return call(*args, **kw)
-    return wrapped
+def _current(stream, tensor):
+    """Context in which ``stream`` (a torch stream or a handle) is the current one: what a call
+    allocates then belongs to the stream that uses it."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, tensor.device)
+    return torch.cuda.stream(stream)
+
+
+# The short way (_native.cpp): the same calls with the tensors read natively.  Its functions return
+# None wherever anything is out of the ordinary, and the call then goes step by step through the
+# checks below, which say what is wrong.
+_native = None
+
+
+def _short():
+    global _native
+    if _native is None:
+        _library()
+        try:
+            import torch  # noqa: F401 - its libraries have to be there first
+            from . import _native as native
+        except ImportError as e:
+            raise RuntimeError("_native.so is missing or does not fit this torch: build it with "
+                               "`python -m sparse_attention_indexer_exact_gb300._build`") from e
+        _native = native
+    return _native
 
 
 # The checks of one tensor: its device's number, or an error that names it.
@@ -197,9 +209,8 @@ def cache_alloc(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int
     return torch.zeros((num_pages, page_size, num_kv_heads, cache_row_bytes(head_dim)), dtype=torch.uint8, device=device)
 
 
-@_on_stream
 def cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new: int, page_size: int, compress_ratio: int = 1,
-                 slots=None, counts=None):
+                 slots=None, counts=None, *, stream=None):
     """Give each request the pages that its new entries need, and map those entries to slots.
 
     ``cached_lens`` and ``kv_lens`` (int32 [requests]) are each request's uncompressed length before
@@ -208,6 +219,13 @@ def cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new: int, pa
     order, -1 behind them and where no page was left) and ``counts`` (int32 [3]: new entries, pages
     taken, pages missing).
     """
+    if stream is not None:
+        with _current(stream, kv_lens):
+            return cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new, page_size, compress_ratio, slots, counts)
+    done = (_native or _short()).cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new, page_size,
+                                              compress_ratio, slots, counts)
+    if done is not None:
+        return done
     import torch
     device = _device(kv_lens, "kv_lens")
     requests = kv_lens.shape[0] if kv_lens.dim() == 1 else 0
@@ -230,10 +248,14 @@ def cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new: int, pa
     return slots, counts
 
 
-@_on_stream
-def cache_append(k, v, cache, slots, *, k_scale: float = 1.0, v_scale: float = 1.0) -> None:
+def cache_append(k, v, cache, slots, *, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Quantise ``k`` and ``v`` [tokens, kv_heads, head_dim] (bfloat16 or float16, strides in multiples
     of 8) into ``cache`` at ``slots`` (int32 [tokens]; -1 skips the token)."""
+    if stream is not None:
+        with _current(stream, cache):
+            return cache_append(k, v, cache, slots, k_scale=k_scale, v_scale=v_scale)
+    if (_native or _short()).cache_append(k, v, cache, slots, k_scale, v_scale):
+        return
     c = _cache_struct(cache, k_scale, v_scale)
     device = cache.get_device()
     _on(k, device, "k")
@@ -251,11 +273,17 @@ def cache_append(k, v, cache, slots, *, k_scale: float = 1.0, v_scale: float = 1
             at, tokens)
 
 
-@_on_stream
-def cache_read(cache, slots, head_dim: int, dtype=None, *, k_scale: float = 1.0, v_scale: float = 1.0):
+def cache_read(cache, slots, head_dim: int, dtype=None, *, k_scale: float = 1.0, v_scale: float = 1.0, stream=None):
     """The values held at ``slots`` (int32 [n]): K and V, each [n, kv_heads, head_dim] of ``dtype``
     (bfloat16 by default, or float16); zeros for a slot that names no entry."""
     import torch
+    if stream is not None:
+        with _current(stream, cache):
+            return cache_read(cache, slots, head_dim, dtype, k_scale=k_scale, v_scale=v_scale)
+    kind = 0 if dtype is None or dtype == torch.bfloat16 else 1 if dtype == torch.float16 else -1
+    done = (_native or _short()).cache_read(cache, slots, head_dim, kind, k_scale, v_scale)
+    if done is not None:
+        return done
     c = _cache_struct(cache, k_scale, v_scale)
     device = cache.get_device()
     if c.head_dim != head_dim:
@@ -314,9 +342,8 @@ def _indices_2d(t, device: int, rows):
     return t.data_ptr(), shape[1]
 
 
-@_on_stream
 def attend_decode(q, cache, block_table, kv_lens, next_n: int, compress_ratio: int, indices=None, *, scale=None,
-                  k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False):
+                  k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False, stream=None):
     """Attention of decode rows over the 4-bit cache; returns (out, lse or None).
 
     ``q`` is [rows, heads, head_dim] (bfloat16 or float16, strides in multiples of 8); row r belongs to
@@ -325,6 +352,14 @@ def attend_decode(q, cache, block_table, kv_lens, next_n: int, compress_ratio: i
     ``topk_decode`` returns them) lists, or all where it is None.  ``scale`` defaults to
     1 / sqrt(head_dim).  ``lse`` (fp32 [rows, heads]) is the log of each row's sum of exponentials.
     """
+    if stream is not None:
+        with _current(stream, q):
+            return attend_decode(q, cache, block_table, kv_lens, next_n, compress_ratio, indices, scale=scale, k_scale=k_scale,
+                                 v_scale=v_scale, out=out, lse=lse, want_lse=want_lse)
+    done = (_native or _short()).attend_decode(q, cache, k_scale, v_scale, scale, out, lse, want_lse, block_table, kv_lens,
+                                               next_n, compress_ratio, indices)
+    if done is not None:
+        return done
     device, head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
     rows = head[5]
     requests = (rows + next_n - 1) // max(next_n, 1)
@@ -338,15 +373,22 @@ def attend_decode(q, cache, block_table, kv_lens, next_n: int, compress_ratio: i
     return out, lse
 
 
-@_on_stream
 def attend_prefill(q, cache, block_table, row_requests, row_starts, row_ends, indices, *, scale=None,
-                   k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False):
+                   k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False, stream=None):
     """Attention of prefill rows over their selection in the 4-bit cache; returns (out, lse or None).
 
     Row r belongs to request ``row_requests[r]`` (int32; outside the block table: no entries) and sees
     its first ``row_ends[r] - row_starts[r]`` entries, the window given to ``topk_prefill``, whose
     ``indices`` (int32 [rows, k]) it attends to.  The rest is as in :func:`attend_decode`.
     """
+    if stream is not None:
+        with _current(stream, q):
+            return attend_prefill(q, cache, block_table, row_requests, row_starts, row_ends, indices, scale=scale,
+                                  k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, want_lse=want_lse)
+    done = (_native or _short()).attend_prefill(q, cache, k_scale, v_scale, scale, out, lse, want_lse, block_table,
+                                                row_requests, row_starts, row_ends, indices)
+    if done is not None:
+        return done
     device, head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
     rows = head[5]
     table, table_stride, width = _table_2d(block_table, device, 0)
