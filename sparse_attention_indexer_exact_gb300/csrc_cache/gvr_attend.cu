@@ -39,9 +39,7 @@ constexpr int STEP = 32;  // entries a warp takes at a time: one per lane
 constexpr int STAGES = 3;
 constexpr int MAX_CLUSTER = 8;
 constexpr float NO_TOP = -3.4028235e38f;  // the maximum of no scores: finite, so that differences are
-constexpr int CTA_STEPS = 3;
-constexpr int PART_STEPS = 4;
-constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_THREADS = 512, JOIN_WAYS = 8;
 
 struct AttendParams {
   const uint8_t* data;
@@ -147,14 +145,14 @@ struct Shape {
   static constexpr int RB = row_bytes(D);
   static constexpr int PITCH = 16 * (RB / 16 | 1);  // of a row in shared memory
   static constexpr int Q = 8 * NT;  // query vectors of a job
-  static constexpr int WARPS = D <= 128 && NT == 1 ? 8 : 4, THREADS = 32 * WARPS;
+  static constexpr int WARPS = 4, THREADS = 32 * WARPS;  // at most
   // accumulators and queries take 3 D / 8 NT registers: that leaves room for 16, 12 or 8 warps on an SM
-  static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 2 : D * NT == 128 ? 3 : 2;
+  static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 4 : D * NT == 128 ? 3 : 2;
   static constexpr int STAGE_BYTES = STEP * PITCH;
-  static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
-  static constexpr int PLACES = WARPS * STEP * 4;
-  static constexpr int JOIN = (WARPS * Q * D + 4 * WARPS * Q) * int(sizeof(float));
-  static constexpr int SMEM = RING + PLACES > JOIN ? RING + PLACES : JOIN;
+  static constexpr int RING = STAGES * STAGE_BYTES;                          // of a warp
+  static constexpr int WALK = RING + STEP * 4;                               // and its places
+  static constexpr int JOIN = (Q * D + 4 * Q) * int(sizeof(float));
+  static constexpr int WARP_SMEM = WALK > JOIN ? WALK : JOIN;                // the join reuses it
 };
 
 // Eight finished values of a head: sums over exp2(score - all) v, their sum `sum`.
@@ -236,8 +234,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
   const int mine = walkers == 1 ? steps : steps > me ? (steps - me + walkers - 1) / walkers : 0;
 
   // ---- fetching
-  uint8_t* ring = smem + warp * STAGES * S::STAGE_BYTES;
-  uint32_t* places = reinterpret_cast<uint32_t*>(smem + S::RING) + warp * STEP;
+  uint8_t* ring = smem + warp * S::RING;
+  uint32_t* places = reinterpret_cast<uint32_t*>(smem + warps * S::RING) + warp * STEP;
   constexpr int CODES = D / 16, SCALES = S::RB / 16 - CODES;  // 16-byte pieces of a row: of codes, of scales
   // (listed entries are loaded whatever the row's length, which may still be on its way)
   const uint32_t stride = walkers * STEP, end = indices ? uint32_t(p.k) : uint32_t(n);
@@ -640,34 +638,55 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
 }
 
 // Joins the parts of a job that was split over several clusters: one CTA a job, eight values a
-// thread, parts in order.
+// thread, JOIN_WAYS threads for the same values taking every JOIN_WAYS-th part in order and then
+// joining through shared memory.  It is launched while the walk still runs and waits for its end.
 template <int D, int NT>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(AttendParams p) {
   using S = Shape<D, NT>;
+  constexpr int EIGHTS = D / 8, TURN = JOIN_THREADS / JOIN_WAYS, PART = S::Q * (D + 2);
+  __shared__ float shared[JOIN_WAYS][TURN][10];
   const int jobs = p.heads_in * p.tiles_in, item = blockIdx.x / jobs, jb = blockIdx.x % jobs;
   const int groups = p.head_groups * p.tile_groups, group = item % groups;
   const int h = group % p.head_groups * p.heads_in + jb % p.heads_in;
   const int tile = group / p.head_groups * p.tiles_in + jb / p.heads_in;
   const int64_t unit = item / groups;
-  const float* src = p.parts_out + int64_t(blockIdx.x) * p.parts * (S::Q * (D + 2));
-  constexpr int EIGHTS = D / 8;
-  for (int i = threadIdx.x; i < S::Q * EIGHTS; i += JOIN_THREADS) {
-    const int qi = i / EIGHTS, d = (i % EIGHTS) * 8, m = tile * S::Q + qi;
-    const int64_t row = unit * p.fold + m / p.group;
-    if (m >= p.fold * p.group || row >= p.num_rows) continue;
+  const float* src = p.parts_out + int64_t(blockIdx.x) * p.parts * PART;
+  const int way = threadIdx.x / TURN, at = threadIdx.x % TURN;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i0 = 0; i0 < S::Q * EIGHTS; i0 += TURN) {
+    const int i = i0 + at, qi = i / EIGHTS, d = (i % EIGHTS) * 8;
     float all = NO_TOP, sum = 0.f, acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-    for (int r = 0; r < p.parts; ++r) all = fmaxf(all, src[int64_t(r) * (S::Q * (D + 2)) + S::Q * D + qi]);
-    for (int r = 0; r < p.parts; ++r) {
-      const float* from = src + int64_t(r) * (S::Q * (D + 2));
-      const float tr = from[S::Q * D + qi], down = exp2_fast(tr - all);
-      sum += down * from[S::Q * (D + 1) + qi];
+#pragma unroll 4
+    for (int r = way; r < p.parts; r += JOIN_WAYS) {
+      const float* from = src + int64_t(r) * PART;
+      const float tr = from[S::Q * D + qi], sr = from[S::Q * (D + 1) + qi];
       const float4 a = *reinterpret_cast<const float4*>(from + qi * D + d), b = *reinterpret_cast<const float4*>(from + qi * D + d + 4);
-      acc[0] += down * a.x, acc[1] += down * a.y, acc[2] += down * a.z, acc[3] += down * a.w;
-      acc[4] += down * b.x, acc[5] += down * b.y, acc[6] += down * b.z, acc[7] += down * b.w;
+      const float next = fmaxf(all, tr), down = exp2_fast(all - next), up = exp2_fast(tr - next);
+      all = next, sum = sum * down + sr * up;
+      acc[0] = acc[0] * down + a.x * up, acc[1] = acc[1] * down + a.y * up, acc[2] = acc[2] * down + a.z * up;
+      acc[3] = acc[3] * down + a.w * up, acc[4] = acc[4] * down + b.x * up, acc[5] = acc[5] * down + b.y * up;
+      acc[6] = acc[6] * down + b.z * up, acc[7] = acc[7] * down + b.w * up;
     }
-    write_out<D>(p, row, h * p.group + m % p.group, d, all, sum, acc);
+    float* mine = shared[way][at];
+    mine[0] = all, mine[1] = sum;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine[2 + j] = acc[j];
+    __syncthreads();
+    const int m = tile * S::Q + qi;
+    const int64_t row = unit * p.fold + m / p.group;
+    if (way == 0 && m < p.fold * p.group && row < p.num_rows) {
+      for (int w = 1; w < JOIN_WAYS; ++w) {
+        const float* other = shared[w][at];
+        const float next = fmaxf(all, other[0]), down = exp2_fast(all - next), up = exp2_fast(other[0] - next);
+        all = next, sum = sum * down + other[1] * up;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = acc[j] * down + other[2 + j] * up;
+      }
+      write_out<D>(p, row, h * p.group + m % p.group, d, all, sum, acc);
+    }
+    __syncthreads();
   }
 }
 
@@ -677,7 +696,7 @@ struct KernelInfo {
   const void* join;
   int queries, warps;
   int part_bytes;  // of one job's results
-  int smem;
+  int warp_smem;   // shared memory of a warp
 };
 
 template <int D, int NT>
@@ -685,7 +704,7 @@ KernelInfo info() {
   using S = Shape<D, NT>;
   return {{reinterpret_cast<const void*>(attend_kernel<D, NT, false>), reinterpret_cast<const void*>(attend_kernel<D, NT, true>)},
           reinterpret_cast<const void*>(join_kernel<D, NT>), S::Q,
-          S::WARPS, S::Q * (D + 2) * int(sizeof(float)), S::SMEM};
+          S::WARPS, S::Q * (D + 2) * int(sizeof(float)), S::WARP_SMEM};
 }
 
 constexpr int KERNELS = 6;
@@ -706,7 +725,7 @@ struct Device {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
   int sms = 0, smem_per_sm = 0, smem_reserved = 0;
-  int ctas_by_registers[KERNELS][2] = {};  // of the kernel's full size, per SM
+  int warps[KERNELS][2] = {};  // resident per SM, as far as registers go
 };
 Device g_devices[kMaxDevices];
 
@@ -730,12 +749,78 @@ cudaError_t device_info(Device** out) {
         if (d.err == cudaSuccess)
           d.err = cudaFuncSetAttribute(k.kernel[f], cudaFuncAttributeMaxDynamicSharedMemorySize, most - int(a.sharedSizeBytes));
         if (d.err == cudaSuccess)
-          d.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.ctas_by_registers[i][f], k.kernel[f], 32 * k.warps, 0);
+          d.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.warps[i][f], k.kernel[f], 32, 0);
       }
     }
   });
   *out = &d;
   return d.err;
+}
+
+// A launch shape: a CTA's jobs are all query tiles of a KV head as far as its warps go, then
+// neighbouring KV heads (a divisor of their number), then several warps a job.
+struct Geometry {
+  int heads_in = 1, tiles_in = 1, head_groups = 1, tile_groups = 1, split_log2 = 0, cluster = 1;
+  int64_t groups = 1, parts = 1;  // CTAs side by side for a unit; clusters of CTAs for the entries
+  float cost = 1e30f;
+};
+
+// Expected time in us of a launch, from what was measured over shapes of 1 to 700 rows and 512 to 131071
+// entries: a step of each kernel beside w warps on its SM, what a warp does around its steps, what a
+// second join and what many CTAs cost.  (head_dim 128, 8 queries: 0.55 a step alone, 1.16 beside 8 warps,
+// 2.03 beside 16, so more than 8 warps an SM gain little, and cost their start.  CTAs of eight warps were
+// slower everywhere: their clusters spread less evenly over the SMs.)
+struct Expected {
+  float least, fixed, per_warp;
+};
+constexpr Expected STEP_US[KERNELS] = {{0.35f, 0.2f, 0.06f}, {0.5f, 0.4f, 0.07f}, {0.8f, 0.6f, 0.1f},
+                                       {0.55f, 0.3f, 0.108f}, {0.8f, 0.8f, 0.1f}, {0.9f, 0.9f, 0.16f}};
+
+struct Call {
+  int kernel, kv_heads, tiles;
+  int64_t units, steps, part_room;
+  bool listed, large;  // entries listed by indices; a cache larger than the TLBs cover
+};
+
+Geometry plan(const Device& d, const KernelInfo& info, int warps_by_registers, const Call& call, int warps) {
+  Geometry g;
+  g.tile_groups = (call.tiles + warps - 1) / warps;
+  g.tiles_in = (call.tiles + g.tile_groups - 1) / g.tile_groups;
+  g.heads_in = std::min(call.kv_heads, warps / g.tiles_in);
+  while (call.kv_heads % g.heads_in) --g.heads_in;
+  g.head_groups = call.kv_heads / g.heads_in;
+  g.groups = int64_t(g.tile_groups) * g.head_groups;
+  while ((g.heads_in * g.tiles_in) << (g.split_log2 + 1) <= warps) ++g.split_log2;
+  const int jobs = g.heads_in * g.tiles_in, cta_warps = jobs << g.split_log2;
+  const int per_sm = std::max(1, std::min(warps_by_registers / cta_warps, d.smem_per_sm / (cta_warps * info.warp_smem + d.smem_reserved)));
+  const int64_t resident = int64_t(d.sms) * per_sm, items = call.units * g.groups;
+  const int64_t turns = (call.steps + (1 << g.split_log2) - 1) >> g.split_log2;  // steps of a warp, were there one CTA
+  const Expected& x = STEP_US[call.kernel];
+  const float missing = call.listed && call.large ? 0.21f / 256.f * std::pow(float(g.head_groups), 0.7f) : 0.f;
+  for (int64_t split = 1; split == 1 || split <= turns;) {
+    // up to a cluster, then whole clusters (`parts`) joined by a second kernel through the workspace
+    const int cs = int(std::min<int64_t>(split, MAX_CLUSTER));
+    const int64_t parts = split / cs, ctas = items * split;
+    if (parts > 1 && (parts * items * jobs > call.part_room || ctas > resident)) break;
+    const float own = float((turns + split - 1) / split);
+    auto cta_us = [&](float w) {
+      float step = std::max(x.least, x.fixed + x.per_warp * (call.listed ? w : 0.7f * w));  // of whole rows some end early
+      // heads of a listed entry that are fetched by CTAs apart: more requests, and in a cache that the TLBs
+      // do not cover more misses (5 GB, 8 heads in 4 groups beside 14 warps: 1.4 times)
+      if (call.listed) step *= 1.f + 0.015f * float(g.head_groups - 1) + (call.large ? missing * w * w : 0.f);
+      return 0.2f * w + 0.4f * float(cta_warps) + own * step;
+    };
+    float cost;
+    if (ctas <= resident) cost = cta_us(float((ctas + d.sms - 1) / d.sms * cta_warps));
+    else cost = float(ctas) / float(resident) * cta_us(float(per_sm * cta_warps)) + cta_us(float(cta_warps));
+    if (!call.listed) cost *= 1.f + 0.25f / float(split);  // rows shorter than the table: the longest end last
+    if (ctas > 1024) cost += 0.011f * float(ctas - 1024);
+    if (cta_warps > jobs || split > 1) cost += 0.7f;
+    if (parts > 1) cost += 2.5f;
+    if (cost < g.cost) g.cost = cost, g.cluster = cs, g.parts = parts;
+    split = split < MAX_CLUSTER ? split + 1 : split * 2;
+  }
+  return g;
 }
 
 gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride, int64_t q_head_stride, int32_t dtype,
@@ -768,44 +853,31 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
   if (members > kIntMax) return GVR_ERR_ARG;
   const int kernel = choose_kernel(cache->head_dim, members);
   const KernelInfo& info = kernel_info(kernel);
-  // a CTA's jobs: all query tiles of a KV head as far as its warps go, then neighbouring KV heads
-  // (a divisor of their number), then several warps a job
   p.tiles = int32_t((members + info.queries - 1) / info.queries);
-  const int warps = info.warps;
-  p.tile_groups = (p.tiles + warps - 1) / warps;
-  p.tiles_in = (p.tiles + p.tile_groups - 1) / p.tile_groups;
-  p.heads_in = warps / p.tiles_in;
-  while (p.kv_heads % p.heads_in) --p.heads_in;
-  p.head_groups = p.kv_heads / p.heads_in;
-  const int jobs = p.heads_in * p.tiles_in;
-  p.split_log2 = jobs > warps / 2 ? 0 : jobs > warps / 4 ? 1 : jobs > warps / 8 ? 2 : 3;  // a power of two
-  p.split = 1 << p.split_log2;
-  const int threads = 32 * jobs * p.split, smem = info.smem;
   const int64_t units = (num_rows + p.fold - 1) / p.fold;
-  const int64_t groups = int64_t(p.tile_groups) * p.head_groups;
-  if (groups > 65535 || units > kIntMax / groups / MAX_CLUSTER) return GVR_ERR_ARG;
-  p.items = int32_t(units * groups);
+  if (int64_t(p.kv_heads) * p.tiles > 65535 || units > kIntMax / MAX_CLUSTER / (int64_t(p.kv_heads) * p.tiles)) return GVR_ERR_ARG;
   Device* d = nullptr;
   if (device_info(&d) != cudaSuccess) return GVR_ERR_LAUNCH;
-  const int64_t resident = int64_t(d->sms) * std::max(1, std::min(d->ctas_by_registers[kernel][p.fold > 1], d->smem_per_sm / (smem + 256 + d->smem_reserved)));
-  // CTAs per item: the cluster size with the fewest rounds of steps, counting a CTA's start and end
-  // as CTA_STEPS steps
-  const int64_t steps = ((p.indices ? k : p.capacity) + STEP * p.split - 1) / (STEP * p.split);  // of a warp
-  int cs = 1;
-  int64_t least = INT64_MAX;
-  for (int x = 1; x <= MAX_CLUSTER && x <= std::max<int64_t>(1, steps); ++x) {
-    const int64_t cost = (p.items * int64_t(x) + resident - 1) / resident * ((steps + x - 1) / x + CTA_STEPS);
-    if (cost < least) least = cost, cs = x;
+  const int64_t steps = ((p.indices ? k : p.capacity) + STEP - 1) / STEP;
+  const Call call = {kernel, p.kv_heads, p.tiles, units, steps,
+                     workspace ? int64_t(std::min<size_t>(workspace_bytes, size_t(1) << 40)) / info.part_bytes : 0,
+                     p.indices != nullptr, cache->num_pages * cache->page_stride > (int64_t(2) << 30)};
+  Geometry best;
+  for (int warps = info.warps; warps >= 1; warps /= 2) {
+    const Geometry g = plan(*d, info, d->warps[kernel][p.fold > 1], call, warps);
+    if (g.cost < best.cost) best = g;
   }
-  // few items of many entries: as many clusters an item as the device holds, while each keeps
-  // PART_STEPS steps a CTA, joined by a second kernel through the workspace
-  p.parts = 1;
-  if (workspace && cs == MAX_CLUSTER) {
-    const int64_t full = resident / (int64_t(p.items) * cs), worth = steps / (int64_t(cs) * PART_STEPS);
-    const int64_t room = int64_t(workspace_bytes) / info.part_bytes / (int64_t(p.items) * jobs);
-    p.parts = int32_t(std::max<int64_t>(1, std::min(full, std::min(worth, room))));
-    p.parts_out = static_cast<float*>(workspace);
-  }
+  p.heads_in = best.heads_in;
+  p.tiles_in = best.tiles_in;
+  p.head_groups = best.head_groups;
+  p.tile_groups = best.tile_groups;
+  p.split_log2 = best.split_log2;
+  p.split = 1 << best.split_log2;
+  p.items = int32_t(units * best.groups);
+  const int jobs = p.heads_in * p.tiles_in, threads = 32 * jobs * p.split, smem = jobs * p.split * info.warp_smem, cs = best.cluster;
+  const int64_t groups = best.groups;
+  p.parts = int32_t(best.parts);
+  p.parts_out = static_cast<float*>(workspace);
   void* args[] = {&p};
   const void* main_kernel = info.kernel[p.fold > 1];
   const cudaStream_t on = static_cast<cudaStream_t>(stream);
@@ -827,7 +899,18 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
     cfg.numAttrs = 1;
     e = cudaLaunchKernelExC(&cfg, main_kernel, args);
   }
-  if (e == cudaSuccess && p.parts > 1) e = cudaLaunchKernel(info.join, dim3(uint32_t(p.items * jobs)), dim3(JOIN_THREADS), args, 0, on);
+  if (e == cudaSuccess && p.parts > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(uint32_t(p.items * jobs));
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.stream = on;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelExC(&cfg, info.join, args);
+  }
   return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
 }
 
