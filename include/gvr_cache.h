@@ -100,6 +100,7 @@ gvr_status cache_tables(const int32_t* cached_lens, const int32_t* kv_lens, int6
  * `dtype` with unit inner stride and the given token and head strides (in elements, multiples of
  * 8; bases 16-byte aligned); token t goes to slots[t].  Slots that name an entry must be
  * distinct: which token's values an entry named twice holds is unspecified.
+ * num_tokens * num_kv_heads < 2^31.
  */
 gvr_status cache_append(const gvr_cache* cache, const void* k, int64_t k_token_stride,
                         int64_t k_head_stride, const void* v, int64_t v_token_stride,
@@ -110,6 +111,7 @@ gvr_status cache_append(const gvr_cache* cache, const void* k, int64_t k_token_s
  * The values held at slots[0 .. num_tokens): k and v, packed [num_tokens][num_kv_heads][head_dim]
  * of `dtype`, 16-byte aligned, either may be NULL.  code * scale is exact in both types;
  * k_scale and v_scale are multiplied in fp32 and the product rounded to `dtype`.
+ * num_tokens * num_kv_heads < 2^31.
  */
 gvr_status cache_read(const gvr_cache* cache, const int32_t* slots, int64_t num_tokens,
                       int32_t dtype, void* k, void* v, void* stream);

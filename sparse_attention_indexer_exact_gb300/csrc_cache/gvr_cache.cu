@@ -160,19 +160,20 @@ __global__ void __launch_bounds__(TABLE_THREADS) cache_tables_kernel(TableParams
   for (int64_t t4 = at * 4; t4 < p.num_slots; t4 += stride * 4) {
     int slot[4] = {-1, -1, -1, -1};
     if (t4 < total_entries) {
-      int r = owner(entry_first, p.requests, int(t4));
+      int r = owner(entry_first, p.requests, int(t4)), page = -1;
+      int64_t at_block = -1;  // the block that `page` is of, of request r
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t t = t4 + i;
         if (t >= total_entries) break;
-        while (r + 1 < p.requests && entry_first[r + 1] <= t) ++r;
-        const int64_t entry = int64_t(held[r]) + (t - entry_first[r]);
-        const int64_t block = entry >> p.page_shift;
-        if (block >= p.width) continue;
-        const int64_t j = block - pages_of(held[r], p.page_shift) + page_first[r];  // place among the new pages
-        int page;
-        if (block < pages_of(held[r], p.page_shift)) page = p.table[r * p.table_stride + block];
-        else page = j < p.num_free ? p.free_pages[j] : -1;
+        while (r + 1 < p.requests && entry_first[r + 1] <= t) ++r, at_block = -1;
+        const int64_t entry = int64_t(held[r]) + (t - entry_first[r]), block = entry >> p.page_shift;
+        if (block != at_block) {  // mostly once
+          const int have = pages_of(held[r], p.page_shift);
+          const int64_t j = block - have + page_first[r];  // place among the new pages
+          page = block >= p.width ? -1 : block < have ? p.table[r * p.table_stride + block] : j < p.num_free ? p.free_pages[j] : -1;
+          at_block = block;
+        }
         slot[i] = slot_of(page, int(entry), p.page_shift);
       }
     }
@@ -189,15 +190,22 @@ __global__ void __launch_bounds__(TABLE_THREADS) cache_tables_kernel(TableParams
 // ------------------------------------------------------------------------------ append and read
 constexpr int COPY_THREADS = 256;
 
+struct Factor {
+  float value, six, sixth;  // the cache's factor f, 6 f and the correctly rounded 1 / (6 f); sixth 0: divide
+};
+
 struct CopyParams {
   uint8_t* data;
   const int32_t* slots;
   const void* k;
   const void* v;
   int64_t k_token, k_head, v_token, v_head;  // strides in elements
-  int64_t page_stride, work;                 // work: tokens * heads * blocks of a head
-  int32_t num_pages, heads, page_shift;
-  float k_scale, v_scale;
+  int64_t page_stride;
+  uint32_t tokens;
+  uint32_t heads;
+  int32_t num_pages, page_shift;
+  Factor k_scale, v_scale;
+  int32_t heads_log2;  // -1: no power of two
 };
 
 template <bool BF16>
@@ -223,31 +231,67 @@ __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// One block of 16 values: scale (8 bits) and codes (16 x 4 bits).
-template <bool BF16>
-__device__ __forceinline__ uint32_t quantise(const uint32_t (&x)[8], float factor, uint2& codes) {
-  uint32_t m = x[0] & 0x7fff7fffu;
-#pragma unroll
-  for (int i = 1; i < 8; ++i) m = max_nan<BF16>(m, x[i] & 0x7fff7fffu);
-  const float2 two = to_f32<BF16>(max_nan<BF16>(m, (m >> 16) | (m << 16)));
-  const uint32_t scale = f32_to_e4m3(two.x / (6.f * factor));
-  const float unit = f16x2_to_f32(e4m3x2_to_f16x2(scale)).x * factor;
-  uint32_t c[2] = {0, 0};
-  if (unit > 0.f) {  // neither 0 nor NaN
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 v = to_f32<BF16>(x[i]);
-      c[i >> 2] |= f32x2_to_e2m1(v.x / unit, v.y / unit) << (8 * (i & 3));
-    }
-  }
-  codes = make_uint2(c[0], c[1]);
-  return scale;
+// Two products and two fused multiply-adds in one instruction each.
+__device__ __forceinline__ uint64_t f32x2(float2 v) {
+  return uint64_t(__float_as_uint(v.x)) | uint64_t(__float_as_uint(v.y)) << 32;
+}
+__device__ __forceinline__ float2 f32x2(uint64_t v) {
+  return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-// Sixteen values as two 16-byte loads.
-__device__ __forceinline__ void load16(const uint4* src, uint32_t (&x)[8]) {
-  const uint4 a = __ldg(src), b = __ldg(src + 1);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// x / d as IEEE division gives it, r being the correctly rounded 1 / d: one residual step makes the product
+// x r correctly rounded (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990), as long as nothing over- or underflows.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, d, x), r, q);
+}
+
+// Half of a block of 16 values in each of two neighbouring lanes: the block's scale (8 bits) and this
+// lane's codes (8 x 4 bits).
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantise(const uint4& v, const Factor& f, uint32_t& codes) {
+  const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = x[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = max_nan<BF16>(m, x[i] & 0x7fff7fffu);
+  m = max_nan<BF16>(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const float most = to_f32<BF16>(max_nan<BF16>(m, (m >> 16) | (m << 16))).x;
+  // the residual step wants normal numbers all the way: not for zeros, infinities and far factors
+  const bool plain = f.sixth != 0.f && most > 1e-18f && most < 1e18f;
+  const uint32_t scale = f32_to_e4m3(plain ? quotient(most, f.six, f.sixth) : most / f.six);
+  const float unit = f16x2_to_f32(e4m3x2_to_f16x2(scale)).x * f.value;
+  codes = 0;
+  if (unit > 0.f) {  // neither 0 nor NaN
+    if (plain) {
+      const float r = __frcp_rn(unit);
+      const uint64_t rr = f32x2(make_float2(r, r)), minus = f32x2(make_float2(-unit, -unit));
+      float2 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t a = f32x2(to_f32<BF16>(x[i])), y = mul2(a, rr);
+        q[i] = f32x2(fma2(fma2(y, minus, a), rr, y));
+      }
+      codes = f32x8_to_e2m1(q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = to_f32<BF16>(x[i]);
+        codes |= f32x2_to_e2m1(a.x / unit, a.y / unit) << (8 * i);
+      }
+    }
+  }
+  return scale;
 }
 
 // Address of a slot's row of one head, or nullptr for a slot that names no entry.
@@ -256,64 +300,57 @@ __device__ __forceinline__ uint8_t* row_of(const CopyParams& p, int slot, int he
   return off < 0 ? nullptr : p.data + off;
 }
 
-// A thread takes one block of 16 values of K and the same block of V: neighbouring threads read
-// neighbouring 32-byte pieces and write neighbouring 8-byte pieces of one row.  Bound by the
-// bytes of K and V.
+// D / 8 neighbouring lanes take the K and V of one token and head, eight values of each a lane: a warp
+// reads (or, for cache_read, writes) 512 neighbouring bytes at a time, and writes 128 (64) of codes.
+// Bound by these bytes; 16333 tokens x 8 heads of 128 in bf16: APPEND_US, READ_US.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(COPY_THREADS) cache_append_kernel(CopyParams p) {
-  constexpr int BLOCKS = D / 16;
-  const int64_t i = int64_t(blockIdx.x) * COPY_THREADS + threadIdx.x;
-  if (i >= p.work) return;
-  const int b = int(i % BLOCKS);
-  const int64_t th = i / BLOCKS, t = th / p.heads;
-  const int h = int(th - t * p.heads);
-  uint8_t* row = row_of(p, p.slots[t], h, row_bytes(D));
+  constexpr int LANES = D / 8;
+  const uint32_t th = blockIdx.x * uint32_t(COPY_THREADS / LANES) + threadIdx.x / LANES, t = p.heads_log2 >= 0 ? th >> p.heads_log2 : th / p.heads;
+  const int h = int(th - t * p.heads), b = threadIdx.x % LANES;
+  uint8_t* row = t < p.tokens ? row_of(p, p.slots[t], h, row_bytes(D)) : nullptr;
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  if (row) {
+    k = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k) + int64_t(t) * p.k_token + h * p.k_head) + b);
+    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + int64_t(t) * p.v_token + h * p.v_head) + b);
+  }
+  uint32_t kc, vc;
+  const uint32_t ks = quantise<BF16>(k, p.k_scale, kc), vs = quantise<BF16>(v, p.v_scale, vc);  // by all lanes
   if (!row) return;
-  uint32_t k[8], v[8];
-  load16(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k) + t * p.k_token + h * p.k_head + b * 16), k);
-  load16(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + t * p.v_token + h * p.v_head + b * 16), v);
-  uint2 kc, vc;
-  const uint32_t ks = quantise<BF16>(k, p.k_scale, kc), vs = quantise<BF16>(v, p.v_scale, vc);
-  *reinterpret_cast<uint2*>(row + b * 8) = kc;
-  *reinterpret_cast<uint2*>(row + D / 2 + b * 8) = vc;
-  row[D + b] = uint8_t(ks);
-  row[D + BLOCKS + b] = uint8_t(vs);
+  *reinterpret_cast<uint32_t*>(row + b * 4) = kc;
+  *reinterpret_cast<uint32_t*>(row + D / 2 + b * 4) = vc;
+  // even lanes write the scales of K, odd ones those of V
+  row[D + (b & 1) * (D / 16) + b / 2] = uint8_t(b & 1 ? vs : ks);
 }
 
 template <bool BF16>
-__device__ __forceinline__ void dequantise(uint2 codes, uint32_t scale, float factor, uint4* dst) {
-  const float unit = f16x2_to_f32(e4m3x2_to_f16x2(scale)).x;
-  uint32_t out[8];
+__device__ __forceinline__ uint4 dequantise(uint32_t codes, uint32_t scale, float factor) {
+  const uint32_t unit = e4m3x2_to_f16x2(scale | scale << 8);
+  uint32_t h[4], out[4];
+  e2m1_to_f16x2(codes, h);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t h[4];
-    e2m1_to_f16x2(j ? codes.y : codes.x, h);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 c = f16x2_to_f32(h[i]);
-      out[4 * j + i] = from_f32<BF16>(c.x * unit * factor, c.y * unit * factor);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = f16x2_to_f32(hmul2(h[i], unit));  // exact
+    out[i] = from_f32<BF16>(x.x * factor, x.y * factor);
   }
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(COPY_THREADS) cache_read_kernel(CopyParams p) {
-  constexpr int BLOCKS = D / 16;
-  const int64_t i = int64_t(blockIdx.x) * COPY_THREADS + threadIdx.x;
-  if (i >= p.work) return;
-  const int b = int(i % BLOCKS);
-  const int64_t th = i / BLOCKS, t = th / p.heads;
+  constexpr int LANES = D / 8;
+  const uint32_t th = blockIdx.x * uint32_t(COPY_THREADS / LANES) + threadIdx.x / LANES, t = p.heads_log2 >= 0 ? th >> p.heads_log2 : th / p.heads;
+  if (t >= p.tokens) return;
+  const int b = threadIdx.x % LANES;
   const uint8_t* row = row_of(p, p.slots[t], int(th - t * p.heads), row_bytes(D));
-  uint2 kc = make_uint2(0, 0), vc = kc;
-  uint32_t ks = 0, vs = 0;
+  uint32_t kc = 0, vc = 0, ks = 0, vs = 0;
   if (row) {
-    if (p.k) kc = *reinterpret_cast<const uint2*>(row + b * 8), ks = row[D + b];
-    if (p.v) vc = *reinterpret_cast<const uint2*>(row + D / 2 + b * 8), vs = row[D + BLOCKS + b];
+    if (p.k) kc = *reinterpret_cast<const uint32_t*>(row + b * 4), ks = row[D + b / 2];
+    if (p.v) vc = *reinterpret_cast<const uint32_t*>(row + D / 2 + b * 4), vs = row[D + D / 16 + b / 2];
   }
-  if (p.k) dequantise<BF16>(kc, ks, p.k_scale, static_cast<uint4*>(const_cast<void*>(p.k)) + i * 2);
-  if (p.v) dequantise<BF16>(vc, vs, p.v_scale, static_cast<uint4*>(const_cast<void*>(p.v)) + i * 2);
+  const int64_t at = int64_t(th) * LANES + b;
+  if (p.k) static_cast<uint4*>(const_cast<void*>(p.k))[at] = dequantise<BF16>(kc, ks, p.k_scale.value);
+  if (p.v) static_cast<uint4*>(const_cast<void*>(p.v))[at] = dequantise<BF16>(vc, vs, p.v_scale.value);
 }
 
 using CopyKernel = void (*)(CopyParams);
@@ -325,19 +362,23 @@ CopyKernel copy_kernel(int dim, bool append) {
   return append ? cache_append_kernel<256, BF16> : cache_read_kernel<256, BF16>;
 }
 
+Factor factor_of(float f) {
+  const float six = 6.f * f;
+  return {f, six, f > 1e-12f && f < 1e12f ? 1.f / six : 0.f};
+}
+
 gvr_status launch_copy(const gvr_cache* c, CopyParams& p, int32_t dtype, int64_t tokens, bool append, void* stream) {
-  const int64_t blocks = c->head_dim / 16;
-  if (tokens > INT64_MAX / 4096 / c->num_kv_heads) return GVR_ERR_ARG;
+  if (tokens > kIntMax / c->num_kv_heads) return GVR_ERR_ARG;
   p.data = static_cast<uint8_t*>(c->data);
   p.page_stride = c->page_stride;
+  p.tokens = uint32_t(tokens);
   p.num_pages = int32_t(c->num_pages);
-  p.work = tokens * c->num_kv_heads * blocks;
   p.heads = c->num_kv_heads;
   p.page_shift = log2_of(c->page_size);
-  p.k_scale = c->k_scale;
-  p.v_scale = c->v_scale;
-  const int64_t grid = (p.work + COPY_THREADS - 1) / COPY_THREADS;
-  if (grid > kIntMax) return GVR_ERR_ARG;
+  p.k_scale = factor_of(c->k_scale);
+  p.v_scale = factor_of(c->v_scale);
+  p.heads_log2 = (c->num_kv_heads & (c->num_kv_heads - 1)) == 0 ? log2_of(c->num_kv_heads) : -1;
+  const int64_t rows = COPY_THREADS / (c->head_dim / 8), grid = (tokens * c->num_kv_heads + rows - 1) / rows;
   const CopyKernel kernel = dtype == GVR_BF16 ? copy_kernel<true>(c->head_dim, append) : copy_kernel<false>(c->head_dim, append);
   void* args[] = {&p};
   if (cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(uint32_t(grid)), dim3(COPY_THREADS), args, 0,
