@@ -192,6 +192,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
   const int tile_in = p.tiles_in == 1 ? 0 : job / p.heads_in;
   const int h = head0 + job - tile_in * p.heads_in, tile = tile0 + tile_in;
 
+  begin();
+
   // ---- the job's queries, on their way: lane (g, c) holds query 8 t + g at D/4 c + [0, D/4)
   const int m0 = tile * S::Q;
   const int members = tile < p.tiles ? (FOLD ? p.fold * p.group : p.group) : 0;
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(AttendParams p) {
   const int64_t unit = item / groups;
   const float* src = p.parts_out + int64_t(blockIdx.x) * p.parts * PART;
   const int way = threadIdx.x / TURN, at = threadIdx.x % TURN;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin();
   for (int i0 = 0; i0 < S::Q * EIGHTS; i0 += TURN) {
     const int i = i0 + at, qi = i / EIGHTS, d = (i % EIGHTS) * 8;
     float all = NO_TOP, sum = 0.f, acc[8];
@@ -880,37 +882,9 @@ gvr_status attend(const gvr_cache* cache, AttendParams& p, int64_t q_row_stride,
   p.parts_out = static_cast<float*>(workspace);
   void* args[] = {&p};
   const void* main_kernel = info.kernel[p.fold > 1];
-  const cudaStream_t on = static_cast<cudaStream_t>(stream);
   const dim3 grid(uint32_t(units * cs), uint32_t(groups), uint32_t(p.parts));
-  cudaError_t e;
-  if (cs == 1) {
-    e = cudaLaunchKernel(main_kernel, grid, dim3(threads), args, size_t(smem), on);
-  } else {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = size_t(smem);
-    cfg.stream = on;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = uint32_t(cs);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelExC(&cfg, main_kernel, args);
-  }
-  if (e == cudaSuccess && p.parts > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(uint32_t(p.items * jobs));
-    cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.stream = on;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelExC(&cfg, info.join, args);
-  }
+  cudaError_t e = launch(main_kernel, grid, threads, smem, cs, args, stream);
+  if (e == cudaSuccess && p.parts > 1) e = launch(info.join, dim3(uint32_t(p.items * jobs)), JOIN_THREADS, 0, 1, args, stream);
   return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
 }
 

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(THREADS) cache_tables_kernel(TableParams p) {
   __shared__ int warp_pages[WARPS], warp_entries[WARPS], warp_missing[WARPS];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  begin();
   const int per = (p.requests + THREADS - 1) / THREADS;
   const int r0 = min(tid * per, p.requests), r1 = min(r0 + per, p.requests);
   int pages = 0, entries = 0, missing = 0;
@@ -308,6 +309,7 @@ __device__ __forceinline__ uint8_t* row_of(const CopyParams& p, int slot, int he
 template <int D, bool BF16>
 __global__ void __launch_bounds__(COPY_THREADS) cache_append_kernel(CopyParams p) {
   constexpr int LANES = D / 8;
+  begin();
   const uint32_t th = blockIdx.x * uint32_t(COPY_THREADS / LANES) + threadIdx.x / LANES, t = p.heads_log2 >= 0 ? th >> p.heads_log2 : th / p.heads;
   const int h = int(th - t * p.heads), b = threadIdx.x % LANES;
   uint8_t* row = t < p.tokens ? row_of(p, p.slots[t], h, row_bytes(D)) : nullptr;
@@ -341,6 +343,7 @@ __device__ __forceinline__ uint4 dequantise(uint32_t codes, uint32_t scale, floa
 template <int D, bool BF16>
 __global__ void __launch_bounds__(COPY_THREADS) cache_read_kernel(CopyParams p) {
   constexpr int LANES = D / 8;
+  begin();
   const uint32_t th = blockIdx.x * uint32_t(COPY_THREADS / LANES) + threadIdx.x / LANES, t = p.heads_log2 >= 0 ? th >> p.heads_log2 : th / p.heads;
   if (t >= p.tokens) return;
   const int b = threadIdx.x % LANES;
@@ -383,8 +386,7 @@ gvr_status launch_copy(const gvr_cache* c, CopyParams& p, int32_t dtype, int64_t
   const int64_t rows = COPY_THREADS / (c->head_dim / 8), grid = (tokens * c->num_kv_heads + rows - 1) / rows;
   const CopyKernel kernel = dtype == GVR_BF16 ? copy_kernel<true>(c->head_dim, append) : copy_kernel<false>(c->head_dim, append);
   void* args[] = {&p};
-  if (cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(uint32_t(grid)), dim3(COPY_THREADS), args, 0,
-                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  if (launch(reinterpret_cast<const void*>(kernel), dim3(uint32_t(grid)), COPY_THREADS, 0, 1, args, stream) != cudaSuccess)
     return GVR_ERR_LAUNCH;
   return GVR_OK;
 }
@@ -460,8 +462,7 @@ gvr_status cache_tables(const int32_t* cached_lens, const int32_t* kv_lens, int6
                        : step ? reinterpret_cast<const void*>(cache_tables_kernel<TABLE_THREADS, 1>)
                               : reinterpret_cast<const void*>(cache_tables_kernel<TABLE_THREADS, 4>);
   void* args[] = {&p};
-  if (cudaLaunchKernel(kernel, dim3(grid), dim3(threads), args, size_t(num_requests) * 3 * sizeof(int),
-                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
+  if (launch(kernel, dim3(grid), threads, int(num_requests * 3 * sizeof(int)), 1, args, stream) != cudaSuccess)
     return GVR_ERR_LAUNCH;
   return GVR_OK;
 }
