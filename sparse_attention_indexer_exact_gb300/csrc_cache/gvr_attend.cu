@@ -147,7 +147,7 @@ struct Shape {
   static constexpr int Q = 8 * NT;  // query vectors of a job
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;  // at most
   // accumulators and queries take 3 D / 8 NT registers: that leaves room for 16, 12 or 8 warps on an SM
-  static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 4 : D * NT == 128 ? 3 : 2;
+  static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 4 : D * NT == 128 ? 3 : 2, FOLD_BLOCKS = D * NT == 128 ? 3 : BLOCKS;
   static constexpr int STAGE_BYTES = STEP * PITCH;
   static constexpr int RING = STAGES * STAGE_BYTES;                          // of a warp
   static constexpr int WALK = RING + STEP * 4;                               // and its places
@@ -174,7 +174,7 @@ __device__ __forceinline__ void write_out(const AttendParams& p, int64_t row, in
 
 // FOLD: the unit is the next_n rows of a request (whole-cache decode with next_n > 1).
 template <int D, int NT, bool FOLD>
-__global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) attend_kernel(AttendParams p) {
+__global__ void __launch_bounds__(Shape<D, NT>::THREADS, FOLD ? Shape<D, NT>::FOLD_BLOCKS : Shape<D, NT>::BLOCKS) attend_kernel(AttendParams p) {
   using S = Shape<D, NT>;
   constexpr int KSTEPS = D / 16;       // 16-wide steps of the head dimension
   constexpr int KW = D / 32;           // 32-bit words of K codes per lane and entry
@@ -327,6 +327,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
   // entries below this are seen by every query of the unit
   const int sure = FOLD ? decode_entries(kv, p.next_n, 0, p.ratio, p.capacity) : n;
 
+  const int first_row = FOLD ? m0 / p.group : 0, last_row = FOLD ? min((m0 + S::Q - 1) / p.group, p.fold - 1) : 0;  // of the job
+  int row_of_query[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) row_of_query[t] = FOLD ? (m0 + 8 * t + g) / p.group : 0;
+
   // ---- the walk
   float o[NT][KSTEPS][4];
   float top[NT][2], total[NT][2];
@@ -461,8 +466,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
       // O^T += V^T P^T: lane (g, c) expands V at D/8 g + [0, D/8) of four entries of each tile.  An
       // entry that is left out has P = 0 and, as 0 x NaN is NaN, a V scale of 0.  At the border that
       // differs from row to row, so each row of the job takes a pass with its own entries.
-      int j = border ? m0 / p.group : 0;
-      const int j_end = border ? min((m0 + S::Q - 1) / p.group, p.fold - 1) : 0;
+      int j = border ? first_row : 0;
+      const int j_end = border ? last_row : 0;
       do {
         uint32_t there = mask, pj[2][NT][2];
 #pragma unroll
@@ -474,7 +479,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, Shape<D, NT>::BLOCKS) a
           there &= seen <= 0 ? 0u : seen >= 32 ? 0xffffffffu : (1u << int(seen)) - 1;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            if ((m0 + 8 * t + g) / p.group != j) pj[0][t][0] = pj[0][t][1] = pj[1][t][0] = pj[1][t][1] = 0;
+            if (row_of_query[t] != j) pj[0][t][0] = pj[0][t][1] = pj[1][t][0] = pj[1][t][1] = 0;
         }
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
