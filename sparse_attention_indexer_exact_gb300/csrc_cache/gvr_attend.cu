@@ -466,21 +466,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, FOLD ? Shape<D, NT>::FO
       // O^T += V^T P^T: lane (g, c) expands V at D/8 g + [0, D/8) of four entries of each tile.  An
       // entry that is left out has P = 0 and, as 0 x NaN is NaN, a V scale of 0.  At the border that
       // differs from row to row, so each row of the job takes a pass with its own entries.
-      int j = border ? first_row : 0;
-      const int j_end = border ? last_row : 0;
-      do {
-        uint32_t there = mask, pj[2][NT][2];
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) pj[mt][t][0] = pb[mt][t][0], pj[mt][t][1] = pb[mt][t][1];
-        if (border) {
-          const int64_t seen = decode_entries(kv, p.next_n, j, p.ratio, p.capacity) - first;
-          there &= seen <= 0 ? 0u : seen >= 32 ? 0xffffffffu : (1u << int(seen)) - 1;
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            if (row_of_query[t] != j) pj[0][t][0] = pj[0][t][1] = pj[1][t][0] = pj[1][t][1] = 0;
-        }
+      auto add_values = [&](uint32_t there, const uint32_t (&pj)[2][NT][2]) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
           uint32_t v[4][VW], vs[4];
@@ -521,7 +507,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, FOLD ? Shape<D, NT>::FO
             }
           }
         }
-      } while (++j <= j_end);
+      };
+      if (!border) {
+        add_values(mask, pb);
+      } else {
+        for (int j = first_row; j <= last_row; ++j) {
+          const int64_t seen = decode_entries(kv, p.next_n, j, p.ratio, p.capacity) - first;
+          uint32_t pj[2][NT][2];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) pj[mt][t][x] = row_of_query[t] == j ? pb[mt][t][x] : 0;
+          add_values(mask & (seen <= 0 ? 0u : seen >= 32 ? 0xffffffffu : (1u << int(seen)) - 1), pj);
+        }
+      }
     }
   }
   copy_wait<0>();
