@@ -52,7 +52,7 @@ enum { GVR_BF16 = 0, GVR_F16 = 1 };
 
 #define GVR_CACHE_MAX_REQUESTS 8192   /* cache_tables */
 #define GVR_CACHE_MAX_PAGE_SIZE 4096
-#define GVR_ATTEND_WORKSPACE (1 << 20) /* bytes */
+#define GVR_ATTEND_WORKSPACE (1 << 25) /* bytes */
 
 typedef struct gvr_cache {
   void* data;           /* device, 16-byte aligned */
@@ -125,17 +125,15 @@ gvr_status cache_read(const gvr_cache* cache, const int32_t* slots, int64_t num_
  *   indices int32 [num_rows][k]: the entries that the row attends to, as topk_decode writes them;
  *           NULL: all n_r entries (k is then ignored).  An index outside [0, n_r) (the -1 pad, the
  *           -2 of a failed row) is skipped; one that occurs twice counts twice.
- *   scale   factor of the scores q . k, finite (1 / sqrt(head_dim) is usual).
+ *   scale   factor of the scores q . k (1 / sqrt(head_dim) is usual); scale * k_scale finite in fp32.
  *   out     [num_rows][num_heads][head_dim] of `dtype`, packed, 16-byte aligned: softmax over the
  *           row's entries times V.  A row without entries gets zeros.
  *   lse     optional fp32 [num_rows][num_heads]: log of the sum of exp(scale * q . k); -infinity
  *           for a row without entries.  (Merges this with attention over other entries.)
- *   workspace  optional device memory, 16-byte aligned, of any content and size: rows of very many
- *           entries in a small batch are then split over more of the device, as far as
- *           workspace_bytes goes (GVR_ATTEND_WORKSPACE is always enough).  Its content is not kept:
- *           calls that can overlap on the GPU, or graphs whose replays can, need one each.
- * Every wait for the kernel's own copies is bounded (0.5 s).  If one gives up -- not expected on a
- * healthy GPU -- the outputs of the query heads concerned are NaN.
+ *   workspace  optional device memory, 16-byte aligned, of any content and size: with it, rows of
+ *           many entries and of unequal lengths are spread evenly over the device, in two kernels,
+ *           where workspace_bytes is enough (GVR_ATTEND_WORKSPACE always is).  Its content is not
+ *           kept: calls that can overlap on the GPU, or graphs whose replays can, need one each.
  * Scores, softmax and sums are fp32; K and V values are exact; probabilities are rounded to
  * 11-bit significands before they multiply V.
  */

@@ -53,7 +53,7 @@ def _declare(lib):
     lib.gvr_cache_status_string.restype = ctypes.c_char_p
 
 
-_WORKSPACE = 1 << 20  # GVR_ATTEND_WORKSPACE
+_WORKSPACE = 1 << 25  # GVR_ATTEND_WORKSPACE
 _LONG = 8192  # selections over this many entries a row get a workspace, as whole caches do
 
 _lib = None

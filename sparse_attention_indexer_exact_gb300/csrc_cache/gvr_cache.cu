@@ -305,7 +305,8 @@ __device__ __forceinline__ uint8_t* row_of(const CopyParams& p, int slot, int he
 
 // D / 8 neighbouring lanes take the K and V of one token and head, eight values of each a lane: a warp
 // reads (or, for cache_read, writes) 512 neighbouring bytes at a time, and writes 128 (64) of codes.
-// Bound by these bytes; 16333 tokens x 8 heads of 128 in bf16: APPEND_US, READ_US.
+// 16333 tokens x 8 heads of 128 in bf16, 86 MB in and out: append 19.6 us (4.4 TB/s; the conversion of four
+// elements a clock and SM partition, about 11 us, is not all hidden), read 14.6 us (5.9 TB/s; bound by bytes).
 template <int D, bool BF16>
 __global__ void __launch_bounds__(COPY_THREADS) cache_append_kernel(CopyParams p) {
   constexpr int LANES = D / 8;

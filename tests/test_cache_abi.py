@@ -176,6 +176,17 @@ def test_attend_prefill_refusals(lib):
     assert call(rows=0, q=None, out=None, table=None, req=None, starts=None, ends=None, indices=None) == 0
 
 
+def test_attend_refuses_a_factor_beyond_fp32(lib):
+    """scale and k_scale are finite, their product is not."""
+    names = ["q", "qr", "qh", "dtype", "rows", "heads", "table", "stride", "width", "lens", "next_n", "cr", "indices", "k",
+             "scale", "out", "lse", "ws", "ws_bytes", "stream"]
+    call = caller(lib.attend_decode, names, dict(ATTEND, lens=A, next_n=2, cr=4))
+    for scale in (3e38, -3e38):
+        assert call(scale=scale) == ARG
+        assert call(cache=dict(k_scale=10.0), scale=scale) == ARG
+    assert call(cache=dict(k_scale=1e38), scale=10.0) == ARG
+
+
 def test_bindings_refuse_host_tensors_and_wrong_shapes(gvr):
     torch = pytest.importorskip("torch")
     cache = torch.zeros(4, 16, 2, 144, dtype=torch.uint8)

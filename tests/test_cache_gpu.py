@@ -202,14 +202,18 @@ def compare(out, lse, ref, cache, dim, vs=1.0):
 
 
 def decode_case(gvr, seed, dim, dtype, kv_heads, group, ps, next_n, cr, lens, k, ks=1.0, vs=1.0, scale=None, qsize=1.0,
-                spoil=True, spread=0.5):
+                spoil=True, spread=0.5, pages=None):
     g = np.random.default_rng(seed)
     lens = np.asarray(lens)
     requests, rows = len(lens), len(lens) * next_n
     width = max(1, -(-(int(lens.max()) // cr) // ps))
-    pages = requests * width + 2
-    cache = random_cache(g, pages, ps, kv_heads, dim, spread)
-    table = g.permutation(pages)[:requests * width].reshape(requests, width)
+    if pages is None:
+        pages = requests * width + 2
+        cache = random_cache(g, pages, ps, kv_heads, dim, spread)
+        table = g.permutation(pages)[:requests * width].reshape(requests, width)
+    else:  # requests share them
+        cache = random_cache(g, pages, ps, kv_heads, dim, spread)
+        table = g.integers(0, pages, (requests, width))
     entries = cc.row_entries(lens, next_n, cr, rows, width * ps)
     if spoil and width > 1:
         table[0, 0], table[-1, -1] = -1, pages
@@ -377,6 +381,209 @@ def test_same_result_every_time(gvr):
     torch.cuda.synchronize()
     for out, lse in got:
         assert np.array_equal(host(out), first[0]) and np.array_equal(host(lse), first[1])
+
+
+# -------------------------------------------------- whole caches in equal shares, joined by a second kernel
+@pytest.mark.parametrize("dim,dtype,kv_heads,group,next_n", [(64, "bf16", 1, 1, 1), (64, "f16", 4, 6, 2), (64, "bf16", 3, 33, 1),
+                                                             (128, "bf16", 8, 4, 1), (128, "f16", 2, 8, 3), (128, "f16", 6, 12, 1),
+                                                             (256, "bf16", 2, 8, 1), (256, "f16", 1, 5, 2)])
+@pytest.mark.parametrize("lens", [[1537], [0, 0, 1602, 0], [1] * 40 + [1999], [1536, 33, 0, 32, 31, 1700, 2, 1569, 800, 64],
+                                  [4000, 3999]])
+def test_decode_shares(gvr, dim, dtype, kv_heads, group, next_n, lens):
+    """One request over all shares, idle ones at the ends, many within one share, ends on and beside steps."""
+    decode_case(gvr, dim + len(lens), dim, dtype, kv_heads, group, 16, next_n, 1, lens, 0, pages=80)
+
+
+@pytest.mark.parametrize("requests", [150, 301, 1024, 1025])
+def test_decode_shares_of_many_requests(gvr, requests):
+    """Up to and beyond what is cut into equal shares; one long request among short ones."""
+    g = np.random.default_rng(requests)
+    lens = g.integers(0, 20, requests)
+    lens[requests // 3] = 1600
+    decode_case(gvr, requests, 64, "bf16", 1, 2, 32, 1, 1, lens, 0, pages=60)
+
+
+@pytest.mark.parametrize("length", [40, 2000])
+def test_decode_shared_entries_of_partial_requests(gvr, length):
+    """A last request of which only some rows are there, and lengths that some rows of a request share."""
+    g = np.random.default_rng(length)
+    ps, next_n, cr, width = 16, 4, 2, 130
+    cache, table = random_cache(g, 2 * width, ps, 2, 64), g.permutation(2 * width).reshape(2, width)
+    lens, rows = np.array([length, length + 3]), 6
+    q = torch.as_tensor(g.standard_normal((rows, 6, 64))).to(torch.bfloat16).to(DEV)
+    out, lse = gvr.attend_decode(q, dev(cache, torch.uint8), dev(table), dev(lens), next_n, cr, want_lse=True)
+    ref = cc.attend(host(q), cache, table, cc.row_entries(lens, next_n, cr, rows, width * ps), [0, 0, 0, 0, 1, 1], None, 1 / 8)
+    compare(out, lse, ref, torch.as_tensor(cache), 64)
+
+
+@pytest.mark.parametrize("length,next_n,cr", [(70, 3, 1), (97, 4, 2), (2050, 3, 1), (4100, 4, 2)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_decode_nan_behind_a_row_that_others_see(gvr, length, next_n, cr, dim):
+    """A NaN that the last row of a request sees and the rows before it do not."""
+    g = np.random.default_rng(length)
+    ps, width = 16, -(-length // 16)
+    cache = random_cache(g, width, ps, 1, dim)
+    lens, table = np.array([length]), np.arange(width)[None]
+    entries = cc.row_entries(lens, next_n, cr, next_n, width * ps)
+    q = torch.as_tensor(g.standard_normal((next_n, 3, dim))).to(torch.float16).to(DEV)
+    bad = cache.copy()
+    bad.reshape(width * ps, -1)[entries[-1] - 1:] = 0xff
+    out, lse = gvr.attend_decode(q, dev(bad, torch.uint8), dev(table), dev(lens), next_n, cr, want_lse=True)
+    ref = cc.attend(host(q), cache, table, entries, [0] * next_n, None, 1 / math.sqrt(dim))
+    clean = [r for r in range(next_n) if entries[r] < entries[-1]]
+    assert 0 < len(clean) < next_n
+    compare(out[clean], lse[clean], [x[clean] for x in ref], torch.as_tensor(cache), dim)
+    last = [r for r in range(next_n) if r not in clean]
+    assert np.isnan(host(out)[last]).all() and np.isnan(host(lse)[last]).all()
+
+
+def test_decode_shares_of_idle_requests_and_no_table(gvr):
+    """A wide table of requests without entries, and a table without columns: zeros, whatever out held."""
+    g = np.random.default_rng(2)
+    cache = dev(random_cache(g, 4, 16, 2, 128), torch.uint8)
+    q = torch.as_tensor(g.standard_normal((3, 4, 128))).to(torch.bfloat16).to(DEV)
+    wide = torch.zeros(3, 200, dtype=torch.int32, device=DEV)
+    for t, lens in ((wide, [0, 0, -5]), (wide[:, :0], [9, 4000, 0]), (torch.empty(3, 0, dtype=torch.int32, device=DEV), [1, 2, 3])):
+        out, lse = torch.full_like(q, 7), torch.full((3, 4), 7.0, device=DEV)
+        gvr.attend_decode(q, cache, t, dev(lens), 1, 1, out=out, lse=lse)
+        assert (host(out) == 0).all() and (host(lse) == -np.inf).all()
+
+
+@pytest.mark.parametrize("k", [8193, 9001])
+def test_long_selections(gvr, k):
+    """Selections long enough to be cut into shares, for decode rows and prefill rows, -1 pads among them."""
+    g = np.random.default_rng(k)
+    lens = np.array([9500, 700, 0, 8200])
+    decode_case(gvr, k, 64, "bf16", 2, 3, 16, 1, 1, lens, k)
+    width = 600
+    cache, table = random_cache(g, 2 * width, 16, 2, 64), g.permutation(2 * width).reshape(2, width)
+    req, starts, ends = np.array([1, 0, 5, 0]), np.array([3, 0, 0, 40]), np.array([9303, 9600, 70, 1000])
+    n = [9300, 9600, 70, 960]
+    idx = np.full((4, k), -1)
+    for r in range(4):
+        m = min(n[r], k)
+        idx[r, :m] = g.permutation(n[r])[:m]
+    q = torch.as_tensor(g.standard_normal((4, 6, 64))).to(torch.float16).to(DEV)
+    out, lse = gvr.attend_prefill(q, dev(cache, torch.uint8), dev(table), dev(req), dev(starts), dev(ends), dev(idx), want_lse=True)
+    compare(out, lse, cc.attend(host(q), cache, table, n, req, idx, 1 / 8), torch.as_tensor(cache), 64)
+
+
+# ------------------------------------------------------------------------------- how calls are made
+def long_case(g):
+    cache, table = dev(random_cache(g, 300, 16, 2, 64), torch.uint8), dev(g.permutation(300).reshape(2, 150))
+    q = torch.as_tensor(g.standard_normal((4, 8, 64))).to(torch.bfloat16).to(DEV)
+    return q, cache, table, dev([2300, 1900]), 2, 1
+
+
+def test_shares_at_once_and_in_two_graphs(gvr):
+    """The same bits from calls on three streams at once, and from two captured graphs replayed beside each other."""
+    args = [long_case(np.random.default_rng(i)) for i in range(3)]
+    first = [[host(x) for x in gvr.attend_decode(*a, want_lse=True)] for a in args]
+    streams, got, graphs = [torch.cuda.Stream() for _ in range(3)], [], []
+    for i in range(2):
+        graphs.append((torch.cuda.CUDAGraph(), []))
+        with torch.cuda.graph(graphs[i][0]):
+            for _ in range(3):
+                graphs[i][1].append(gvr.attend_decode(*args[i], want_lse=True))
+    torch.cuda.synchronize()
+    for i in range(12):
+        with torch.cuda.stream(streams[i % 3]):
+            got.append((i % 3, gvr.attend_decode(*args[i % 3], want_lse=True)))
+    for _ in range(4):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i][0].replay()
+    torch.cuda.synchronize()
+    for i, graph in enumerate(graphs):
+        got += [(i, x) for x in graph[1]]
+    for i, (out, lse) in got:
+        assert np.array_equal(host(out), first[i][0]) and np.array_equal(host(lse), first[i][1])
+
+
+def every_call(gvr, **kw):
+    """One call of each entry point; what they return, on the host."""
+    g = np.random.default_rng(6)
+    cache = gvr.cache_alloc(12, 16, 2, 64, DEV)
+    kv = torch.as_tensor(g.standard_normal((2, 90, 2, 64))).to(torch.float16).to(DEV)
+    q = torch.as_tensor(g.standard_normal((2, 4, 64))).to(torch.float16).to(DEV)
+    table = torch.full((2, 6), -1, dtype=torch.int32, device=DEV)
+    zero, lens, free, idx = dev([0, 0]), dev([50, 40]), dev(np.arange(12)[::-1].copy()), dev(g.integers(-1, 40, (2, 33)))
+    torch.cuda.synchronize()
+    slots, counts = gvr.cache_tables(zero, lens, free, table, 90, 16, **kw)
+    gvr.cache_append(kv[0], kv[1], cache, slots, v_scale=0.5, **kw)
+    got = [slots, counts, table, *gvr.cache_read(cache, slots, 64, torch.float16, v_scale=0.5, **kw)]
+    got += gvr.attend_decode(q, cache, table, lens, 1, 1, idx, want_lse=True, **kw)
+    got += gvr.attend_decode(q, cache, table, lens, 1, 1, scale=0.3, want_lse=True, **kw)
+    got += gvr.attend_prefill(q, cache, table, dev([1, 0]), zero, lens, idx, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    return [host(x) for x in got]
+
+
+def test_streams_given(gvr):
+    """stream= as a torch stream and as a raw handle: the same results as on the current one."""
+    want, s = every_call(gvr), torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        for a, b in zip(every_call(gvr, stream=stream), want):
+            assert np.array_equal(a, b)
+
+
+def test_short_way_and_checked_way_agree(gvr, monkeypatch):
+    """Ordinary calls take the native short way; the checked way behind it gives the same results."""
+    from sparse_attention_indexer_exact_gb300 import cache as mod
+    short, names, taken = mod._short(), ["cache_tables", "cache_append", "cache_read", "attend_decode", "attend_prefill"], []
+
+    class Watched:
+        pass
+
+    def watch(name, through):
+        def call(*args):
+            got = getattr(short, name)(*args) if through else None
+            taken.append((name, got is not None))
+            return got
+        return call
+
+    results = []
+    for through in (True, False):
+        w = Watched()
+        for name in names:
+            setattr(w, name, watch(name, through))
+        monkeypatch.setattr(mod, "_native", w)
+        taken.clear()
+        results.append(every_call(gvr))
+        assert {n for n, _ in taken} == set(names) and all(t == through for _, t in taken)
+    for a, b in zip(*results):
+        assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("apart", [False, True])
+def test_caches_beyond_32_bits(gvr, apart):
+    """Entries more than 2^32 bytes from the cache's start; with pages apart, more than 2^31 16-byte units."""
+    g = np.random.default_rng(9)
+    ps, heads, dim, pages = 16, 2, 128, 1000
+    stride = 36 * 10 ** 6 // 16 * 16 + 16 if apart else 16 * 2 * 144
+    if not apart:
+        pages = (1 << 32) // stride + 500
+    memory = torch.empty(pages * stride, dtype=torch.uint8, device=DEV)
+    cache = memory.as_strided((pages, ps, heads, 144), (stride, heads * 144, 144, 1))
+    used = np.concatenate([[0], pages - 1 - g.permutation(400)[:9]])
+    table, lens = g.permutation(used)[None], np.array([ps * 10 - 3])
+    e = np.arange(lens[0])
+    slots = table[0][e // ps] * ps + e % ps
+    k, v = (torch.as_tensor(g.standard_normal((lens[0], heads, dim))).to(torch.bfloat16).to(DEV) for _ in range(2))
+    gvr.cache_append(k, v, cache, dev(slots))
+    rows = host(cache[dev(used, torch.int64)])
+    small = np.argsort(used)[np.searchsorted(np.sort(used), table[0])][None]  # the same table over the used pages alone
+    packed = cc.pack(host(k), host(v))
+    assert np.array_equal(rows.reshape(-1, heads, 144)[small[0][e // ps] * ps + e % ps], packed)
+    back = gvr.cache_read(cache, dev(slots), dim)
+    want = cc.unpack(packed, dim)
+    assert all(np.array_equal(host(b), w) for b, w in zip(back, want))
+    q = torch.as_tensor(g.standard_normal((1, 8, dim))).to(torch.bfloat16).to(DEV)
+    idx = g.permutation(lens[0])[:100][None]
+    for i in (None, idx):
+        out, lse = gvr.attend_decode(q, cache, dev(table), dev(lens), 1, 1, None if i is None else dev(i), want_lse=True)
+        ref = cc.attend(host(q), rows, small, lens, [0], i, 1 / math.sqrt(dim))
+        compare(out, lse, ref, torch.as_tensor(packed[:, None]), dim)
 
 
 # ----------------------------------------------------------------------------- a step together
