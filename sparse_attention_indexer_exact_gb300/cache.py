@@ -1,9 +1,10 @@
 """The 4-bit paged cache and the attention that reads it at the selected entries.
 
 Bindings of ``include/gvr_cache.h``, in the manner of the package's top-K calls: tensors are
-checked and turned into addresses here, everything else happens in one kernel per call (two for few
-rows of very many entries) on the current stream of the tensors' device, or on the one given as
-``stream=`` to any of the calls.  A decode step, in call order::
+checked and turned into addresses here, everything else happens in one kernel per call (two for
+attention over whole caches of many entries) on the current stream of the tensors' device, or on the
+one given as ``stream=`` to any of the calls.  They are for serving: no gradient passes through them.
+A decode step, in call order::
 
     slots, counts = cache_tables(cached_lens, kv_lens, free_pages, block_table, new, page_size, cr)
     cache_append(k, v, cache, slots)                       # cache = cache_alloc(pages, page_size, heads, dim)
@@ -325,8 +326,8 @@ def _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse):
 
 
 def _workspace(device):
-    """Scratch of one call: from torch's allocator, so each call on each stream has its own, and a
-    captured graph keeps its own."""
+    """Scratch of one call (32 MB): from torch's allocator, so each call on each stream has its own, and
+    a captured graph keeps its own."""
     import torch
     return torch.empty(_WORKSPACE, dtype=torch.uint8, device=device)
 
