@@ -306,19 +306,21 @@ __device__ __forceinline__ uint8_t* row_of(const CopyParams& p, int slot, int he
 
 // D / 8 neighbouring lanes take the K and V of one token and head, eight values of each a lane: a warp
 // reads (or, for cache_read, writes) 512 neighbouring bytes at a time, and writes 128 (64) of codes.
-// 16333 tokens x 8 heads of 128 in bf16, 86 MB in and out: append 19.6 us (4.4 TB/s; the conversion of four
-// elements a clock and SM partition, about 11 us, is not all hidden), read 14.6 us (5.9 TB/s; bound by bytes).
+// 16333 tokens x 8 heads of 128 in bf16, 86 MB in and out: append 17.9 us (4.8 TB/s; the conversions,
+// about 11 us of issue, are not all hidden), read 14.4 us (6.0 TB/s; bound by bytes).  Two rows a thread: 18.7.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(COPY_THREADS) cache_append_kernel(CopyParams p) {
   constexpr int LANES = D / 8;
   begin();
   const uint32_t th = blockIdx.x * uint32_t(COPY_THREADS / LANES) + threadIdx.x / LANES, t = p.heads_log2 >= 0 ? th >> p.heads_log2 : th / p.heads;
   const int h = int(th - t * p.heads), b = threadIdx.x % LANES;
-  uint8_t* row = t < p.tokens ? row_of(p, p.slots[t], h, row_bytes(D)) : nullptr;
+  uint8_t* row = nullptr;
   uint4 k = make_uint4(0, 0, 0, 0), v = k;
-  if (row) {
+  if (t < p.tokens) {  // read whether it has a slot or not, beside its slot: 17.9 us, one after the other 19.4
+    const int slot = __ldg(p.slots + t);
     k = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k) + int64_t(t) * p.k_token + h * p.k_head) + b);
     v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + int64_t(t) * p.v_token + h * p.v_head) + b);
+    row = row_of(p, slot, h, row_bytes(D));
   }
   uint32_t kc, vc;
   const uint32_t ks = quantise<BF16>(k, p.k_scale, kc), vs = quantise<BF16>(v, p.v_scale, vc);  // by all lanes
