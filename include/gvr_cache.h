@@ -99,7 +99,7 @@ gvr_status cache_tables(const int32_t* cached_lens, const int32_t* kv_lens, int6
  * Quantise K and V rows into the cache: k and v are [num_tokens][num_kv_heads][head_dim] of
  * `dtype` with unit inner stride and the given token and head strides (in elements, multiples of
  * 8; bases 16-byte aligned); token t goes to slots[t].  Slots that name an entry must be
- * distinct: which token's values an entry named twice holds is unspecified.
+ * distinct: what an entry named twice holds is unspecified (nothing else is affected).
  * num_tokens * num_kv_heads < 2^31.
  */
 gvr_status cache_append(const gvr_cache* cache, const void* k, int64_t k_token_stride,

@@ -92,7 +92,10 @@ def _current(stream, tensor):
     allocates then belongs to the stream that uses it."""
     import torch
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream, tensor.device)
+        # handle 0 is the default stream; to ExternalStream it would mean a new one
+        stream = torch.cuda.ExternalStream(stream, tensor.device) if int(stream) else torch.cuda.default_stream(tensor.device)
+    if stream.device != tensor.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {tensor.device}")
     return torch.cuda.stream(stream)
 
 

@@ -527,6 +527,21 @@ def test_streams_given(gvr):
             assert np.array_equal(a, b)
 
 
+def test_default_stream_by_its_handle_and_streams_of_other_devices(gvr):
+    """stream=0 is the default stream, not a new one; a stream of another device is refused."""
+    from types import SimpleNamespace
+
+    from sparse_attention_indexer_exact_gb300.cache import _current
+    t = torch.zeros(1, device=DEV)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with _current(0, t):
+            assert torch.cuda.current_stream() == torch.cuda.default_stream()
+        for a, b in zip(every_call(gvr, stream=0), every_call(gvr)):
+            assert np.array_equal(a, b)
+    with pytest.raises(ValueError):
+        _current(torch.cuda.Stream(), SimpleNamespace(device=torch.device("cuda", 1)))
+
+
 def test_short_way_and_checked_way_agree(gvr, monkeypatch):
     """Ordinary calls take the native short way; the checked way behind it gives the same results."""
     from sparse_attention_indexer_exact_gb300 import cache as mod
