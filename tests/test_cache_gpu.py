@@ -403,6 +403,24 @@ def test_decode_shares_of_many_requests(gvr, requests):
     decode_case(gvr, requests, 64, "bf16", 1, 2, 32, 1, 1, lens, 0, pages=60)
 
 
+@pytest.mark.parametrize("room", [16, 100_000, 1_000_000, 1 << 25])
+@pytest.mark.parametrize("dim,kv_heads,group,next_n,lens", [(64, 4, 6, 2, [1700, 5, 3000]), (64, 3, 33, 1, [2100] * 3),
+                                                            (128, 8, 4, 1, [4000]), (128, 2, 16, 1, [1999, 1, 0, 1800]),
+                                                            (256, 2, 3, 2, [1600, 1700])])
+def test_decode_shares_as_far_as_the_workspace_goes(gvr, monkeypatch, room, dim, kv_heads, group, next_n, lens):
+    """A workspace without room for the shares (long rows in clusters), with just some and with enough: the same sums,
+    and nothing written behind it."""
+    from types import SimpleNamespace
+
+    from sparse_attention_indexer_exact_gb300 import cache as mod
+    buf = torch.full((room + 4096,), 171, dtype=torch.uint8, device=DEV)
+    monkeypatch.setattr(mod, "_native", SimpleNamespace(attend_decode=lambda *a: None))
+    monkeypatch.setattr(mod, "_WORKSPACE", room)
+    monkeypatch.setattr(mod, "_workspace", lambda device: buf[:room])
+    decode_case(gvr, dim + room % 7, dim, "bf16", kv_heads, group, 16, next_n, 1, lens, 0, pages=90)
+    assert (buf[room:] == 171).all()
+
+
 @pytest.mark.parametrize("length", [40, 2000])
 def test_decode_shared_entries_of_partial_requests(gvr, length):
     """A last request of which only some rows are there, and lengths that some rows of a request share."""
