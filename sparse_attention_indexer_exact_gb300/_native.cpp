@@ -5,18 +5,21 @@
 // return its results, or return None where anything is out of the ordinary: a wrong type or shape,
 // another device than the current one, a refusal by the library.  cache.py then takes its own way,
 // which does the same step by step and raises the error that names what is wrong.  Measured on a
-// GB300's host: 20 us a call of attend_decode through Python and ctypes.
+// GB300's host: 20 us a call of attend_decode through Python and ctypes, 3.9 this way (1.9 without outputs to
+// allocate).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/core/LegacyTypeDispatch.h>
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 
 #include "gvr_cache.h"
 
@@ -64,8 +67,10 @@ struct Where {
     need(t.is_cuda() && t.device().index() == device && t.scalar_type() == type && t.layout() == at::kStrided);
     return t;
   }
+  // From torch's allocator on the current stream, without the dispatcher (1.1 -> 0.6 us each).
   Tensor empty(at::IntArrayRef size, at::ScalarType type) const {
-    return at::empty(size, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, device)));
+    return at::detail::empty_generic(size, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type,
+                                     std::nullopt);
   }
 };
 
@@ -156,7 +161,7 @@ PyObject* append(PyObject* const* a) {
   Py_RETURN_TRUE;
 }
 
-// (cache, slots, head_dim, like, k_scale, v_scale): `like` is a tensor of the wanted type
+// (cache, slots, head_dim, kind, k_scale, v_scale): kind is the wanted type, as in gvr_cache.h
 PyObject* read(PyObject* const* a) {
   const Where w;
   const gvr_cache c = cache_of(w, tensor(a[0]), number(a[4]), number(a[5]));
@@ -166,8 +171,8 @@ PyObject* read(PyObject* const* a) {
   need(kind == GVR_BF16 || kind == GVR_F16);
   const int32_t* at = int32s(w, slots, 0);
   const int64_t n = slots.size(0);
-  const Tensor kv = w.empty({2, n, c.num_kv_heads, c.head_dim}, kind == GVR_BF16 ? at::kBFloat16 : at::kHalf);
-  const Tensor k = kv.select(0, 0), v = kv.select(0, 1);
+  const at::ScalarType type = kind == GVR_BF16 ? at::kBFloat16 : at::kHalf;
+  const Tensor k = w.empty({n, c.num_kv_heads, c.head_dim}, type), v = w.empty({n, c.num_kv_heads, c.head_dim}, type);
   need(cache_read(&c, at, n, kind, k.data_ptr(), v.data_ptr(), w.stream) == GVR_OK);
   return pair(k, v);
 }
