@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(THREADS) cache_tables_kernel(TableParams p) {
       for (int i = 0; i < VEC; ++i) {
         const int64_t t = t4 + i;
         if (t >= total_entries) break;
-        while (r + 1 < p.requests && entry_first[r + 1] <= t) ++r, at_block = -1;
+        if (r + 1 < p.requests && entry_first[r + 1] <= t) r = owner(entry_first, p.requests, int(t)), at_block = -1;
         const int64_t entry = int64_t(held[r]) + (t - entry_first[r]), block = entry >> p.page_shift;
         if (block != at_block) {  // mostly once
           const int have = pages_of(held[r], p.page_shift);
