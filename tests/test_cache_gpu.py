@@ -83,6 +83,18 @@ def test_tables_borders(gvr):
     check_tables(gvr, [3, 0], [5, 2], [1], t, 4, 16, 1)
 
 
+@pytest.mark.parametrize("grow,new", [([0, 700, 1999], 9), ([3, 4, 1998], 2), ([1999], 1), ([], 0), ([0], 40)])
+def test_tables_of_mostly_idle_requests(gvr, grow, new):
+    """Runs of requests without new entries between the few that have some, within four neighbouring slots too."""
+    g = np.random.default_rng(new)
+    cached = g.integers(0, 60, 2000)
+    lens = cached.copy()
+    lens[grow] += new
+    table, free = g.permutation(2000 * 13)[:2000 * 13].reshape(2000, 13), 26000 + g.permutation(30)
+    for max_new in (0, 7, 20000):
+        check_tables(gvr, cached, lens, free, table, max_new, 8, 1)
+
+
 def test_tables_most_requests(gvr):
     n = gvr.MAX_CACHE_REQUESTS
     g = np.random.default_rng(5)
@@ -341,6 +353,28 @@ def test_decode_masked_nan_stays_out(gvr):
     assert np.isfinite(host(out)[0, :2]).all() and np.isnan(host(out)[0, 2:]).all() and np.isnan(host(lse)[0, 2:]).all()
 
 
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("length,next_n,k,dtype", [(90, 1, 40, "bf16"), (90, 2, 0, "f16"), (2000, 2, 0, "bf16"), (2000, 1, 0, "f16")])
+def test_decode_bad_query_stays_in_its_head(gvr, bad, length, next_n, k, dtype):
+    """A query that is not finite spoils its own row and head, none that it shares a job with."""
+    g = np.random.default_rng(length)
+    cache, table, rows = random_cache(g, 130, 16, 2, 128), g.permutation(130)[:125][None], next_n
+    lens = np.array([length])
+    idx = g.permutation(length - next_n)[None, :k].repeat(rows, 0) if k else None
+    q = torch.as_tensor(g.standard_normal((rows, 12, 128))).to(DT[dtype]).to(DEV)
+    ref = cc.attend(host(q), cache, table, cc.row_entries(lens, next_n, 1, rows, 2000), [0] * rows, idx, 1 / math.sqrt(128))
+    q[0, 4, 77] = bad
+    out, lse = gvr.attend_decode(q, dev(cache, torch.uint8), dev(table), dev(lens), next_n, 1, None if idx is None else dev(idx),
+                                 want_lse=True)
+    assert not np.isfinite(host(out)[0, 4]).any() and not np.isfinite(host(lse)[0, 4])
+    fine = np.ones((rows, 12), bool)
+    fine[0, 4] = False
+    out, lse, ref = out.reshape(-1, 128), lse.reshape(-1), [x.reshape(rows * 12, *x.shape[2:]) if x.ndim > 1 else x.repeat(12) for x in ref]
+    keep = np.flatnonzero(fine.reshape(-1))
+    compare(out[keep][:, None], lse[keep][:, None], [x[keep][:, None] if i < 4 else x[keep] for i, x in enumerate(ref)],
+            torch.as_tensor(cache), 128)
+
+
 @pytest.mark.parametrize("dim,dtype,group,kv_heads,k", [(64, "f16", 8, 2, 40), (128, "bf16", 8, 1, 512), (256, "bf16", 3, 2, 100)])
 def test_prefill_selected(gvr, dim, dtype, group, kv_heads, k):
     g = np.random.default_rng(dim)
@@ -586,6 +620,41 @@ def test_short_way_and_checked_way_agree(gvr, monkeypatch):
         assert {n for n, _ in taken} == set(names) and all(t == through for _, t in taken)
     for a, b in zip(*results):
         assert np.array_equal(a, b)
+
+
+FIRST_CALLS = """
+import sys, torch
+import sparse_attention_indexer_exact_gb300 as gvr
+d = "cuda:0"
+q, k = torch.randn(2, 8, 128, device=d).half(), torch.randn(20, 2, 128, device=d).half()
+cache, table = torch.zeros(300, 16, 2, 144, dtype=torch.uint8, device=d), torch.arange(300, device=d).int().view(2, 150)
+lens, cached, free = torch.tensor([2000, 40], device=d).int(), torch.tensor([1990, 30], device=d).int(), torch.arange(10, device=d).int()
+idx = torch.arange(64, device=d).int().view(2, 32)
+def step():
+    slots, counts = gvr.cache_tables(cached, lens, free, table, 20, 16)
+    gvr.cache_append(k, k, cache, slots)
+    return [slots, counts, *gvr.cache_read(cache, slots, 128), *gvr.attend_decode(q, cache, table, lens, 1, 1, want_lse=True),
+            *gvr.attend_decode(q, cache, table, lens, 1, 1, idx, want_lse=True)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+graph.replay()
+got = [x.clone() for x in captured]
+assert got[1].tolist() == [20, 1, 0]
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("the same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured(gvr):
+    """Nothing of a first call (attributes, lookups, loading) is at odds with a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "the same" in run.stdout, run.stderr[-2000:]
 
 
 @pytest.mark.parametrize("apart", [False, True])
