@@ -227,7 +227,7 @@ struct Listed {
   }
   void* at() const { return workspace.defined() ? workspace.data_ptr() : nullptr; }
 
-  static constexpr int64_t LONG = 8192;  // as in cache.py
+  static constexpr int64_t LONG = 2048;  // as in cache.py
 };
 
 // (q, cache, k_scale, v_scale, scale, out, lse, want_lse, block_table, kv_lens, next_n, compress_ratio, indices)

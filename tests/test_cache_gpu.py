@@ -501,7 +501,7 @@ def test_decode_shares_of_idle_requests_and_no_table(gvr):
         assert (host(out) == 0).all() and (host(lse) == -np.inf).all()
 
 
-@pytest.mark.parametrize("k", [8193, 9001])
+@pytest.mark.parametrize("k", [2047, 2049, 8193, 9001])
 def test_long_selections(gvr, k):
     """Selections long enough to be cut into shares, for decode rows and prefill rows, -1 pads among them."""
     g = np.random.default_rng(k)
