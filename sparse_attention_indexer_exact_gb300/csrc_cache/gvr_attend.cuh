@@ -689,8 +689,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, FOLD ? Shape<D, NT>::FO
 // many equal ranges as there are CTAs (of a group of heads and a query tile, blockIdx.y).  A CTA walks over
 // its range, unit by unit, and writes a piece for each: piece c + u of CTA c and unit u, which is unique, as
 // both only grow along the steps.  A warp has a head: CTAs of four neighbouring heads, whose rows lie next
-// to each other, took 46.9 us where CTAs of two took 53.3 (48 requests of 1 to 16384 entries, 4 KV heads of
-// 64) and clusters, one a unit, 73.5; 131071 entries of one request, 8 KV heads of 128: 40.3, 42.7 and 46.9.
+// to each other, took 46.2 us where CTAs of two took 53.3 (48 requests of 1 to 16384 entries, 4 KV heads of
+// 64) and clusters, one a unit, 73.5; 131071 entries of one request, 8 KV heads of 128: 40.5, 42.7 and 46.9.  The join starts while
+// the last pieces are written: 0.3 to 0.5 us (from the start of this kernel on its CTAs would lie unevenly: up to 2 more).
 __device__ __forceinline__ int range_start(int c, int ctas, int steps) { return int(int64_t(c) * steps / ctas); }
 
 template <int D, int NT, bool FOLD>
@@ -741,6 +742,7 @@ __global__ void __launch_bounds__(128, Shape<D, NT>::BALANCED_WARPS / 4) balance
       float o[NT][KSTEPS][4], top[NT][2], total[NT][2];
       walk<D, NT, FOLD>(p, u, h, m0, first, 1, mine, min(u.listed, uint32_t(first + mine) * STEP), smem + warp * S::RING,
                         reinterpret_cast<uint32_t*>(smem + warps * S::RING) + warp * STEP, raw, o, top, total);
+      if (at + mine == last) let_next_start();  // all that is left is this piece
       float* piece = pieces + int64_t(int(blockIdx.x) + unit) * (S::Q * (D + 2));
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -770,7 +772,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(AttendParams p) {
   __shared__ int sums[2][WARPS];
   const int unit = blockIdx.x, tid = threadIdx.x;
   const int tile = blockIdx.y / p.kv_heads, h = int(blockIdx.y) - tile * p.kv_heads;
-  begin();
   int before = 0, steps = 0;  // of the units before this one, of all
   for (int i = tid; i < p.units; i += JOIN_THREADS) {
     const int x = steps_of(load_unit<FOLD>(p, i).listed);
@@ -796,6 +797,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(AttendParams p) {
   const bool is = qi < S::Q;
   const int group = tile * p.head_groups + h / p.heads_in;
   const float* src = p.pieces + (int64_t(group * p.heads_in + h % p.heads_in) * (p.balanced_ctas + p.units) + first + unit) * PIECE;
+  begin();  // so far only what balanced_kernel has found written, too
   float all = NO_TOP, sum = 0.f, acc[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = 0.f;

@@ -67,10 +67,13 @@ inline cudaError_t launch(const void* kernel, dim3 grid, int threads, int smem, 
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-// Waits until the kernel before this one is complete and its writes are visible.  (No kernel lets the
-// next one start earlier than at its end: CTAs that wait in the free slots of a running kernel lie
-// unevenly over the SMs, and a decode batch took 70 us instead of 43.)
+// Waits until the kernel before this one is complete and its writes are visible.  (No kernel but one
+// lets the next one start earlier than at its end: CTAs that wait in the free slots of a running kernel
+// lie unevenly over the SMs, and a decode batch took 70 us instead of 43.)
 __device__ __forceinline__ void begin() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next kernel start once every CTA of this one has come here, after begin(), or has ended.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------------------- conversions
 // Four bytes of two e2m1 codes each -> four f16x2, low half from the low four bits.  Exact.
