@@ -171,11 +171,12 @@ struct Shape {
 template <int D>
 __device__ __forceinline__ void write_out(const AttendParams& p, int64_t row, int head, int d, float all, float sum,
                                           const float (&acc)[8]) {
-  const float norm = sum == 0.f ? 0.f : p.v_scale / sum;
+  // v_scale last: v_scale / sum would lose bits, or all, of a small factor over many entries
+  const float norm = sum == 0.f ? 0.f : 1.f / sum;
   uint32_t packed[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float lo = acc[2 * j] * norm, hi = acc[2 * j + 1] * norm;
+    const float lo = acc[2 * j] * norm * p.v_scale, hi = acc[2 * j + 1] * norm * p.v_scale;
     if (p.bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed[j]) : "f"(hi), "f"(lo));
     else packed[j] = pack_f16(lo, hi);
   }
