@@ -134,8 +134,9 @@ gvr_status cache_read(const gvr_cache* cache, const int32_t* slots, int64_t num_
  *           many entries and of unequal lengths are spread evenly over the device, in two kernels,
  *           where workspace_bytes is enough (GVR_ATTEND_WORKSPACE always is).  Its content is not
  *           kept: calls that can overlap on the GPU, or graphs whose replays can, need one each.
- * Scores, softmax and sums are fp32; K and V values are exact; probabilities are rounded to
- * 11-bit significands before they multiply V.
+ * Scores, softmax and sums are fp32; K and V values are exact.  Before they multiply V, softmax weights
+ * exp(score) are rounded to 11-bit significands; those below 2^-21 of the largest that is summed with them
+ * (part of the row, or all) are off by at most 2^-32 of that largest one instead.
  */
 gvr_status attend_decode(const gvr_cache* cache, const void* q, int64_t q_row_stride,
                          int64_t q_head_stride, int32_t dtype, int64_t num_rows, int32_t num_heads,

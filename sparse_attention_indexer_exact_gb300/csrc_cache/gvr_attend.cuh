@@ -3,8 +3,8 @@
 //
 // Mathematics.  For a query vector q of one head and entries e with keys k_e and values v_e,
 //   s_e = scale q.k_e,  o = sum_e exp(s_e - m) v_e / sum_e exp(s_e - m),  lse = m + log sum_e ...
-// in one pass over the entries with a running maximum m and running sums that are rescaled when m
-// grows, in any grouping of the entries: groups join by the same rescaling.
+// in one pass over the entries with a base m that follows their running maximum and running sums that
+// are rescaled when m grows, in any grouping of the entries: groups join by the same rescaling.
 //
 // Work split.  A unit is a set of rows that read the same entries: one row, or (whole-cache decode)
 // the next_n rows of a request.  Its queries fall into jobs of one KV head and 8 NT query vectors
@@ -24,8 +24,11 @@
 // into the instruction's operand layout, so nothing expanded is ever stored.  e2m1 * e4m3 has at most
 // 5 significant bits and an exponent within f16's, so K and V are exact in f16.  Queries are brought
 // to f16 exactly, too: a power of two per query puts a bf16 query's largest element at 2^14, and what
-// f16 cannot hold below that is under 2^-39 of it.  P is rounded to f16 (11 bits): eight times finer
-// than bf16 outputs, and averaged over the entries.
+// f16 cannot hold below that is under 2^-39 of it.  P is rounded to f16: eight times finer than bf16
+// outputs, and averaged over the entries.  To use f16's range the base lies 2^7 below the maximum, when it
+// is set: P is at most 2^7 then, and 2^15 before the base is set again.  So weights down to 2^-21 of the
+// largest of their walk have 11 bits, and what lies below is off by at most 2^-32 of it (with the maximum as
+// the base it was 2^-14 and 2^-25, and a long tail 18 nats below one entry was lost).
 //
 // What bounds it.  Instructions: at head_dim 128 and 8 queries a step takes a warp 587, of them 32 matrix
 // instructions, 128 expansions and 128 scale products, and an SM partition about 1100 clocks, whether two
@@ -48,7 +51,9 @@ namespace gvrc {
 constexpr int STEP = 32;  // entries a warp takes at a time: one per lane
 constexpr int STAGES = 3;
 constexpr int MAX_CLUSTER = 8;
-constexpr float NO_TOP = -3.4028235e38f;  // the maximum of no scores: finite, so that differences are
+constexpr float NO_TOP = -3.4028235e38f;  // the base of no scores: finite, so that differences are
+constexpr float BELOW = 7.f;              // of the base to the maximum that it is set from, in log2 units
+constexpr float ABOVE = 15.f;             // of a score to the base, at most: P up to 2^15 is within f16
 constexpr int JOIN_THREADS = 128;
 
 struct AttendParams {
@@ -239,7 +244,7 @@ __device__ __forceinline__ Unit load_unit(const AttendParams& p, int unit) {
 __device__ __forceinline__ int steps_of(uint32_t listed) { return int((listed + (STEP - 1)) / STEP); }
 
 // A warp's walk over `mine` steps of a unit's entries, from step `first` on, every `every`-th; positions
-// from `end` on are not looked at.  Leaves sums of exp2(score - top) v, the tops and the sums of exp2.
+// from `end` on are not looked at.  Leaves sums of exp2(score - top) v, the tops (bases) and the sums of exp2.
 template <int D, int NT, bool FOLD>
 __device__ __forceinline__ void walk(const AttendParams& p, const Unit& u, int h, int m0, int first_step, int every, int mine,
                                      uint32_t end, uint8_t* ring, uint32_t* places, const uint32_t (&raw)[NT][D / 8],
@@ -425,8 +430,8 @@ __device__ __forceinline__ void walk(const AttendParams& p, const Unit& u, int h
           }
       }
 
-      // The base that scores are taken against: the maximum when it was last set, kept while no score is
-      // more than 2^8 above it (P stays within f16).
+      // The base that scores are taken against: 2^7 below the maximum when it was last set, kept while no
+      // score is more than 2^15 above it.
       bool grow = false;
       float high[NT][2];  // of this lane's scores, in log2 units; factors are positive
 #pragma unroll
@@ -434,7 +439,7 @@ __device__ __forceinline__ void walk(const AttendParams& p, const Unit& u, int h
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           high[t][j] = fmaxf(fmaxf(s[0][t][j], s[0][t][j + 2]), fmaxf(s[1][t][j], s[1][t][j + 2])) * factor[t][j];
-          grow |= high[t][j] > top[t][j] + 8.f;
+          grow |= high[t][j] > top[t][j] + ABOVE;
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -442,7 +447,7 @@ __device__ __forceinline__ void walk(const AttendParams& p, const Unit& u, int h
           float down[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float next = fmaxf(top[t][j], high[t][j]);
+            float next = fmaxf(top[t][j], high[t][j] - BELOW);
             next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 4));
             next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 8));
             next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, 16));
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::THREADS, FOLD ? Shape<D, NT>::FO
   float* partial = reinterpret_cast<float*>(smem);   // [warps][Q][D]
   float* tops = partial + warps * S::Q * D;          // [warps][Q]
   float* sums = tops + warps * S::Q;                 // [warps][Q]
-  float* joined = sums + warps * S::Q;               // [jobs][2][Q]: maximum and sum of a job in this CTA
+  float* joined = sums + warps * S::Q;               // [jobs][2][Q]: base and sum of a job in this CTA
   if (g == 0) {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -815,7 +820,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(AttendParams p) {
   }
   for (int x = 1; x < ways; x <<= 1) {
     const float other = __shfl_xor_sync(0xffffffffu, all, x), next = fmaxf(all, other);
-    const float scale = exp2_fast(all - next);  // of both sides the same maximum: every lane ends with the same sums
+    const float scale = exp2_fast(all - next);  // of both sides the same base: every lane ends with the same sums
     all = next, sum *= scale;
     sum += __shfl_xor_sync(0xffffffffu, sum, x);
 #pragma unroll
