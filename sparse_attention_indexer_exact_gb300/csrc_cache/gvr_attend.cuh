@@ -203,7 +203,7 @@ __device__ __forceinline__ void load_queries(const AttendParams& p, int unit, in
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + int64_t(h * p.group + (FOLD ? m % p.group : m)) * p.q_head + c * (D / 4);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+      const uint4 v = live ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
       raw[t][4 * i] = v.x, raw[t][4 * i + 1] = v.y, raw[t][4 * i + 2] = v.z, raw[t][4 * i + 3] = v.w;
     }
   }
@@ -262,11 +262,11 @@ __device__ __forceinline__ void walk(const AttendParams& p, const Unit& u, int h
   uint32_t pos = first_step * STEP + lane;  // of the entry that this lane loads next; below 2^32 even behind the last
   auto load_entry = [&]() -> int {  // -1: none
     int e = -1;
-    if (pos < end) e = indices ? __ldg(indices + pos) : int(pos);
+    if (pos < end) e = indices ? indices[pos] : int(pos);
     pos += stride;
     return e;
   };
-  auto load_page = [&](int e) -> int { return uint32_t(e) < uint32_t(n) ? __ldg(table + (e >> p.page_shift)) : -1; };
+  auto load_page = [&](int e) -> int { return uint32_t(e) < uint32_t(n) ? table[e >> p.page_shift] : -1; };
   // CODES neighbouring lanes copy a row's codes, every lane a row's scales
   const uint8_t* codes_from = p.data + lane % CODES * 16;
   const uint32_t codes_to = lane / CODES * S::PITCH + lane % CODES * 16, scales_to = lane * S::PITCH + D;

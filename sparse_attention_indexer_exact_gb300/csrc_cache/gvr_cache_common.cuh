@@ -70,6 +70,9 @@ inline cudaError_t launch(const void* kernel, dim3 grid, int threads, int smem, 
 // Waits until the kernel before this one is complete and its writes are visible.  (No kernel but one
 // lets the next one start earlier than at its end: CTAs that wait in the free slots of a running kernel
 // lie unevenly over the SMs, and a decode batch took 70 us instead of 43.)
+// What a kernel before this one may have written is read with ordinary loads alone: they stay behind this wait
+// and see its writes, while loads through the read-only path (ld.global.nc) are for memory that nothing
+// writes while the kernel is there, and this kernel may be there while the one before still runs.
 __device__ __forceinline__ void begin() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets the next kernel start once every CTA of this one has come here, after begin(), or has ended.
