@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 
 __all__ = ["cache_alloc", "cache_row_bytes", "cache_tables", "cache_append", "cache_read", "attend_decode",
            "attend_prefill", "MAX_CACHE_REQUESTS", "HEAD_DIMS"]
@@ -121,6 +122,14 @@ def _short():
     return _native
 
 
+def _int32_value(value, name) -> int:
+    """An integer that the library takes in 32 bits: ctypes would drop the bits above them."""
+    value = operator.index(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, {value} does not")
+    return value
+
+
 # The checks of one tensor: its device's number, or an error that names it.
 def _device(t, name) -> int:
     import torch
@@ -205,7 +214,7 @@ def cache_row_bytes(head_dim: int) -> int:
     """Bytes of one entry of one KV head: K and V codes and scales of ``head_dim`` values."""
     lib = _library()
     out = ctypes.c_int32(0)
-    _check(lib, lib.cache_row_bytes(head_dim, ctypes.byref(out)))
+    _check(lib, lib.cache_row_bytes(_int32_value(head_dim, "head_dim"), ctypes.byref(out)))
     return out.value
 
 
@@ -233,6 +242,7 @@ def cache_tables(cached_lens, kv_lens, free_pages, block_table, max_new: int, pa
     if done is not None:
         return done
     import torch
+    page_size, compress_ratio = _int32_value(page_size, "page_size"), _int32_value(compress_ratio, "compress_ratio")
     device = _device(kv_lens, "kv_lens")
     requests = kv_lens.shape[0] if kv_lens.dim() == 1 else 0
     lens = _int32(kv_lens, device, "kv_lens")
@@ -366,6 +376,7 @@ def attend_decode(q, cache, block_table, kv_lens, next_n: int, compress_ratio: i
                                                next_n, compress_ratio, indices)
     if done is not None:
         return done
+    next_n, compress_ratio = _int32_value(next_n, "next_n"), _int32_value(compress_ratio, "compress_ratio")
     device, head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
     rows = head[5]
     requests = (rows + next_n - 1) // max(next_n, 1)

@@ -31,3 +31,39 @@ def test_every_kernel_waits_for_the_one_before_it():
             kernels += 1
             assert re.search(r"\bbegin\(\);", body.split("\n}\n")[0])
     assert kernels == 6
+
+
+# ------------------------------------------------------------------------------------- arguments
+@pytest.fixture(scope="module")
+def gvr():
+    from sparse_attention_indexer_exact_gb300 import _build
+    _build.build_library()
+    import sparse_attention_indexer_exact_gb300 as mod
+    mod.load_library()
+    return mod
+
+
+@pytest.mark.parametrize("beyond", [2 ** 31, 2 ** 32 + 1, -2 ** 31 - 1, 2 ** 70])
+def test_integers_beyond_32_bits_are_refused(gvr, beyond):
+    """Cut to 32 bits they would be other numbers: 2^32 + 1 draft rows would read a length for each row where one was
+    given for all.  (The host's tensors come to their own refusal only behind this one.)"""
+    torch = pytest.importorskip("torch")
+    i32 = torch.zeros(3, dtype=torch.int32)
+    cache, table, x = torch.zeros(4, 16, 2, 144, dtype=torch.uint8), i32[:, None], torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="head_dim"):
+        gvr.cache_row_bytes(beyond)
+    with pytest.raises(ValueError, match="page_size"):
+        gvr.cache_tables(i32, i32, i32, table, 5, beyond)
+    with pytest.raises(ValueError, match="compress_ratio"):
+        gvr.cache_tables(i32, i32, i32, table, 5, 16, beyond)
+    with pytest.raises(ValueError, match="next_n"):
+        gvr.attend_decode(x, cache, table, i32, beyond, 1)
+    with pytest.raises(ValueError, match="compress_ratio"):
+        gvr.attend_decode(x, cache, table, i32, 1, beyond)
+
+
+def test_integers_of_other_types_are_taken_and_fractions_refused(gvr):
+    np = pytest.importorskip("numpy")
+    assert gvr.cache_row_bytes(np.int64(128)) == 144
+    with pytest.raises(TypeError):
+        gvr.cache_row_bytes(128.0)
