@@ -126,10 +126,18 @@ def _check(status: int):
 
 
 # ----------------------------------------------------------------------------- raw pointers
+def _fit_int32(*values) -> None:
+    """ctypes would cut an integer that the library takes in 32 bits to its lower bits."""
+    for value in values:
+        if not -2 ** 31 <= value < 2 ** 31:
+            raise ValueError(f"next_n, compress_ratio and k must fit 32 bits, {value} does not")
+
+
 def topk_decode_raw(logits_ptr: int, row_stride: int, num_rows: int, kv_lens_ptr: int, next_n: int,
                     compress_ratio: int, k: int, indices_ptr: int, values_ptr: int | None, stream: int,
                     options: Options | None = None) -> None:
     """``topk_decode`` / ``topk_decode_ex`` on raw device addresses (enqueue only)."""
+    _fit_int32(next_n, compress_ratio, k)
     lib = load_library()
     if options is None:
         st = lib.topk_decode(logits_ptr, row_stride, num_rows, kv_lens_ptr, next_n, compress_ratio, k,
@@ -144,6 +152,7 @@ def topk_decode_hinted_raw(logits_ptr: int, row_stride: int, num_rows: int, kv_l
                            compress_ratio: int, k: int, pre_idx_ptr: int, pre_idx_stride: int, indices_ptr: int,
                            values_ptr: int | None, stream: int, options: Options | None = None) -> None:
     """``topk_decode_hinted`` on raw device addresses (enqueue only)."""
+    _fit_int32(next_n, compress_ratio, k)
     lib = load_library()
     st = lib.topk_decode_hinted(logits_ptr, row_stride, num_rows, kv_lens_ptr, next_n, compress_ratio, k,
                                 pre_idx_ptr, pre_idx_stride, indices_ptr, values_ptr, stream,
@@ -156,6 +165,7 @@ def topk_decode_blockskip_raw(logits_ptr: int, row_stride: int, num_rows: int, k
                               indices_ptr: int, values_ptr: int | None, stream: int,
                               options: Options | None = None) -> None:
     """``topk_decode_blockskip`` on raw device addresses (enqueue only)."""
+    _fit_int32(next_n, compress_ratio, k)
     lib = load_library()
     st = lib.topk_decode_blockskip(logits_ptr, row_stride, num_rows, kv_lens_ptr, next_n, compress_ratio, k,
                                    block_max_ptr, block_max_stride, indices_ptr, values_ptr, stream,
@@ -166,6 +176,7 @@ def topk_decode_blockskip_raw(logits_ptr: int, row_stride: int, num_rows: int, k
 def topk_prefill_raw(logits_ptr: int, row_stride: int, num_rows: int, row_starts_ptr: int, row_ends_ptr: int,
                      k: int, indices_ptr: int, stream: int, options: Options | None = None) -> None:
     """``topk_prefill`` / ``topk_prefill_ex`` on raw device addresses (enqueue only)."""
+    _fit_int32(k)
     lib = load_library()
     if options is None:
         st = lib.topk_prefill(logits_ptr, row_stride, num_rows, row_starts_ptr, row_ends_ptr, k, indices_ptr,
@@ -180,6 +191,7 @@ def topk_decode_ws_raw(logits_ptr: int, row_stride: int, num_rows: int, kv_lens_
                        compress_ratio: int, k: int, indices_ptr: int, values_ptr: int | None, workspace_ptr: int,
                        workspace_bytes: int, stream: int, options: Options | None = None) -> None:
     """``topk_decode_ws`` on raw device addresses (enqueue only)."""
+    _fit_int32(next_n, compress_ratio, k)
     lib = load_library()
     st = lib.topk_decode_ws(logits_ptr, row_stride, num_rows, kv_lens_ptr, next_n, compress_ratio, k, indices_ptr,
                             values_ptr, workspace_ptr, workspace_bytes, stream,
@@ -191,6 +203,7 @@ def topk_prefill_ws_raw(logits_ptr: int, row_stride: int, num_rows: int, row_sta
                         k: int, indices_ptr: int, workspace_ptr: int, workspace_bytes: int, stream: int,
                         options: Options | None = None) -> None:
     """``topk_prefill_ws`` on raw device addresses (enqueue only)."""
+    _fit_int32(k)
     lib = load_library()
     st = lib.topk_prefill_ws(logits_ptr, row_stride, num_rows, row_starts_ptr, row_ends_ptr, k, indices_ptr,
                              workspace_ptr, workspace_bytes, stream,
@@ -203,6 +216,7 @@ def topk_decode_noalloc_raw(logits_ptr: int, row_stride: int, num_rows: int, kv_
                             stream: int) -> None:
     """``topk_decode_noalloc`` on raw device addresses: the library's own fixed scratch, no
     allocation and no workspace (at most 128 rows; calls that overlap on the GPU race)."""
+    _fit_int32(next_n, compress_ratio, k)
     lib = load_library()
     _check(lib.topk_decode_noalloc(logits_ptr, row_stride, num_rows, kv_lens_ptr, next_n, compress_ratio, k,
                                    indices_ptr, values_ptr, stream))
