@@ -86,7 +86,7 @@ gvr_status cache_row_bytes(int32_t head_dim, int32_t* bytes);
  *                saturate at 2^31 - 1.
  *   cached_lens, kv_lens  int32 [num_requests], num_requests <= GVR_CACHE_MAX_REQUESTS.
  *   free_pages   int32 [num_free], distinct page numbers not in use; may be NULL if num_free is 0.
- * table_width * page_size < 2^31; table_stride >= table_width.
+ * table_width * page_size < 2^31; num_requests * table_width < 2^31; table_stride >= table_width.
  * With no requests counts and slots are still written (0 and -1).
  */
 gvr_status cache_tables(const int32_t* cached_lens, const int32_t* kv_lens, int64_t num_requests,

@@ -424,6 +424,8 @@ gvr_status cache_tables(const int32_t* cached_lens, const int32_t* kv_lens, int6
       num_free < 0 || num_free > kIntMax || num_slots < 0 || num_slots > kIntMax || table_width < 0 ||
       table_width > kIntMax / page_size)
     return GVR_ERR_ARG;
+  // new pages are numbered in 32 bits: with more, the last ones would not be written
+  if (num_requests > 0 && table_width > kIntMax / num_requests) return GVR_ERR_ARG;
   if (table_stride < table_width || table_stride > kIntMax) return GVR_ERR_STRIDE;
   if (!counts || (num_requests > 0 && (!cached_lens || !kv_lens)) || (num_requests > 0 && table_width > 0 && !block_table) ||
       (num_free > 0 && !free_pages) || (num_slots > 0 && !slots))

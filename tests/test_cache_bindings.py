@@ -67,3 +67,16 @@ def test_integers_of_other_types_are_taken_and_fractions_refused(gvr):
     assert gvr.cache_row_bytes(np.int64(128)) == 144
     with pytest.raises(TypeError):
         gvr.cache_row_bytes(128.0)
+
+
+def test_tables_of_too_many_elements_are_refused(gvr):
+    """8192 requests of 2^18 pages each could take 2^31 new ones, which sums of 32 bits do not tell apart."""
+    lib, at, missing, argument = gvr.load_library(), 0x10000, 1, 5  # an aligned address that is never read
+
+    def call(requests, width):  # without counts, so refused in any case, behind the check of the sizes
+        return lib.cache_tables(at, at, requests, 1, 1, at, 9, at, width, width, at, 40, None, None)
+
+    for requests, width in ((8192, 2 ** 18), (8191, 2 ** 18 + 65), (2, 2 ** 30), (8192, 2 ** 31 - 1)):
+        assert requests * width >= 2 ** 31 and call(requests, width) == argument
+    for requests, width in ((8192, 2 ** 18 - 1), (1, 2 ** 31 - 1), (0, 2 ** 31 - 1)):
+        assert requests * width < 2 ** 31 and call(requests, width) == missing
