@@ -6,17 +6,22 @@ beside this file; it rebuilds only when a source is newer than the library.  No
 CMake, no torch extension machinery: the library is a plain shared object with
 an ``extern "C"`` interface (``include/gvr_topk.h``, ``include/gvr_cache.h``).
 Beside it g++ builds ``_native.so`` (``_native.cpp``), the short way from torch
-tensors to the cache's calls, against the installed torch and the library.
+tensors to the cache's calls, against the installed torch and the library.  The
+library does not need it, or torch: where those or Python's headers are not
+there, ``_native.so`` is left out with a warning, and the cache's calls go through
+ctypes.
 """
 from __future__ import annotations
 
 import glob
 import importlib.util
 import os
+import shutil
 import subprocess
 import sysconfig
 import tempfile
 import threading
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -64,11 +69,21 @@ def _run(cmd: list[str]) -> str:
     return r.stdout + r.stderr
 
 
-def _torch_root() -> str:
+def _torch_root() -> str | None:
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch is needed to build _native.so")
-    return list(spec.submodule_search_locations)[0]
+    return list(spec.submodule_search_locations)[0] if spec and spec.submodule_search_locations else None
+
+
+def native_lacks() -> str | None:
+    """What _native.so cannot be built without and is not there."""
+    torch = _torch_root()
+    if torch is None:
+        return "torch is not installed"
+    for header in (os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h"),
+                   os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        if not os.path.exists(header):
+            return f"{header} is missing"
+    return None if shutil.which("g++") else "g++ is missing"
 
 
 def native_commands(obj: str, out: str = NATIVE_PATH) -> tuple[list[str], list[str]]:
@@ -92,24 +107,27 @@ def stale(out: str = LIB_PATH, of: list[str] | None = None) -> bool:
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile libgvrtopk.so for sm_103a, and _native.so, where missing or older than their sources."""
+    """Compile libgvrtopk.so for sm_103a, and _native.so where it can be built, if missing or older than their sources."""
     with _lock:
         library = force or stale()
         native = force or library or stale(NATIVE_PATH, [NATIVE_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+        lacks = native_lacks() if native else None
+        if lacks:
+            native = False
+            warnings.warn(f"_native.so is not built ({lacks}): the cache calls go through ctypes", RuntimeWarning)
         if library or native:
             extra = ["-Xptxas", "-v"] if verbose else []
             with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor() as pool:
                 jobs = [(u, os.path.join(tmp, os.path.basename(u) + ".o")) for u in units()] if library else []
-                obj = os.path.join(tmp, "native.o")
-                commands = [compile_command(*j, extra) for j in jobs]
+                compiled = [pool.submit(_run, compile_command(*j, extra)) for j in jobs]
                 if native:
-                    native_compile, native_link = native_commands(obj)
-                    commands.append(native_compile)
-                said = list(pool.map(_run, commands))
+                    native_compile, native_link = native_commands(os.path.join(tmp, "native.o"))
+                    native_compiled = pool.submit(_run, native_compile)
+                said = [c.result() for c in compiled]
                 if library:
                     said.append(_run(link_command([o for _, o in jobs])))
-                if native:
-                    said.append(_run(native_link))
+                if native:  # behind the library, which is there whatever becomes of this
+                    said += [native_compiled.result(), _run(native_link)]
             if verbose:
                 print("".join(said))
     return LIB_PATH

@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import math
 import operator
+import warnings
 
 __all__ = ["cache_alloc", "cache_row_bytes", "cache_tables", "cache_append", "cache_read", "attend_decode",
            "attend_prefill", "MAX_CACHE_REQUESTS", "HEAD_DIMS"]
@@ -104,8 +105,16 @@ def _current(stream, tensor):
 
 # The short way (_native.cpp): the same calls with the tensors read natively.  Its functions return
 # None wherever anything is out of the ordinary, and the call then goes step by step through the
-# checks below, which say what is wrong.
+# checks below, which say what is wrong.  Where it was not built every call does.
 _native = None
+
+
+class _NoShortWay:
+    @staticmethod
+    def _nothing(*args):
+        return None
+
+    cache_tables = cache_append = cache_read = attend_decode = attend_prefill = _nothing
 
 
 def _short():
@@ -116,8 +125,9 @@ def _short():
             import torch  # noqa: F401 - its libraries have to be there first
             from . import _native as native
         except ImportError as e:
-            raise RuntimeError("_native.so is missing or does not fit this torch: build it with "
-                               "`python -m sparse_attention_indexer_exact_gb300._build`") from e
+            warnings.warn(f"_native.so is missing or does not fit this torch ({e}): the cache calls take 15 us more of host "
+                          "time; build it with `python -m sparse_attention_indexer_exact_gb300._build`", RuntimeWarning)
+            native = _NoShortWay
         _native = native
     return _native
 

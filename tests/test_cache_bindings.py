@@ -80,3 +80,72 @@ def test_tables_of_too_many_elements_are_refused(gvr):
         assert requests * width >= 2 ** 31 and call(requests, width) == argument
     for requests, width in ((8192, 2 ** 18 - 1), (1, 2 ** 31 - 1), (0, 2 ** 31 - 1)):
         assert requests * width < 2 ** 31 and call(requests, width) == missing
+
+
+# ------------------------------------------------------------------- the library without its tensor binding
+@pytest.fixture
+def commands(monkeypatch):
+    """The commands that a build runs, which are not run."""
+    from sparse_attention_indexer_exact_gb300 import _build
+    ran = []
+    monkeypatch.setattr(_build, "_run", lambda cmd: ran.append(cmd) or "")
+    return ran
+
+
+def lacking(monkeypatch, what):
+    from sparse_attention_indexer_exact_gb300 import _build
+    if what == "torch":
+        find = _build.importlib.util.find_spec
+        monkeypatch.setattr(_build.importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    elif what == "Python's headers":
+        monkeypatch.setattr(_build.sysconfig, "get_paths", lambda *a: {"include": os.path.join(ROOT, "none")})
+    else:
+        monkeypatch.setattr(_build.shutil, "which", lambda name: None)
+
+
+@pytest.mark.parametrize("what", ["torch", "Python's headers", "g++"])
+def test_the_library_is_built_where_its_binding_cannot_be(commands, monkeypatch, what):
+    from sparse_attention_indexer_exact_gb300 import _build
+    lacking(monkeypatch, what)
+    with pytest.warns(RuntimeWarning, match="_native.so is not built"):
+        assert _build.build_library(force=True) == _build.LIB_PATH
+    assert len(commands) == len(_build.units()) + 1 and _build.LIB_PATH in commands[-1]
+    assert not any(_build.NATIVE_SOURCE in c or _build.NATIVE_PATH in c for c in commands)
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library(monkeypatch):
+    from sparse_attention_indexer_exact_gb300 import _build
+    ran = []
+
+    def run(cmd):
+        if _build.NATIVE_SOURCE in cmd:
+            raise RuntimeError("no")
+        ran.append(cmd)
+        return ""
+
+    monkeypatch.setattr(_build, "_run", run)
+    with pytest.raises(RuntimeError):
+        _build.build_library(force=True)
+    assert _build.LIB_PATH in ran[-1] and len(ran) == len(_build.units()) + 1
+
+
+def test_cache_calls_without_the_binding_go_step_by_step(gvr, monkeypatch):
+    """As far as the host goes: each call comes to the checks that name what is wrong."""
+    import sys
+    torch = pytest.importorskip("torch")
+    from sparse_attention_indexer_exact_gb300 import cache
+    monkeypatch.setattr(cache, "_native", None)
+    monkeypatch.delattr(gvr, "_native", raising=False)
+    monkeypatch.setitem(sys.modules, gvr.__name__ + "._native", None)  # as if the file were not there
+    i32, c, x = torch.zeros(3, dtype=torch.int32), torch.zeros(4, 16, 2, 144, dtype=torch.uint8), torch.zeros(3, 2, 128).half()
+    with pytest.warns(RuntimeWarning, match="_native.so is missing"):
+        with pytest.raises(TypeError, match="CUDA"):
+            gvr.cache_append(x, x, c, i32)
+    import warnings
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")  # said once
+        for call in (lambda: gvr.cache_tables(i32, i32, i32, i32[:, None], 5, 16), lambda: gvr.cache_read(c, i32, 128),
+                     lambda: gvr.attend_decode(x, c, i32[:, None], i32, 1, 1),
+                     lambda: gvr.attend_prefill(x, c, i32[:, None], i32, i32, i32, i32[:, None])):
+            with pytest.raises(TypeError, match="CUDA"):
+                call()
