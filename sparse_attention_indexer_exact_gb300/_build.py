@@ -32,6 +32,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgvrtopk.so")
 NATIVE_SOURCE = os.path.join(PKG, "_native.cpp")
 NATIVE_PATH = os.path.join(PKG, "_native.so")
+NATIVE_STAMP = NATIVE_PATH + ".for"  # the torch and Python that it was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()
 
@@ -74,6 +75,25 @@ def _torch_root() -> str | None:
     return list(spec.submodule_search_locations)[0] if spec and spec.submodule_search_locations else None
 
 
+def native_target() -> str:
+    """The torch and Python of this process: _native.so is compiled against their insides, so it fits no others."""
+    torch = _torch_root()
+    version = "none"
+    if torch is not None:
+        scope: dict = {}
+        with open(os.path.join(torch, "version.py")) as f:  # without importing torch
+            exec(f.read(), scope)
+        version = str(scope["__version__"])
+    return f"torch {version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def native_stale() -> bool:
+    if stale(NATIVE_PATH, [NATIVE_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))]) or not os.path.exists(NATIVE_STAMP):
+        return True
+    with open(NATIVE_STAMP) as f:
+        return f.read() != native_target()
+
+
 def native_lacks() -> str | None:
     """What _native.so cannot be built without and is not there."""
     torch = _torch_root()
@@ -92,7 +112,7 @@ def native_commands(obj: str, out: str = NATIVE_PATH) -> tuple[list[str], list[s
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include") if os.path.isabs(nvcc_path()) else \
         "/usr/local/cuda/include"
     include = [os.path.join(torch, "include"), sysconfig.get_paths()["include"], cuda, INCLUDE]
-    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *[x for d in include for x in ("-I", d)], "-c",
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f'-DGVR_BUILT_FOR="{native_target()}"', *[x for d in include for x in ("-I", d)], "-c",
                 NATIVE_SOURCE, "-o", obj]
     link = ["g++", "-shared", obj, "-o", out, "-L", PKG, "-l:libgvrtopk.so", "-L", os.path.join(torch, "lib"),
             "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
@@ -107,10 +127,11 @@ def stale(out: str = LIB_PATH, of: list[str] | None = None) -> bool:
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile libgvrtopk.so for sm_103a, and _native.so where it can be built, if missing or older than their sources."""
+    """Compile libgvrtopk.so for sm_103a, and _native.so where it can be built, if missing or older than their sources
+    (_native.so: or built for another torch or Python)."""
     with _lock:
         library = force or stale()
-        native = force or library or stale(NATIVE_PATH, [NATIVE_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+        native = force or library or native_stale()
         lacks = native_lacks() if native else None
         if lacks:
             native = False
@@ -127,7 +148,12 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
                 if library:
                     said.append(_run(link_command([o for _, o in jobs])))
                 if native:  # behind the library, which is there whatever becomes of this
-                    said += [native_compiled.result(), _run(native_link)]
+                    said.append(native_compiled.result())
+                    if os.path.exists(NATIVE_STAMP):
+                        os.remove(NATIVE_STAMP)
+                    said.append(_run(native_link))
+                    with open(NATIVE_STAMP, "w") as f:
+                        f.write(native_target())
             if verbose:
                 print("".join(said))
     return LIB_PATH

@@ -286,4 +286,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The short way from tens
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__native() { return PyModule_Create(&module); }
+// BUILT_FOR is compared before the first call: under another torch nothing here may be used.
+PyMODINIT_FUNC PyInit__native() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "BUILT_FOR", GVR_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

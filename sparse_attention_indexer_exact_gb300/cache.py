@@ -123,7 +123,10 @@ def _short():
         _library()
         try:
             import torch  # noqa: F401 - its libraries have to be there first
+            from . import _build
             from . import _native as native
+            if native.BUILT_FOR != _build.native_target():
+                raise ImportError(f"built for {native.BUILT_FOR}, this is {_build.native_target()}")
         except ImportError as e:
             warnings.warn(f"_native.so is missing or does not fit this torch ({e}): the cache calls take 15 us more of host "
                           "time; build it with `python -m sparse_attention_indexer_exact_gb300._build`", RuntimeWarning)

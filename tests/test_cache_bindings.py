@@ -149,3 +149,48 @@ def test_cache_calls_without_the_binding_go_step_by_step(gvr, monkeypatch):
                      lambda: gvr.attend_prefill(x, c, i32[:, None], i32, i32, i32, i32[:, None])):
             with pytest.raises(TypeError, match="CUDA"):
                 call()
+
+
+# ----------------------------------------------------------------------- the binding under another torch
+def test_the_binding_is_rebuilt_for_another_torch(gvr, commands, monkeypatch, tmp_path):
+    from sparse_attention_indexer_exact_gb300 import _build
+    _build.build_library()
+    assert not commands  # all there
+    stamp = tmp_path / "stamp"
+    monkeypatch.setattr(_build, "NATIVE_STAMP", str(stamp), raising=False)
+    for before in (None, "torch 2.8.0, cpython-312-x86_64-linux-gnu"):
+        if before:
+            stamp.write_text(before)
+        commands.clear()
+        _build.build_library()
+        assert [_build.NATIVE_SOURCE in c for c in commands] == [True, False]  # compiled and linked, and nothing else
+        assert stamp.read_text() == _build.native_target()
+    commands.clear()
+    _build.build_library()
+    assert not commands
+
+
+def test_the_binding_knows_what_it_was_built_for(gvr):
+    torch = pytest.importorskip("torch")
+    from sparse_attention_indexer_exact_gb300 import _build, _native
+    assert _native.BUILT_FOR == _build.native_target() and f"torch {torch.__version__}," in _native.BUILT_FOR
+
+
+def test_a_binding_for_another_torch_is_not_used(gvr, monkeypatch):
+    """Its file may load, but reads tensors by another layout: the call goes step by step."""
+    import sys
+    from types import SimpleNamespace
+    torch = pytest.importorskip("torch")
+    from sparse_attention_indexer_exact_gb300 import cache
+
+    def never(*args):
+        raise AssertionError("used")
+
+    other = SimpleNamespace(BUILT_FOR="torch 2.8.0, cpython-312-x86_64-linux-gnu", cache_append=never)
+    monkeypatch.setattr(cache, "_native", None)
+    monkeypatch.setattr(gvr, "_native", other, raising=False)
+    monkeypatch.setitem(sys.modules, gvr.__name__ + "._native", other)
+    i32, c, x = torch.zeros(3, dtype=torch.int32), torch.zeros(4, 16, 2, 144, dtype=torch.uint8), torch.zeros(3, 2, 128).half()
+    with pytest.warns(RuntimeWarning, match="built for torch 2.8.0"):
+        with pytest.raises(TypeError, match="CUDA"):
+            gvr.cache_append(x, x, c, i32)
