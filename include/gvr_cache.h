@@ -132,7 +132,9 @@ gvr_status cache_read(const gvr_cache* cache, const int32_t* slots, int64_t num_
  *           for a row without entries.  (Merges this with attention over other entries.)
  *   workspace  optional device memory, 16-byte aligned, of any content and size: with it, rows of
  *           many entries and of unequal lengths are spread evenly over the device, in two kernels,
- *           where workspace_bytes is enough (GVR_ATTEND_WORKSPACE always is).  Its content is not
+ *           where workspace_bytes is enough (GVR_ATTEND_WORKSPACE always is).  How many is judged by k
+ *           or, over whole caches, by the table's width; selections of up to 2048 entries are mostly
+ *           faster without a workspace (700 rows of 2048: 159 us with, 142 without).  Its content is not
  *           kept: calls that can overlap on the GPU, or graphs whose replays can, need one each.
  * Scores, softmax and sums are fp32; K and V values are exact.  Before they multiply V, softmax weights
  * exp(score) are rounded to 11-bit significands; those below 2^-21 of the largest that is summed with them

@@ -57,8 +57,9 @@ def _declare(lib):
 
 
 _WORKSPACE = 1 << 25  # GVR_ATTEND_WORKSPACE
-# Selections over this many entries a row get a workspace, as whole caches do.  64 rows of 3000 entries, 64 heads over 8
-# of 128: 55 us with it, 61 without; one row of 3000 10.9 and 14.9; but 128 rows of 1024 47 and 42, 700 of 2048 159 and 141.
+# Selections over this many entries a row get a workspace, as whole caches do.  topk_decode and topk_prefill select up to
+# 2048; longer ones come from elsewhere.  64 rows of 3000 entries, 64 heads over 8 of 128: 55 us with it, 61 without; one row of
+# 3000 10.9 and 14.9.  Of 2048: 128 rows 70 and 76, but 37 rows under one KV head 19.8 and 18.3, 700 prefill rows 159 and 142.
 _LONG = 2048
 
 _lib = None
@@ -93,7 +94,8 @@ def _launch(device: int, call, *args):
 
 def _current(stream, tensor):
     """Context in which ``stream`` (a torch stream or a handle) is the current one: what a call
-    allocates then belongs to the stream that uses it."""
+    allocates then belongs to the stream that uses it.  A handle does not tell its device: one of another
+    device is refused by the launch."""
     import torch
     if not isinstance(stream, torch.cuda.Stream):
         # handle 0 is the default stream; to ExternalStream it would mean a new one

@@ -12,7 +12,7 @@ constexpr int MAX_WARPS = 4;           // of a CTA
 // Equal shares (balanced_kernel) take a second kernel, 3 us.  Against clusters, 8 KV heads of 128: one request of
 // 1024 entries 10.1 us against 8.2, of 1536 9.9 against 9.8, of 2048 10.2 against 11.4; 8 requests of up to 2048
 // 14 against 12, 64 28.5 against 31.5.  400 of up to 2000, two rows each, 4 KV heads of 64: 57 against 73.
-constexpr int BALANCED_STEPS = 48;     // of 32 entries, at least
+constexpr int BALANCED_STEPS = 48;     // of 32 entries, at least: k, or the table's width, as lengths are on the device
 constexpr int BALANCED_UNITS = 1024;   // at most
 
 const KernelInfo& kernel_info(int i) {

@@ -30,15 +30,17 @@
 // largest of their walk have 11 bits, and what lies below is off by at most 2^-32 of it (with the maximum as
 // the base it was 2^-14 and 2^-25, and a long tail 18 nats below one entry was lost).
 //
-// What bounds it.  Instructions: at head_dim 128 and 8 queries a step takes a warp 587, of them 32 matrix
-// instructions, 128 expansions and 128 scale products, and an SM partition about 1100 clocks, whether two
-// warps share it or four (matrix, FMA and ALU pipes busy 23, 31 and 44 % of them, one after the other).  The
+// What bounds it.  The work of a step, no one unit: at head_dim 128 and 8 queries it takes a warp 587
+// instructions, of them 32 matrix instructions, 128 expansions and 128 scale products, and an SM partition about
+// 1100 clocks, whether two warps share it or four, while the matrix, FMA and ALU pipes are busy 23, 31 and 44 %
+// of them, 2.1 of 4 instructions are issued a clock and DRAM gives 55 %.  Of 69.4 us (2048 entries a row), leaving out
+// the copies takes 10.7, V's scale products 6.3, V's interleaving 4.3, K's scale products 2.9, the exponentials 1.0.  The
 // expansion costs the same for 1 to 8 queries, so more query heads a KV head cost little up to there.
 // A scale product on the accumulators or on P instead would take fewer, but needs the 16 values of a scale
 // in one tile row's lanes, which the cache's order of codes does not give.
 // 128 rows x 1024 of up to 131072 entries, 8 KV heads of 128, 64 query heads: 42.8 us, 3.6 TB/s of rows read
 // (147 MB; 22.9 us at the rate of a copy).  700 prefill rows x up to 2048 entries, 4 KV heads of 128, 32 query
-// heads: 140 us.  One row x 512 entries: 6.7 us.
+// heads: 140 us.  One row x 512 entries: 6.8 us.
 #pragma once
 
 #include <type_traits>
@@ -161,7 +163,8 @@ struct Shape {
   static constexpr int PITCH = 16 * (RB / 16 | 1);  // of a row in shared memory
   static constexpr int Q = 8 * NT;  // query vectors of a job
   static constexpr int WARPS = 4, THREADS = 32 * WARPS;  // at most
-  // accumulators and queries take 3 D / 8 NT registers: that leaves room for 16, 12 or 8 warps on an SM
+  // accumulators and queries take 3 D / 8 NT registers: that leaves room for 16, 12 or 8 warps on an SM.  (At head_dim
+  // 256 shared memory has room for fewer, 29,312 bytes each: 4, 6 or 7 in CTAs of four, two or one.)
   static constexpr int BLOCKS = D * NT <= 128 && NT == 1 ? 4 : D * NT == 128 ? 3 : 2, FOLD_BLOCKS = D * NT == 128 ? 3 : BLOCKS;
   // of balanced_kernel, in CTAs of at most four
   static constexpr int BALANCED_WARPS = D * NT >= 256 ? 8 : 12;
