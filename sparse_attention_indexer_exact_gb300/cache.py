@@ -127,8 +127,9 @@ def _short():
             import torch  # noqa: F401 - its libraries have to be there first
             from . import _build
             from . import _native as native
-            if native.BUILT_FOR != _build.native_target():
-                raise ImportError(f"built for {native.BUILT_FOR}, this is {_build.native_target()}")
+            built_for = getattr(native, "BUILT_FOR", "an unknown torch")
+            if built_for != _build.native_target():
+                raise ImportError(f"built for {built_for}, this is {_build.native_target()}")
         except ImportError as e:
             warnings.warn(f"_native.so is missing or does not fit this torch ({e}): the cache calls take 15 us more of host "
                           "time; build it with `python -m sparse_attention_indexer_exact_gb300._build`", RuntimeWarning)

@@ -194,3 +194,15 @@ def test_a_binding_for_another_torch_is_not_used(gvr, monkeypatch):
     with pytest.warns(RuntimeWarning, match="built for torch 2.8.0"):
         with pytest.raises(TypeError, match="CUDA"):
             gvr.cache_append(x, x, c, i32)
+
+
+def test_a_binding_that_does_not_say_what_it_was_built_for_is_not_used(gvr, monkeypatch):
+    import sys
+    from types import SimpleNamespace
+    from sparse_attention_indexer_exact_gb300 import cache
+    pytest.importorskip("torch")
+    monkeypatch.setattr(cache, "_native", None)
+    monkeypatch.setattr(gvr, "_native", SimpleNamespace(), raising=False)
+    monkeypatch.setitem(sys.modules, gvr.__name__ + "._native", gvr._native)
+    with pytest.warns(RuntimeWarning, match="built for an unknown torch"):
+        assert cache._short().cache_append() is None
