@@ -36,7 +36,8 @@
  * reads no device memory on the host, does not synchronise, and enqueues one kernel (attention
  * with a workspace: one or two) on `stream` of the current device, so it can be captured in a
  * graph; calls share no state, on any streams.  Counts of 0 are no-ops that return GVR_OK.  Statuses are those of
- * gvr_topk.h; gvr_cache_status_string says what each means here.
+ * gvr_topk.h; gvr_cache_status_string says what each means here.  Strides, counts of slots and of free
+ * pages, and k are below 2^31.
  */
 #ifndef GVR_CACHE_H
 #define GVR_CACHE_H
@@ -52,6 +53,8 @@ enum { GVR_BF16 = 0, GVR_F16 = 1 };
 
 #define GVR_CACHE_MAX_REQUESTS 8192   /* cache_tables */
 #define GVR_CACHE_MAX_PAGE_SIZE 4096
+#define GVR_ATTEND_MAX_NEXT_N 4096
+#define GVR_ATTEND_MAX_HEADS (1 << 20)
 #define GVR_ATTEND_WORKSPACE (1 << 25) /* bytes */
 
 typedef struct gvr_cache {
@@ -61,7 +64,7 @@ typedef struct gvr_cache {
                            page_size * num_kv_heads * row_bytes; the whole cache may span 2^32
                            rows, or 64 GB where the stride is not a multiple of row_bytes */
   int32_t page_size;    /* entries per page: a power of two, 1 to GVR_CACHE_MAX_PAGE_SIZE */
-  int32_t num_kv_heads; /* >= 1 */
+  int32_t num_kv_heads; /* 1 to 65535 */
   int32_t head_dim;     /* 64, 128 or 256 */
   int32_t reserved;     /* must be 0 */
   float k_scale;        /* finite and > 0 */
@@ -119,7 +122,10 @@ gvr_status cache_read(const gvr_cache* cache, const int32_t* slots, int64_t num_
 /*
  * Attention of decode rows over the cache.  Row r belongs to request r / next_n and sees its
  * entries [0, n_r), n_r exactly as in topk_decode (0 when kv_lens < next_n), clamped to
- * table_width * page_size.  Query head h reads KV head h / (num_heads / num_kv_heads).
+ * table_width * page_size.  Query head h reads KV head h / (num_heads / num_kv_heads).  next_n is 1 to
+ * GVR_ATTEND_MAX_NEXT_N, num_heads a multiple of num_kv_heads up to GVR_ATTEND_MAX_HEADS.  What no grid
+ * holds is refused (GVR_ERR_ARG): KV heads times tiles of 8 to 32 of the queries that share one (num_heads /
+ * num_kv_heads, times next_n over whole caches) above 65535.
  *   q       [num_rows][num_heads][head_dim] of `dtype`, unit inner stride, row and head strides in
  *           elements (multiples of 8; base 16-byte aligned).
  *   indices int32 [num_rows][k]: the entries that the row attends to, as topk_decode writes them;

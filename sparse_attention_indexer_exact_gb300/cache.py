@@ -379,7 +379,7 @@ def attend_decode(q, cache, block_table, kv_lens, next_n: int, compress_ratio: i
     """Attention of decode rows over the 4-bit cache; returns (out, lse or None).
 
     ``q`` is [rows, heads, head_dim] (bfloat16 or float16, strides in multiples of 8); row r belongs to
-    request r // next_n and sees its (kv_len - next_n + r % next_n + 1) // compress_ratio entries, found
+    request r // next_n (``next_n`` up to 4096) and sees its (kv_len - next_n + r % next_n + 1) // compress_ratio entries, found
     through ``block_table`` (int32 [requests, pages]): those that ``indices`` (int32 [rows, k], as
     ``topk_decode`` returns them) lists, or all where it is None.  ``scale`` defaults to
     1 / sqrt(head_dim).  ``lse`` (fp32 [rows, heads]) is the log of each row's sum of exponentials.

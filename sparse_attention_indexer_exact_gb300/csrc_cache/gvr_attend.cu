@@ -218,7 +218,7 @@ gvr_status check_attend(const gvr_cache* cache, const void* q, int64_t q_row_str
   const gvr_status s = check_cache(cache);
   if (s != GVR_OK) return s;
   if ((dtype != GVR_BF16 && dtype != GVR_F16) || num_rows < 0 || num_heads < 1 || num_heads % cache->num_kv_heads != 0 ||
-      num_heads > 1 << 20 || !std::isfinite(float(double(scale) * cache->k_scale * 1.4426950408889634)) || table_width < 0 || table_width > kIntMax / cache->page_size)
+      num_heads > GVR_ATTEND_MAX_HEADS || !std::isfinite(float(double(scale) * cache->k_scale * 1.4426950408889634)) || table_width < 0 || table_width > kIntMax / cache->page_size)
     return GVR_ERR_ARG;
   if (q_row_stride < 0 || q_head_stride < 0 || q_row_stride % 8 != 0 || q_head_stride % 8 != 0 || q_row_stride > kIntMax ||
       q_head_stride > kIntMax || table_stride < table_width || table_stride > kIntMax)
@@ -243,7 +243,7 @@ gvr_status attend_decode(const gvr_cache* cache, const void* q, int64_t q_row_st
   const gvr_status s = check_attend(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table,
                                     table_stride, table_width, scale, out, lse);
   if (s != GVR_OK) return s;
-  if (next_n < 1 || next_n > 4096 || compress_ratio < 1 || (indices && (k < 1 || k > kIntMax))) return GVR_ERR_ARG;
+  if (next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N || compress_ratio < 1 || (indices && (k < 1 || k > kIntMax))) return GVR_ERR_ARG;
   if (num_rows == 0) return GVR_OK;
   if (!kv_lens) return GVR_ERR_NULL;
   if (!aligned(kv_lens, 4) || !aligned(indices, 4) || !aligned(workspace, 16)) return GVR_ERR_ALIGN;

@@ -206,3 +206,22 @@ def test_a_binding_that_does_not_say_what_it_was_built_for_is_not_used(gvr, monk
     monkeypatch.setitem(sys.modules, gvr.__name__ + "._native", gvr._native)
     with pytest.warns(RuntimeWarning, match="built for an unknown torch"):
         assert cache._short().cache_append() is None
+
+
+def test_limits_of_attention_stand_in_its_header(gvr):
+    """At the header's limits a call comes to the pointer it lacks; beyond them it is refused for its arguments."""
+    import ctypes
+    from sparse_attention_indexer_exact_gb300.cache import _Cache
+    header = open(os.path.join(ROOT, "include", "gvr_cache.h")).read()
+    assert "GVR_ATTEND_MAX_NEXT_N 4096\n" in header and "GVR_ATTEND_MAX_HEADS (1 << 20)\n" in header and "1 to 65535 */" in header
+    lib, at, missing, argument = gvr.load_library(), 0x10000, 1, 5  # an aligned address that is never read
+
+    def call(next_n=1, heads=4, kv_heads=2):  # without lengths, so refused in any case
+        cache = _Cache(at, 10, 16 * kv_heads * 144, 16, kv_heads, 128, 0, 1.0, 1.0)
+        return lib.attend_decode(ctypes.byref(cache), at, 512, 128, 0, 4, heads, at, 8, 8, None, next_n, 4, at, 32, 0.1, at, None,
+                                 None, 0, None)
+
+    for kw in (dict(next_n=4096), dict(heads=1 << 20), dict(heads=65535, kv_heads=65535)):
+        assert call(**kw) == missing, kw
+    for kw in (dict(next_n=0), dict(next_n=4097), dict(heads=(1 << 20) + 2), dict(heads=65536, kv_heads=65536)):
+        assert call(**kw) == argument, kw
