@@ -1,0 +1,76 @@
+/*
+ * gvr_long.h -- C ABI of libgvrtopk for caches that live long, over the 4-bit paged cache of
+ * gvr_cache.h: the attention weight that each cached entry draws, and eviction of the entries that
+ * draw least.
+ *
+ * Entries, cache, block tables, conventions and statuses are those of gvr_cache.h, with two
+ * differences: a call enqueues two kernels (attend_weights: one), and workspaces, where there are
+ * any, are required.  Their content is not kept between calls: calls that can overlap on the GPU, or graphs whose
+ * replays can, need one each.
+ */
+#ifndef GVR_LONG_H
+#define GVR_LONG_H
+
+#include "gvr_cache.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define GVR_LONG_MAX_REQUESTS 8192 /* requests, and groups, of a call */
+
+/*
+ * The attention weight that each entry draws: for every request b and entry e that it sees,
+ *   weights[b][e] += sum over its rows j that see e and their heads h of exp(scale * q[j][h] . k_e - lse[j][h]),
+ * the softmax weights of attend_decode without indices over the same arguments, whose lse this takes
+ * (fp32 [num_rows][num_heads]).  Everything up to next_n and compress_ratio is as there.
+ *   weights  fp32 [requests][weights_stride], weights_stride at least table_width * page_size; only the entries that some
+ *            row of the request sees are read and written.
+ * Sums are fp32 in a fixed order; an entry that lies on no page draws nothing.  At most GVR_LONG_MAX_REQUESTS requests.
+ */
+gvr_status attend_weights(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                          int32_t dtype, int64_t num_rows, int32_t num_heads, const int32_t* block_table,
+                          int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int32_t next_n,
+                          int32_t compress_ratio, const float* lse, float scale, float* weights,
+                          int64_t weights_stride, void* stream);
+
+/*
+ * Cut each request's cache to `keep` entries.  A request of n = kv_lens / compress_ratio entries (at most
+ * table_width * page_size) with n > keep keeps its last `recent` entries and of the others the keep - recent
+ * of largest weight, those of equal weight by lower number, a NaN before all numbers, -0 as 0.  They keep their order
+ * and become entries 0 .. keep - 1.  Pages before the first one in which an entry changes stay the request's; from there
+ * on entries are copied to pages taken from free_pages (ceil(keep / page_size) minus the staying ones, requests in
+ * order), and the request's old pages from there on are released.  No page that a request held is written: another
+ * request may hold it too, and releasing it means this request's hold alone.
+ *   weights      fp32 [num_requests][weights_stride], weights_stride at least table_width * page_size; of a request that is
+ *                cut, the kept entries' weights in their new places, and 0 from `keep` to n.
+ *   block_table  updated in place: new pages, and -1 for released ones that none replaces.
+ *   kept         int32 [num_requests][keep]: the old numbers of the entries that it has now, ascending, -1 behind them; of a request
+ *                with n <= keep all its entries.
+ *   new_lens     int32 [num_requests]: keep * compress_ratio + kv_lens % compress_ratio where it was cut, else kv_lens.
+ *   released     int32 [max_released]: released pages, requests in order, pages in order; -1 behind the last one.  What
+ *                it has no room for is only counted.
+ *   counts       int32 [3]: pages taken from free_pages, pages released, requests that were left as they were although n > keep:
+ *                those from the first one on that free_pages has no pages for (in order, none later is served), and requests with
+ *                an entry on no page.  Their row of kept is -1 alone.
+ * 1 <= keep < 2^31 / compress_ratio, 0 <= recent <= keep; num_requests at most GVR_LONG_MAX_REQUESTS, num_requests * table_width and
+ * num_requests * keep below 2^31.  free_pages: distinct page numbers not in use.  workspace: 16-byte aligned, cache_evict_workspace's bytes.
+ * weights, block_table, kept, new_lens, released and counts must not overlap.
+ */
+gvr_status cache_evict(const gvr_cache* cache, float* weights, int64_t weights_stride, int32_t* block_table,
+                       int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int64_t num_requests,
+                       int32_t compress_ratio, const int32_t* free_pages, int64_t num_free, int32_t keep, int32_t recent,
+                       int32_t* kept, int32_t* new_lens, int32_t* released, int64_t max_released, int32_t* counts,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that cache_evict needs. */
+gvr_status cache_evict_workspace(int64_t num_requests, int32_t keep, size_t* bytes);
+
+/* Static English text for a status returned by the functions of this header; never NULL. */
+const char* gvr_long_status_string(gvr_status status);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GVR_LONG_H */

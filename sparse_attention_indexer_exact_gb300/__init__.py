@@ -24,6 +24,11 @@ What a serving step needs around the selection (``include/gvr_cache.h``, ``cache
 * ``cache_append`` / ``cache_read`` -- a paged K/V cache held in 4 bits (``cache_alloc``);
 * ``attend_decode`` / ``attend_prefill`` -- attention over that cache at the selected entries, or
   (decode) over all of a request's entries.
+
+And around caches that live long (``include/gvr_long.h``, ``longcache.py``):
+
+* ``attend_weights`` -- the attention weight that each cached entry draws, added up;
+* ``cache_evict`` -- each request's cache cut to its heaviest and its latest entries.
 """
 from __future__ import annotations
 
@@ -32,8 +37,10 @@ import os
 import threading
 
 from . import cache as _cache
+from . import longcache as _longcache
 from .cache import (HEAD_DIMS, MAX_CACHE_REQUESTS, attend_decode, attend_prefill, cache_alloc, cache_append, cache_read,
                     cache_row_bytes, cache_tables)
+from .longcache import MAX_LONG_REQUESTS, attend_weights, cache_evict
 
 __all__ = ["topk_decode", "topk_prefill", "topk_decode_raw", "topk_decode_hinted_raw", "topk_decode_blockskip_raw",
            "topk_prefill_raw", "topk_decode_ws_raw", "topk_prefill_ws_raw", "topk_decode_noalloc_raw",
@@ -42,7 +49,7 @@ __all__ = ["topk_decode", "topk_prefill", "topk_decode_raw", "topk_decode_hinted
            "GvrError", "library_path", "load_library", "FLAG_FORCE_RESCUE", "FLAG_NO_FLOOR", "FLAG_ZERO_CAP",
            "FLAG_RADIX_REFINE", "FLAG_DETERMINISTIC", "FLAG_SORTED", "FLAG_STREAM_RESCUE", "FLAG_COMPACT_LISTS",
            "FLAG_CLUSTER_KERNEL", "FLAG_SPLIT_ALONE", "FLAG_SPLIT_KERNEL", "FLAG_DIAG_FAIL_ROW0", "FLAG_SHORT_KERNEL",
-           "FLAG_BLOCKSKIP_ALWAYS", "PATH_NAMES", "SUPPORTED_K", *_cache.__all__]
+           "FLAG_BLOCKSKIP_ALWAYS", "PATH_NAMES", "SUPPORTED_K", *_cache.__all__, *_longcache.__all__]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libgvrtopk.so")
@@ -59,7 +66,7 @@ PATH_NAMES = {-1: "device_error", 0: "short", 1: "refine", 2: "rescue_bracket", 
 SUPPORTED_K = (512, 1024, 2048)
 EXPORTED_SYMBOLS = ("topk_decode", "topk_prefill", "topk_decode_ex", "topk_prefill_ex", "topk_decode_hinted",
                     "topk_decode_blockskip", "topk_decode_ws", "topk_prefill_ws", "gvr_workspace_size",
-                    "topk_decode_noalloc", "gvr_status_string", "gvr_plan", *_cache.EXPORTED_SYMBOLS)
+                    "topk_decode_noalloc", "gvr_status_string", "gvr_plan", *_cache.EXPORTED_SYMBOLS, *_longcache.EXPORTED_SYMBOLS)
 
 
 class GvrError(RuntimeError):
@@ -102,6 +109,7 @@ def _declare(lib):
     lib.gvr_status_string.argtypes = [ctypes.c_int]
     lib.gvr_status_string.restype = ctypes.c_char_p
     _cache._declare(lib)
+    _longcache._declare(lib)
     return lib
 
 

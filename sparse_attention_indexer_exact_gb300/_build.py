@@ -1,10 +1,10 @@
 """Build step for libgvrtopk.so (the CUDA kernels and their C ABI), in-tree, for sm_103a.
 
 ``build_library()`` runs nvcc over each translation unit (``csrc/gvr_topk.cu``,
-``csrc_cache/*.cu``) at the same time, links them, and writes ``libgvrtopk.so``
-beside this file; it rebuilds only when a source is newer than the library.  No
-CMake, no torch extension machinery: the library is a plain shared object with
-an ``extern "C"`` interface (``include/gvr_topk.h``, ``include/gvr_cache.h``).
+``csrc_cache/*.cu``, ``csrc_long/*.cu``) at the same time, links them, and writes
+``libgvrtopk.so`` beside this file; it rebuilds only when a source is newer than the
+library.  No CMake, no torch extension machinery: the library is a plain shared object with
+an ``extern "C"`` interface (``include/gvr_topk.h``, ``gvr_cache.h``, ``gvr_long.h``).
 Beside it g++ builds ``_native.so`` (``_native.cpp``), the short way from torch
 tensors to the cache's calls, against the installed torch and the library.  The
 library does not need it, or torch: where those or Python's headers are not
@@ -28,6 +28,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 CSRC_CACHE = os.path.join(PKG, "csrc_cache")
+CSRC_LONG = os.path.join(PKG, "csrc_long")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libgvrtopk.so")
 NATIVE_SOURCE = os.path.join(PKG, "_native.cpp")
@@ -45,7 +46,7 @@ def nvcc_path() -> str:
 
 
 def sources() -> list[str]:
-    return sorted([f for d in (CSRC, CSRC_CACHE) for ext in ("*.cu", "*.cuh", "*.h") for f in glob.glob(os.path.join(d, ext))] +
+    return sorted([f for d in (CSRC, CSRC_CACHE, CSRC_LONG) for ext in ("*.cu", "*.cuh", "*.h") for f in glob.glob(os.path.join(d, ext))] +
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 
 

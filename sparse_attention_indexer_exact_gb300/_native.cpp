@@ -1,4 +1,4 @@
-// _native.cpp -- the short way from torch tensors to the C ABI of include/gvr_cache.h.
+// _native.cpp -- the short way from torch tensors to the C ABI of include/gvr_cache.h and gvr_long.h.
 //
 // A call of cache.py costs the host more than the GPU needs for the smallest ones, nearly all of it in
 // reading tensor properties from Python.  The functions here read them directly, make the call and
@@ -21,7 +21,7 @@
 #include <cmath>
 #include <optional>
 
-#include "gvr_cache.h"
+#include "gvr_long.h"
 
 namespace {
 
@@ -260,6 +260,75 @@ PyObject* prefill(PyObject* const* a) {
   return pair(x.out, x.lse);
 }
 
+struct Weights {
+  float* data;
+  int64_t stride;
+};
+
+Weights weights_of(const Where& w, const Tensor& t, int64_t requests, int64_t least) {
+  w.on(t, at::kFloat);
+  need(t.dim() == 2 && t.size(0) >= requests && t.size(1) >= least && (t.numel() == 0 || t.size(1) <= 1 || t.stride(1) == 1));
+  return {static_cast<float*>(t.data_ptr()), t.size(0) > 1 ? t.stride(0) : t.size(1)};
+}
+
+// (q, cache, k_scale, scale, block_table, kv_lens, next_n, compress_ratio, lse, weights)
+PyObject* entry_weights(PyObject* const* a) {
+  const Where w;
+  const Tensor &q = tensor(a[0]), &lse = tensor(a[8]);
+  const gvr_cache c = cache_of(w, tensor(a[1]), number(a[2]), 1.f);
+  const int32_t kind = dtype_of(q);
+  const Heads h = heads_of(w, q, c.head_dim);
+  const int64_t rows = q.size(0), heads = q.size(1);
+  need(heads > 0 && heads <= INT32_MAX && c.num_kv_heads > 0 && heads % c.num_kv_heads == 0);
+  const float scale = a[3] == Py_None ? float(1.0 / std::sqrt(double(c.head_dim))) : number(a[3]);
+  const int32_t next_n = integer32(a[6]), ratio = integer32(a[7]);
+  need(next_n >= 1);
+  const int64_t requests = (rows + next_n - 1) / next_n;
+  const Table t = table_of(w, tensor(a[4]), requests);
+  const int32_t* lens = int32s(w, tensor(a[5]), requests);
+  w.on(lse, at::kFloat);
+  need(lse.dim() == 2 && lse.size(0) == rows && lse.size(1) == heads && lse.is_contiguous());
+  const Weights to = weights_of(w, tensor(a[9]), requests, t.width * c.page_size);
+  need(attend_weights(&c, h.data, h.row, h.head, kind, rows, int32_t(heads), t.data, t.stride, t.width, lens, next_n, ratio,
+                      static_cast<const float*>(lse.data_ptr()), scale, to.data, to.stride, w.stream) == GVR_OK);
+  Py_RETURN_TRUE;
+}
+
+// An int32 output: new, or the caller's if it has this very shape.
+Tensor ints(const Where& w, PyObject* o, at::IntArrayRef size) {
+  if (o == Py_None) return w.empty(size, at::kInt);
+  const Tensor& t = w.on(tensor(o), at::kInt);
+  need(t.sizes() == size && t.is_contiguous());
+  return t;
+}
+
+// (weights, cache, block_table, kv_lens, free_pages, keep, recent, compress_ratio, max_released, kept, new_lens, released, counts)
+PyObject* evict(PyObject* const* a) {
+  const Where w;
+  const gvr_cache c = cache_of(w, tensor(a[1]), 1.f, 1.f);
+  const Tensor &lens = tensor(a[3]), &free_pages = tensor(a[4]);
+  need(lens.dim() == 1);
+  const int64_t requests = lens.size(0), most = integer(a[8]);
+  const int32_t *lens_at = int32s(w, lens, 0), *free_at = int32s(w, free_pages, 0);
+  const int32_t keep = integer32(a[5]), recent = integer32(a[6]), ratio = integer32(a[7]);
+  const Table t = table_of(w, tensor(a[2]), requests);
+  const Weights x = weights_of(w, tensor(a[0]), requests, t.width * c.page_size);
+  size_t bytes = 0;
+  need(most >= 0 && most <= INT32_MAX && cache_evict_workspace(requests, keep, &bytes) == GVR_OK);
+  const Tensor out[4] = {ints(w, a[9], {requests, keep}), ints(w, a[10], {requests}), ints(w, a[11], {most}), ints(w, a[12], {3})};
+  const Tensor space = w.empty({int64_t(bytes)}, at::kByte);
+  auto at = [&](int i) { return static_cast<int32_t*>(out[i].data_ptr()); };
+  need(cache_evict(&c, x.data, x.stride, t.data, t.stride, t.width, lens_at, requests, ratio, free_at, free_pages.size(0), keep, recent,
+                   at(0), at(1), at(2), most, at(3), space.data_ptr(), bytes, w.stream) == GVR_OK);
+  PyObject* r = PyTuple_New(4);
+  for (int i = 0; r && i < 4; ++i) {
+    PyObject* o = THPVariable_Wrap(out[i]);
+    if (!o) Py_CLEAR(r);
+    else PyTuple_SET_ITEM(r, i, o);
+  }
+  return r;
+}
+
 template <PyObject* (*call)(PyObject* const*), int arguments>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n == arguments) {
@@ -279,7 +348,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<tables, 9>("cache_tables"), method<append, 6>("cache_append"), method<read, 6>("cache_read"),
-                         method<decode, 13>("attend_decode"), method<prefill, 13>("attend_prefill"), {nullptr, nullptr, 0, nullptr}};
+                         method<decode, 13>("attend_decode"), method<prefill, 13>("attend_prefill"),
+                         method<entry_weights, 10>("attend_weights"), method<evict, 13>("cache_evict"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The short way from tensors to the cache kernels.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

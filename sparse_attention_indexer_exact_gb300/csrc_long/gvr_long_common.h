@@ -1,0 +1,31 @@
+// gvr_long_common.h -- what the host code of include/gvr_long.h shares: the checks of a call's rows.
+#pragma once
+
+#include <cmath>
+
+#include "../csrc_cache/gvr_cache_common.cuh"
+#include "gvr_long.h"
+
+namespace gvrc {
+
+// The arguments that attend_shared and attend_weights have in common, as attend_decode checks them.
+inline gvr_status check_rows(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t dtype,
+                             int64_t num_rows, int32_t num_heads, const int32_t* table, int64_t table_stride,
+                             int64_t table_width, const int32_t* lens, int32_t next_n, int32_t ratio, float scale) {
+  const gvr_status s = check_cache(cache);
+  if (s != GVR_OK) return s;
+  if ((dtype != GVR_BF16 && dtype != GVR_F16) || num_rows < 0 || num_heads < 1 || num_heads % cache->num_kv_heads != 0 ||
+      num_heads > GVR_ATTEND_MAX_HEADS || !std::isfinite(float(double(scale) * cache->k_scale * 1.4426950408889634)) || table_width < 0 ||
+      table_width > kIntMax / cache->page_size || next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N || ratio < 1 ||
+      int64_t(next_n) * (num_heads / cache->num_kv_heads) > (1 << 20) || (num_rows + next_n - 1) / next_n > GVR_LONG_MAX_REQUESTS)
+    return GVR_ERR_ARG;
+  if (q_row_stride < 0 || q_head_stride < 0 || q_row_stride % 8 != 0 || q_head_stride % 8 != 0 || q_row_stride > kIntMax ||
+      q_head_stride > kIntMax || table_stride < table_width || table_stride > kIntMax)
+    return GVR_ERR_STRIDE;
+  if (num_rows == 0) return GVR_OK;
+  if (!q || !lens || (table_width > 0 && !table)) return GVR_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(table, 4) || !aligned(lens, 4)) return GVR_ERR_ALIGN;
+  return GVR_OK;
+}
+
+}  // namespace gvrc
