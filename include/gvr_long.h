@@ -1,10 +1,10 @@
 /*
  * gvr_long.h -- C ABI of libgvrtopk for caches that live long, over the 4-bit paged cache of
- * gvr_cache.h: the attention weight that each cached entry draws, and eviction of the entries that
- * draw least.
+ * gvr_cache.h: attention of requests that share long prefixes, the attention weight that each cached
+ * entry draws, and eviction of the entries that draw least.
  *
  * Entries, cache, block tables, conventions and statuses are those of gvr_cache.h, with two
- * differences: a call enqueues two kernels (attend_weights: one), and workspaces, where there are
+ * differences: a call enqueues two or three kernels (attend_weights: one), and workspaces, where there are
  * any, are required.  Their content is not kept between calls: calls that can overlap on the GPU, or graphs whose
  * replays can, need one each.
  */
@@ -18,6 +18,35 @@ extern "C" {
 #endif
 
 #define GVR_LONG_MAX_REQUESTS 8192 /* requests, and groups, of a call */
+
+/*
+ * Whole-cache attention of decode rows (attend_decode without indices) whose requests share prefixes:
+ * each group's prefix is read once for all rows of the group.
+ *   group_starts    int32 [num_groups + 1]: group g is the requests [group_starts[g], group_starts[g + 1]).
+ *                   Requests before the first and behind the last are in no group.  A start below one before it
+ *                   counts as that one, a negative one as 0, one beyond the requests as their number.
+ *   prefix_entries  int32 [num_groups]: the first prefix_entries[g] entries of all requests of the group
+ *                   are the same.  The caller vouches for it; they are read through the block table of the
+ *                   group's first request that has that many.  (Usually its full pages are the very same pages.  The
+ *                   page in which a prefix ends may be each request's own copy.)  Negative counts as 0.
+ * A request whose rows do not all see the whole prefix, and a request alone in its group, is attended as one in no
+ * group.  num_groups 0 to GVR_LONG_MAX_REQUESTS (0: the pointers may be NULL), and as many requests.
+ * Result, roundings and everything else are as in attend_decode without indices; next_n times num_heads /
+ * num_kv_heads is at most 2^20.
+ *   workspace       16-byte aligned, attend_shared_workspace's bytes.
+ * Every wait inside the kernel is bounded (0.5 s): should one give up, which is not expected on a healthy GPU, all of
+ * out and lse are NaN.
+ */
+gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         int32_t dtype, int64_t num_rows, int32_t num_heads, const int32_t* block_table,
+                         int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int32_t next_n,
+                         int32_t compress_ratio, const int32_t* group_starts, const int32_t* prefix_entries,
+                         int64_t num_groups, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that attend_shared needs on the current device for a cache of num_kv_heads heads of head_dim. */
+gvr_status attend_shared_workspace(int32_t num_kv_heads, int32_t head_dim, int64_t num_rows, int32_t num_heads,
+                                   int32_t next_n, int64_t num_groups, size_t* bytes);
 
 /*
  * The attention weight that each entry draws: for every request b and entry e that it sees,

@@ -27,6 +27,7 @@ What a serving step needs around the selection (``include/gvr_cache.h``, ``cache
 
 And around caches that live long (``include/gvr_long.h``, ``longcache.py``):
 
+* ``attend_shared`` -- whole-cache attention whose requests share prefixes, each read once;
 * ``attend_weights`` -- the attention weight that each cached entry draws, added up;
 * ``cache_evict`` -- each request's cache cut to its heaviest and its latest entries.
 """
@@ -40,7 +41,7 @@ from . import cache as _cache
 from . import longcache as _longcache
 from .cache import (HEAD_DIMS, MAX_CACHE_REQUESTS, attend_decode, attend_prefill, cache_alloc, cache_append, cache_read,
                     cache_row_bytes, cache_tables)
-from .longcache import MAX_LONG_REQUESTS, attend_weights, cache_evict
+from .longcache import MAX_LONG_REQUESTS, attend_shared, attend_weights, cache_evict
 
 __all__ = ["topk_decode", "topk_prefill", "topk_decode_raw", "topk_decode_hinted_raw", "topk_decode_blockskip_raw",
            "topk_prefill_raw", "topk_decode_ws_raw", "topk_prefill_ws_raw", "topk_decode_noalloc_raw",

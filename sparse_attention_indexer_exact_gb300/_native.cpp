@@ -260,6 +260,28 @@ PyObject* prefill(PyObject* const* a) {
   return pair(x.out, x.lse);
 }
 
+// (q, cache, k_scale, v_scale, scale, out, lse, want_lse, block_table, kv_lens, next_n, compress_ratio, group_starts, prefix_entries)
+PyObject* entry_shared(PyObject* const* a) {
+  const Where w;
+  const Attend x(w, a);
+  const int32_t next_n = integer32(a[10]), ratio = integer32(a[11]);
+  need(next_n >= 1);
+  const int64_t requests = (x.rows + next_n - 1) / next_n;
+  const Table t = table_of(w, tensor(a[8]), requests);
+  const int32_t* lens = int32s(w, tensor(a[9]), requests);
+  const Tensor& prefix = tensor(a[13]);
+  const int32_t* prefix_at = int32s(w, prefix, 0);
+  const int64_t groups = prefix.size(0);
+  const int32_t* starts = int32s(w, tensor(a[12]), groups ? groups + 1 : 0);
+  size_t bytes = 0;
+  need(attend_shared_workspace(x.c.num_kv_heads, x.c.head_dim, x.rows, int32_t(x.heads), next_n, groups, &bytes) == GVR_OK);
+  const Tensor space = w.empty({int64_t(bytes)}, at::kByte);
+  need(attend_shared(&x.c, x.q.data, x.q.row, x.q.head, x.kind, x.rows, int32_t(x.heads), t.data, t.stride, t.width, lens, next_n, ratio,
+                     starts, prefix_at, groups, x.scale, x.out.data_ptr(), static_cast<float*>(x.lse_at), space.data_ptr(), bytes,
+                     w.stream) == GVR_OK);
+  return pair(x.out, x.lse);
+}
+
 struct Weights {
   float* data;
   int64_t stride;
@@ -349,7 +371,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<tables, 9>("cache_tables"), method<append, 6>("cache_append"), method<read, 6>("cache_read"),
                          method<decode, 13>("attend_decode"), method<prefill, 13>("attend_prefill"),
-                         method<entry_weights, 10>("attend_weights"), method<evict, 13>("cache_evict"), {nullptr, nullptr, 0, nullptr}};
+                         method<entry_shared, 14>("attend_shared"), method<entry_weights, 10>("attend_weights"), method<evict, 13>("cache_evict"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", "The short way from tensors to the cache kernels.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

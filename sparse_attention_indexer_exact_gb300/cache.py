@@ -117,7 +117,7 @@ class _NoShortWay:
         return None
 
     cache_tables = cache_append = cache_read = attend_decode = attend_prefill = _nothing
-    attend_weights = cache_evict = _nothing  # longcache.py
+    attend_shared = attend_weights = cache_evict = _nothing  # longcache.py
 
 
 def _short():

@@ -1,0 +1,157 @@
+// gvr_shared.cu -- attend_shared of include/gvr_long.h: argument checks, workspace and launches of the kernels of
+// gvr_shared.cuh.
+#include <algorithm>
+#include <mutex>
+
+#include "gvr_shared.cuh"
+
+namespace gvrc {
+namespace {
+
+const SharedInfo& shared_kernels(int dim) {
+  static const SharedInfo all[3] = {shared_64(), shared_128(), shared_256()};
+  return all[dim == 64 ? 0 : dim == 128 ? 1 : 2];
+}
+
+struct SharedDevice {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+SharedDevice g_shared_devices[kMaxDevices];
+
+// Where everything lies in the workspace.
+struct Layout {
+  int64_t plan, sets, joined, cta_set, prefix, suffix, bytes;
+  int32_t suffix_rows;
+};
+
+int64_t align16(int64_t x) { return (x + 15) / 16 * 16; }
+
+gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group, int64_t num_rows, int64_t next_n, int64_t groups, int64_t grid, Layout* l) {
+  const int64_t requests = (num_rows + next_n - 1) / next_n, members = next_n * group;
+  const int64_t tiles = (members + k.queries - 1) / k.queries;
+  // a group has its queries / k.queries tiles and at most one more
+  const int64_t prefix_units = groups > 0 ? kv_heads * (num_rows * group / k.queries + groups) : 0;
+  const int64_t suffix_units = requests * kv_heads * tiles;
+  if (prefix_units > kIntMax / 2 || suffix_units > kIntMax / 2) return GVR_ERR_ARG;
+  l->suffix_rows = int32_t(std::min<int64_t>(128, (members + 7) / 8 * 8));
+  const int64_t suffix_floats = int64_t(k.tiles) * l->suffix_rows * (dim + 2);
+  l->plan = 0;
+  l->sets = align16(sizeof(Plan));
+  l->joined = l->sets + align16((groups + requests) * int64_t(sizeof(Set)));
+  l->cta_set = l->joined + align16(requests * int64_t(sizeof(Joined)));
+  l->prefix = l->cta_set + align16(grid * 4);
+  l->suffix = l->prefix + (groups > 0 ? (grid + prefix_units) * k.piece_floats * 4 : 0);
+  l->bytes = l->suffix + (grid + suffix_units) * suffix_floats * 4;
+  return GVR_OK;
+}
+
+}  // namespace
+}  // namespace gvrc
+
+extern "C" {
+
+gvr_status attend_shared_workspace(int32_t num_kv_heads, int32_t head_dim, int64_t num_rows, int32_t num_heads,
+                                   int32_t next_n, int64_t num_groups, size_t* bytes) {
+  using namespace gvrc;
+  if (!bytes) return GVR_ERR_NULL;
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || num_kv_heads < 1 || num_kv_heads > 65535 || num_rows < 0 || num_heads < 1 ||
+      num_heads % num_kv_heads != 0 || num_heads > GVR_ATTEND_MAX_HEADS || next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N ||
+      int64_t(next_n) * (num_heads / num_kv_heads) > (1 << 20) || num_groups < 0 || num_groups > GVR_LONG_MAX_REQUESTS ||
+      num_rows > int64_t(GVR_LONG_MAX_REQUESTS) * next_n)
+    return GVR_ERR_ARG;
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) return GVR_ERR_LAUNCH;
+  Layout l = {};
+  const gvr_status s = layout(shared_kernels(head_dim), head_dim, num_kv_heads, num_heads / num_kv_heads, num_rows, next_n, num_groups, sms, &l);
+  *bytes = size_t(l.bytes);
+  return s;
+}
+
+gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         int32_t dtype, int64_t num_rows, int32_t num_heads, const int32_t* block_table,
+                         int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int32_t next_n,
+                         int32_t compress_ratio, const int32_t* group_starts, const int32_t* prefix_entries,
+                         int64_t num_groups, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  using namespace gvrc;
+  const gvr_status s = check_rows(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table, table_stride, table_width,
+                                  kv_lens, next_n, compress_ratio, scale);
+  if (s != GVR_OK) return s;
+  if (num_groups < 0 || num_groups > GVR_LONG_MAX_REQUESTS) return GVR_ERR_ARG;
+  if (num_rows == 0) return GVR_OK;
+  if (!out || (num_groups > 0 && (!group_starts || !prefix_entries))) return GVR_ERR_NULL;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(group_starts, 4) || !aligned(prefix_entries, 4)) return GVR_ERR_ALIGN;
+  const int dim = cache->head_dim, row = row_bytes(dim);
+  const SharedInfo& k = shared_kernels(dim);
+  SharedParams p = {};
+  p.kv_heads = cache->num_kv_heads;
+  p.group = num_heads / cache->num_kv_heads;
+  p.capacity = cache->num_pages > 0 ? int32_t(table_width * cache->page_size) : 0;
+  p.requests = int32_t((num_rows + next_n - 1) / next_n);
+  // work is counted in 32 bits: each unit's steps, twice where two tiles take them
+  const int64_t steps = (int64_t(p.capacity) + k.step - 1) / k.step, members = int64_t(next_n) * p.group;
+  const int64_t units = int64_t(p.kv_heads) * (num_rows * p.group / k.queries + num_groups + p.requests * ((members + k.queries - 1) / k.queries));
+  if (units > kIntMax / 2 || (steps > 0 && units > kIntMax / 2 / steps)) return GVR_ERR_ARG;
+  int sms = 0, dev = 0;
+  if (sm_count(&sms) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return GVR_ERR_LAUNCH;
+  Layout l = {};
+  const gvr_status fits = layout(k, dim, p.kv_heads, p.group, num_rows, next_n, num_groups, sms, &l);
+  if (fits != GVR_OK) return fits;
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < size_t(l.bytes)) return GVR_ERR_WORKSPACE;
+  SharedDevice& d = g_shared_devices[dev];  // sm_count has checked dev
+  std::call_once(d.once, [&d]() {
+    for (int each : {64, 128, 256}) {
+      const SharedInfo& i = shared_kernels(each);
+      if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(i.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, i.smem);
+      if (d.err == cudaSuccess)
+        d.err = cudaFuncSetAttribute(i.plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (5 * GVR_LONG_MAX_REQUESTS + 1) * 4);
+    }
+  });
+  if (d.err != cudaSuccess) return GVR_ERR_LAUNCH;
+  p.data = static_cast<const uint8_t*>(cache->data);
+  p.q = static_cast<const uint16_t*>(q);
+  p.table = block_table;
+  p.lens = kv_lens;
+  p.group_starts = group_starts;
+  p.prefix_entries = prefix_entries;
+  p.out = out;
+  p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.plan = reinterpret_cast<Plan*>(ws + l.plan);
+  p.sets = reinterpret_cast<Set*>(ws + l.sets);
+  p.joined = reinterpret_cast<Joined*>(ws + l.joined);
+  p.cta_set = reinterpret_cast<int32_t*>(ws + l.cta_set);
+  p.prefix_pieces = reinterpret_cast<float*>(ws + l.prefix);
+  p.suffix_pieces = reinterpret_cast<float*>(ws + l.suffix);
+  p.suffix_rows = l.suffix_rows;
+  p.q_row = q_row_stride;
+  p.q_head = q_head_stride;
+  p.table_stride = table_stride;
+  p.num_rows = num_rows;
+  p.unit = unit_bytes(cache->page_stride, row);
+  p.page_units = uint32_t(cache->page_stride / p.unit);
+  p.row_units = row / p.unit;
+  p.entry_units = p.row_units * cache->num_kv_heads;
+  p.num_pages = int32_t(cache->num_pages);
+  p.page_shift = log2_of(cache->page_size);
+  p.next_n = next_n;
+  p.ratio = compress_ratio;
+  p.bf16 = dtype == GVR_BF16;
+  p.groups = int32_t(num_groups);
+  p.grid = sms;
+  p.scale_log2 = scale == 0.f ? 1.f : float(std::fabs(double(scale)) * cache->k_scale * 1.4426950408889634);
+  p.q_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+  p.v_scale = cache->v_scale;
+  void* args[] = {&p};
+  const int plan_smem = int(4 * num_groups + 1 + p.requests) * 4;
+  cudaError_t e = launch(k.plan, dim3(1), PLAN_THREADS, plan_smem, 1, args, stream);
+  if (e == cudaSuccess) e = launch(k.kernel, dim3(uint32_t(sms)), k.threads, k.smem, 1, args, stream);
+  if (e == cudaSuccess) {
+    const int64_t parts = (members * (dim / 4) + 2 * JOIN_SHARED_THREADS - 1) / (2 * JOIN_SHARED_THREADS);  // two items a thread
+    e = launch(k.join, dim3(uint32_t(p.requests) * uint32_t(p.kv_heads), uint32_t(std::min<int64_t>(parts, 65535))), JOIN_SHARED_THREADS, 0, 1, args, stream);
+  }
+  return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
+}
+
+}  // extern "C"

@@ -3,7 +3,7 @@
 Bindings of ``include/gvr_long.h``, in the manner of ``cache.py`` and over the same 4-bit cache.  They are
 for serving: no gradient passes through them.  A layer that reads its whole cache, in call order::
 
-    out, lse = attend_decode(q, cache, block_table, kv_lens, next_n, cr, want_lse=True)
+    out, lse = attend_shared(q, cache, block_table, kv_lens, next_n, cr, group_starts, prefix_entries, want_lse=True)
     attend_weights(q, cache, block_table, kv_lens, next_n, cr, lse, weights)      # weights += what each entry drew
 
 and once the caches have grown over their budget::
@@ -16,18 +16,20 @@ import ctypes
 import math
 
 from . import cache as _c
-from .cache import _Cache, _cache_struct, _current, _device, _dtype, _heads_3d, _int32, _int32_value, _launch, _on, _table_2d
+from .cache import _attend, _Cache, _cache_struct, _current, _device, _dtype, _heads_3d, _int32, _int32_value, _launch, _on, _table_2d
 
-__all__ = ["attend_weights", "cache_evict", "MAX_LONG_REQUESTS"]
+__all__ = ["attend_shared", "attend_weights", "cache_evict", "MAX_LONG_REQUESTS"]
 
 MAX_LONG_REQUESTS = 8192
 
-EXPORTED_SYMBOLS = ("attend_weights", "cache_evict", "cache_evict_workspace", "gvr_long_status_string")
+EXPORTED_SYMBOLS = ("attend_shared", "attend_shared_workspace", "attend_weights", "cache_evict", "cache_evict_workspace", "gvr_long_status_string")
 
 
 def _declare(lib):
     i64, i32, p, f32, sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
     cache = ctypes.POINTER(_Cache)
+    lib.attend_shared.argtypes = [cache, p, i64, i64, i32, i64, i32, p, i64, i64, p, i32, i32, p, p, i64, f32, p, p, p, sz, p]
+    lib.attend_shared_workspace.argtypes = [i32, i32, i64, i32, i32, i64, ctypes.POINTER(sz)]
     lib.attend_weights.argtypes = [cache, p, i64, i64, i32, i64, i32, p, i64, i64, p, i32, i32, p, f32, p, i64, p]
     lib.cache_evict.argtypes = [cache, p, i64, p, i64, i64, p, i64, i32, p, i64, i32, i32, p, p, p, i64, p, p, sz, p]
     lib.cache_evict_workspace.argtypes = [i64, i32, ctypes.POINTER(sz)]
@@ -67,8 +69,43 @@ def _weights_2d(t, device: int, requests, least):
     return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
 
 
+def attend_shared(q, cache, block_table, kv_lens, next_n: int, compress_ratio: int, group_starts, prefix_entries, *, scale=None,
+                  k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False, stream=None):
+    """:func:`attend_decode` over whole caches, without indices, for requests that share prefixes; returns (out, lse or None).
+
+    ``group_starts`` (int32 [groups + 1]) cuts the requests into groups: group g is requests group_starts[g] up to
+    group_starts[g + 1].  The first ``prefix_entries[g]`` entries (int32 [groups]) of all its requests are the same, as
+    they are behind one prompt: they are read once for the whole group.  The result is that of ``attend_decode``.
+    """
+    if stream is not None:
+        with _current(stream, q):
+            return attend_shared(q, cache, block_table, kv_lens, next_n, compress_ratio, group_starts, prefix_entries, scale=scale,
+                                 k_scale=k_scale, v_scale=v_scale, out=out, lse=lse, want_lse=want_lse)
+    done = (_c._native or _c._short()).attend_shared(q, cache, k_scale, v_scale, scale, out, lse, want_lse, block_table, kv_lens,
+                                                     next_n, compress_ratio, group_starts, prefix_entries)
+    if done is not None:
+        return done
+    import torch
+    next_n, compress_ratio = _int32_value(next_n, "next_n"), _int32_value(compress_ratio, "compress_ratio")
+    device, head, scale, out, lse = _attend(q, cache, k_scale, v_scale, scale, out, lse, want_lse)
+    c, rows, heads = head[0], head[5], head[6]
+    requests = (rows + next_n - 1) // max(next_n, 1)
+    table, table_stride, width = _table_2d(block_table, device, requests)
+    lens = _int32(kv_lens, device, "kv_lens", requests)
+    prefix = _int32(prefix_entries, device, "prefix_entries")
+    groups = prefix_entries.shape[0]
+    starts = _int32(group_starts, device, "group_starts", groups + 1 if groups else 0)
+    lib, size = _c._library(), ctypes.c_size_t(0)
+    with torch.cuda.device(device):  # as many pieces as it has SMs
+        _check(lib, lib.attend_shared_workspace(c.num_kv_heads, c.head_dim, rows, heads, next_n, groups, ctypes.byref(size)))
+    space = torch.empty(size.value, dtype=torch.uint8, device=q.device)
+    _call(device, lib.attend_shared, *head, table, table_stride, width, lens, next_n, compress_ratio, starts, prefix, groups, scale,
+          out.data_ptr(), None if lse is None else lse.data_ptr(), space.data_ptr(), size.value)
+    return out, lse
+
+
 def _rows(q, cache, k_scale, v_scale, scale):
-    """What the attention calls check of queries and cache: (device, arguments, scale)."""
+    """What attend_weights checks of queries and cache: (device, arguments, scale)."""
     c = _cache_struct(cache, k_scale, v_scale)
     device = cache.get_device()
     _on(q, device, "q")
