@@ -21,11 +21,35 @@ SharedDevice g_shared_devices[kMaxDevices];
 
 // Where everything lies in the workspace.
 struct Layout {
-  int64_t plan, sets, joined, cta_set, prefix, suffix, bytes;
+  int64_t plan, sets, joined, cta_set, cta_start, prefix, suffix, bytes;
   int32_t suffix_rows;
 };
 
 int64_t align16(int64_t x) { return (x + 15) / 16 * 16; }
+
+// The driver's encoder of tensor maps.
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+  static const Encode f = []() -> Encode {
+    void* at = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault, &found) != cudaSuccess || found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<Encode>(at);
+  }();
+  return f;
+}
+
+// The cache as words [pages][entries][row words of all heads], copied by a head's rows of up to `step` entries of a page.
+bool tensor_map(const gvr_cache* c, int step, CUtensorMap* map) {
+  const Encode encode = encoder();
+  const cuuint64_t row = row_bytes(c->head_dim), entry = row * c->num_kv_heads;
+  const cuuint64_t size[3] = {entry / 4, cuuint64_t(c->page_size), cuuint64_t(c->num_pages)}, stride[2] = {entry, cuuint64_t(c->page_stride)};
+  const cuuint32_t box[3] = {cuuint32_t(row / 4), cuuint32_t(std::min(c->page_size, step)), 1}, each[3] = {1, 1, 1};
+  return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, c->data, size, stride, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group, int64_t num_rows, int64_t next_n, int64_t groups, int64_t grid, Layout* l) {
   const int64_t requests = (num_rows + next_n - 1) / next_n, members = next_n * group;
@@ -40,7 +64,8 @@ gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group,
   l->sets = align16(sizeof(Plan));
   l->joined = l->sets + align16((groups + requests) * int64_t(sizeof(Set)));
   l->cta_set = l->joined + align16(requests * int64_t(sizeof(Joined)));
-  l->prefix = l->cta_set + align16(grid * 4);
+  l->cta_start = l->cta_set + align16(grid * 4);
+  l->prefix = l->cta_start + align16((grid + 1) * 4);
   l->suffix = l->prefix + (groups > 0 ? (grid + prefix_units) * k.piece_floats * 4 : 0);
   l->bytes = l->suffix + (grid + suffix_units) * suffix_floats * 4;
   return GVR_OK;
@@ -89,8 +114,8 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   p.group = num_heads / cache->num_kv_heads;
   p.capacity = cache->num_pages > 0 ? int32_t(table_width * cache->page_size) : 0;
   p.requests = int32_t((num_rows + next_n - 1) / next_n);
-  // work is counted in 32 bits: each unit's steps, twice where two tiles take them
-  const int64_t steps = (int64_t(p.capacity) + k.step - 1) / k.step, members = int64_t(next_n) * p.group;
+  // work is counted in 32 bits: each unit's steps, twice where two tiles take them, and what it costs beside
+  const int64_t steps = (int64_t(p.capacity) + k.step - 1) / k.step + UNIT_WORK, members = int64_t(next_n) * p.group;
   const int64_t units = int64_t(p.kv_heads) * (num_rows * p.group / k.queries + num_groups + p.requests * ((members + k.queries - 1) / k.queries));
   if (units > kIntMax / 2 || (steps > 0 && units > kIntMax / 2 / steps)) return GVR_ERR_ARG;
   int sms = 0, dev = 0;
@@ -122,6 +147,7 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   p.sets = reinterpret_cast<Set*>(ws + l.sets);
   p.joined = reinterpret_cast<Joined*>(ws + l.joined);
   p.cta_set = reinterpret_cast<int32_t*>(ws + l.cta_set);
+  p.cta_start = reinterpret_cast<int32_t*>(ws + l.cta_start);
   p.prefix_pieces = reinterpret_cast<float*>(ws + l.prefix);
   p.suffix_pieces = reinterpret_cast<float*>(ws + l.suffix);
   p.suffix_rows = l.suffix_rows;
@@ -143,12 +169,14 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   p.scale_log2 = scale == 0.f ? 1.f : float(std::fabs(double(scale)) * cache->k_scale * 1.4426950408889634);
   p.q_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
   p.v_scale = cache->v_scale;
-  void* args[] = {&p};
+  CUtensorMap map = {};
+  if (p.page_shift >= 3 && p.num_pages > 0 && !tensor_map(cache, k.step, &map)) return GVR_ERR_LAUNCH;
+  void* args[] = {&p, &map};
   const int plan_smem = int(4 * num_groups + 1 + p.requests) * 4;
   cudaError_t e = launch(k.plan, dim3(1), PLAN_THREADS, plan_smem, 1, args, stream);
   if (e == cudaSuccess) e = launch(k.kernel, dim3(uint32_t(sms)), k.threads, k.smem, 1, args, stream);
   if (e == cudaSuccess) {
-    const int64_t parts = (members * (dim / 4) + 2 * JOIN_SHARED_THREADS - 1) / (2 * JOIN_SHARED_THREADS);  // two items a thread
+    const int64_t at_once = JOIN_SHARED_THREADS / JOIN_WAYS, parts = (members * (dim / 4) + at_once - 1) / at_once;
     e = launch(k.join, dim3(uint32_t(p.requests) * uint32_t(p.kv_heads), uint32_t(std::min<int64_t>(parts, 65535))), JOIN_SHARED_THREADS, 0, 1, args, stream);
   }
   return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;

@@ -9,13 +9,16 @@
 // into equal ranges, one a CTA of an SM.  A CTA walks over its range, unit by unit, and leaves a piece for each: sums over
 // exp2(score - base) v, base and sum.  A last kernel joins the pieces of every query.  Every sum has a fixed order.
 //
-// A CTA.  Four warps bring K and four bring V: rows of codes and scales arrive by asynchronous copies, are expanded
-// (e2m1 times e4m3 is exact in f16) and laid into shared memory as matrix operands.  One thread issues the products
+// A CTA.  One warp walks over the share: it notes the segments for the others and starts the copies of their rows, a
+// page's rows of a head (up to a step's) a bulk tensor copy.  Four warps expand K and four V (e2m1 times e4m3 is exact
+// in f16), from there into matrix operands in shared memory.  One thread issues the products
 // S = Q K^T and O += P V on the fifth-generation tensor cores, 128 queries a tile: S and O lie in tensor memory.  Four warps a
 // tile take S, a query a thread, so that maximum, base and sum need no exchange, and write P, in f16, over it; P is read
 // from there as an operand.  Two tiles take turns: while one's P is made, the other's products run.  Where a unit
 // has up to 128 queries both tiles hold them, one taking the even steps, one the odd ones.
 #pragma once
+
+#include <cuda.h>
 
 #include "../csrc_cache/gvr_attend.cuh"
 #include "gvr_long_common.h"
@@ -65,6 +68,7 @@ struct SharedParams {
   Set* sets;          // [groups + requests]
   Joined* joined;     // [requests]
   int32_t* cta_set;   // [grid]: the set in which a CTA's share begins
+  int32_t* cta_start;  // [grid + 1]: where it begins
   float* prefix_pieces;
   float* suffix_pieces;
   int64_t q_row, q_head, table_stride, num_rows;
@@ -78,23 +82,26 @@ template <int D>
 struct SharedShape {
   static constexpr int N = D == 256 ? 64 : 128;      // entries a step
   static constexpr int TILES = D == 256 ? 1 : 2;     // O takes D columns of tensor memory a tile, S two times N
-  static constexpr int KBUF = 2, VBUF = D == 64 ? 2 : 1;
-  static constexpr int STAGES = 3;                   // of raw rows
   static constexpr int QUERIES = 128 * TILES;        // of a unit
-  static constexpr int ROWS = N / 4;                 // rows a warp brings in a step
-  static constexpr int PITCH = (D / 2 + D / 16 + 15) / 16 * 16 | 16;  // of a raw row: codes and scales of K or V
-  static constexpr int RING = STAGES * ROWS * PITCH;  // of a warp
+  static constexpr int ROWS = N / 4;                 // rows a warp expands in a step
   static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = N * D * 2;
-  static constexpr int WARPS = 4 * TILES + 9, THREADS = 32 * WARPS;
+  static constexpr int RB = row_bytes(D), RAW = N * RB, STAGES = 3;  // rows as they are, of the steps under way
+  static constexpr int WARPS = 4 * TILES + 12, THREADS = 32 * WARPS;  // S takers, K and V, and the issuer, the walker and two idle ones
   static constexpr int PIECE = QUERIES * (D + 2);    // floats of a prefix piece
-  static constexpr int S_AT = 0, O_AT = 2 * N;       // columns
+  static constexpr int S_AT = 0, O_AT = 2 * N;  // columns; P lies over its scores
   static constexpr int NAN_SLOTS = 4;
-  static constexpr int SMEM = TILES * Q_BYTES + (KBUF + VBUF) * KV_BYTES + 8 * RING + 1024;  // 1024 to align
+  static constexpr int SMEM = TILES * Q_BYTES + 3 * KV_BYTES + STAGES * RAW + 1024;  // two of K, one of V; 1024 to align
+  // Registers of a thread: those who take S hold a row of it.  Their sum is what the CTA is launched with (640 threads of
+  // 96; head_dim 256: 512 of 128, which need no exchange).
+  static constexpr int SOFT_REGS = 152, BRING_REGS = 64, REST_REGS = 48;
 };
 
 // ------------------------------------------------------------------------------------------------ the plan
 constexpr int PLAN_THREADS = 1024;
 constexpr int LEAST_WORK = 2;  // tile steps worth a CTA
+constexpr int UNIT_WORK = 4;   // what a unit costs beside its steps (queries, first pages, its piece), in tile steps
+
+__device__ __forceinline__ int unit_work(const Set& s) { return UNIT_WORK + (s.steps << s.both); }
 
 struct Sum2 {
   int work, units;
@@ -184,8 +191,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
     const int tiles = (set.queries + S::QUERIES - 1) / S::QUERIES;
     set.both = S::TILES == 2 && set.queries > 128;
     set.units = is ? p.kv_heads * tiles : 0;
-    set.steps = is && set.end > set.first ? (set.end - set.first + S::N - 1) / S::N : 0;
-    const int work = set.units * set.steps * (1 + set.both);
+    const int first = set.first & -S::N;  // steps begin at multiples of N
+    set.steps = is && set.end > set.first ? (set.end - first + S::N - 1) / S::N : 0;
+    const int work = set.steps ? set.units * unit_work(set) : 0;
     int at, flag_total;
     int2 total;
     const Sum2 x = plan_scan(work, work > 0, set.units, sums, flags, at, total, flag_total);
@@ -234,8 +242,10 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
   __syncthreads();
   const int total = before.x, ctas = max(1, min(p.grid, total / LEAST_WORK));
   if (tid == 0) *p.plan = {total, ctas, sets, 0};
-  for (int c = tid; c < ctas; c += PLAN_THREADS) {
+  for (int c = tid; c <= ctas; c += PLAN_THREADS) {
     const int at = range_start(c, ctas, total);
+    p.cta_start[c] = at;
+    if (c == ctas) break;
     int lo = 0;
     for (int hi = sets; hi - lo > 1;) {
       const int mid = (lo + hi) >> 1;
@@ -246,327 +256,420 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
 }
 
 // ------------------------------------------------------------------------------------------------ the walk
-// A CTA's part of a unit: steps [lo, hi).
-struct Segment {
-  Set set;
-  int unit, lo, hi;
-  int head, tile;  // KV head, and number of the unit among the set's query tiles
+// A CTA's part of a unit: steps [lo, hi) of its set's; 0 steps: no more.
+struct __align__(16) Segment {
+  int32_t first, end, kv;       // entry of the first step; the set's last entry, and its length (-1: a prefix)
+  int32_t row0, queries, both;  // of the set
+  int32_t lo, hi, head, tile;   // KV head, and number of the unit among the set's query tiles
+  float* piece;
 };
 
-// The steps of [from, to) of the work of a unit that begins at `start`: a step of work 2 belongs to where its first half lies.
+// The steps before `at` of the work of a unit that begins at `start`: a step of work 2 belongs to where its first half lies.
 __device__ __forceinline__ int step_of(int at, int start, int both, int steps) {
-  const int x = max(at - start, 0);
+  const int x = max(at - start - UNIT_WORK, 0);
   return min(both ? (x + 1) >> 1 : x, steps);
 }
 
-struct Walker {
-  const Set* sets;
-  int at, last, next_set, count;
-  Set set;
-
-  __device__ __forceinline__ Walker(const SharedParams& p, const Plan& plan) {
-    const int c = blockIdx.x;
-    sets = p.sets;
-    count = plan.sets;
-    at = last = 0;
-    if (c < plan.ctas && plan.total > 0) {
-      at = range_start(c, plan.ctas, plan.total);
-      last = range_start(c + 1, plan.ctas, plan.total);
-      next_set = p.cta_set[c];
-      load();
-    }
-  }
-  __device__ __forceinline__ void load() {
-    const int4* from = reinterpret_cast<const int4*>(sets + next_set);
-    const int4 a = from[0], b = from[1], c = from[2];
-    set = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
-    ++next_set;
-  }
-  __device__ __forceinline__ bool next(Segment& s, int kv_heads) {
-    while (at < last) {
-      const int work = set.steps << set.both, unit = (at - set.start) / work, start = set.start + unit * work;
-      const int to = min(last, start + work);
-      s.lo = step_of(at, start, set.both, set.steps), s.hi = step_of(to, start, set.both, set.steps);
-      s.set = set;
-      s.unit = unit;
-      s.tile = unit / kv_heads;
-      s.head = unit - s.tile * kv_heads;
-      at = to;
-      if (at < last && unit + 1 == set.units && to == start + work && next_set < count) load();
-      if (s.hi > s.lo) return true;
-    }
-    return false;
-  }
-};
-
-// The next bit of a counter of uses of a barrier with `N` phases in turn.
-struct Turn {
-  uint32_t used = 0;
-  __device__ __forceinline__ int slot(int n) const { return n == 1 ? 0 : int(used) & (n - 1); }
-  __device__ __forceinline__ uint32_t parity(int n) const { return (n == 1 ? used : used >> 1) & 1; }  // n is 1 or 2
-};
-
-constexpr uint64_t GIVE_UP_NS = 500000000;
-
-struct SharedBars {
-  uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], done;
-};
-
-// The next step's rows of K or V, by one warp: fetched STAGES - 1 steps ahead, expanded into the operand tile.
-template <int D, bool V>
-__device__ __forceinline__ bool bring(const SharedParams& p, const Plan& plan, SharedBars* bars, uint8_t* ring, uint32_t tiles, int w, uint32_t* masks, uint32_t* nans) {
-  using S = SharedShape<D>;
-  constexpr int R = S::ROWS, LANES = 32 / R;       // lanes that expand a row
-  constexpr int CODES = D / 32;                    // 16-byte pieces of a row's codes
-  constexpr int BUF = V ? S::VBUF : S::KBUF;
-  constexpr int SCALES = D / 16;
-  const int lane = threadIdx.x & 31, row = lane % R;  // whose address this lane finds
-  const uint32_t ring_at = gvr::smem_u32(ring);
-  // ---- fetching
-  Walker ahead(p, plan);
-  Segment f;
-  bool more = ahead.next(f, p.kv_heads);
-  int step = more ? f.lo : 0;
-  const int32_t* table = p.table + (more ? f.set.request : 0) * p.table_stride;
-  auto entry = [&]() { return f.set.first + step * S::N + w * R + row; };
-  auto load_page = [&]() { const int e = entry(); return more && e < f.set.end ? table[e >> p.page_shift] : -1; };
-  int page = load_page();
-  uint32_t there_of[S::STAGES] = {};
-  auto fetch = [&](int stage) -> uint32_t {
-    uint32_t there = 0;
-    if (more) {
-      const bool is = uint32_t(page) < uint32_t(p.num_pages);
-      there = __ballot_sync(0xffffffffu, is);
-      uint32_t from = is ? row_unit(page, entry(), p.page_shift, p.page_units, p.entry_units, uint32_t(f.head) * p.row_units) : 0;
-      if (there) {  // a missing entry is fetched from where another lies, and left out
-        const uint32_t some = __shfl_sync(0xffffffffu, from, __ffs(there) - 1);
-        if (!is) from = some;
-        const uint32_t to = ring_at + stage * (R * S::PITCH);
-#pragma unroll
-        for (int j = 0; j < R * CODES / 32; ++j) {
-          const int r = j * (32 / CODES) + lane / CODES;
-          const uint32_t of = __shfl_sync(0xffffffffu, from, r);
-          copy16(to + r * S::PITCH + lane % CODES * 16, p.data + uint64_t(of) * p.unit + (V ? D / 2 : 0) + lane % CODES * 16);
-        }
-        if (lane < R) {
-          const uint8_t* scales = p.data + uint64_t(from) * p.unit + D + (V ? SCALES : 0);
-          const uint32_t scales_to = to + lane * S::PITCH + D / 2;
-          if (SCALES == 16) copy16(scales_to, scales);
-          else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(scales_to), "l"(scales), "n"(SCALES == 8 ? 8 : 4) : "memory");
-        }
-      }
-      if (++step == f.hi) {
-        more = ahead.next(f, p.kv_heads);
-        if (more) step = f.lo, table = p.table + f.set.request * p.table_stride;
-      }
-      page = load_page();
-    }
-    copy_commit();
-    return there;
-  };
-#pragma unroll
-  for (int i = 0; i < S::STAGES - 1; ++i) there_of[i] = fetch(i);
-
-  // ---- expanding
-  Walker walk(p, plan);
-  Segment s;
-  Turn turn;
-  int stage = 0;
-  uint32_t count = 0;  // steps so far
-  uint32_t segments[2] = {0, 0};  // so far with work for each tile
-  const int r_own = R == 32 ? lane : lane / LANES, part = R == 32 ? 0 : lane % LANES;  // its row, and which part of it
-  const int tile_row = w * R + r_own;
-  bool ok = true;
-  while (ok && walk.next(s, p.kv_heads)) {
-    const bool one = s.hi - s.lo == 1 && !s.set.both;  // only one tile has work, the first
-    const int sure = s.set.kv < 0 ? s.set.end : decode_entries(s.set.kv, p.next_n, 0, p.ratio, p.capacity);
-    for (int i = s.lo; i < s.hi; ++i, ++count) {
-      copy_wait<S::STAGES - 2>();
-      __syncwarp();
-      there_of[S::STAGES - 1] = fetch(stage == 0 ? S::STAGES - 1 : stage - 1);
-      const uint32_t there = there_of[0];
-#pragma unroll
-      for (int j = 0; j < S::STAGES - 1; ++j) there_of[j] = there_of[j + 1];
-      const uint8_t* raw = ring + stage * (R * S::PITCH) + r_own * S::PITCH;
-      stage = stage == S::STAGES - 1 ? 0 : stage + 1;
-      const int slot = turn.slot(BUF);
-      ok = gvr::mbar_wait_bounded(V ? &bars->v_free[slot] : &bars->k_free[slot], turn.parity(BUF) ^ 1, GIVE_UP_NS);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const bool is = there >> r_own & 1;
-      constexpr int VALUES = D / LANES;  // of this lane
-      uint32_t scales[VALUES / 64 > 0 ? VALUES / 64 : 1];  // four a word
-      load_words<VALUES / 64>(raw + D / 2 + part * (VALUES / 16), scales);
-      if (V) {
-        const int e = s.set.first + i * S::N + tile_row;
-        if (!is) {  // P is 0 there, and 0 x NaN is not
-#pragma unroll
-          for (int j = 0; j < VALUES / 64; ++j) scales[j] = 0;
-        } else if (s.set.first + i * S::N + S::N > sure && e >= sure) {
-          // A NaN that only some rows see: it is taken out of V, and put into those rows' results (by the block of 16 values)
-          uint32_t blocks = 0;
-#pragma unroll
-          for (int j = 0; j < VALUES / 16; ++j) {
-            const uint32_t b = scales[j / 4] >> (8 * (j % 4)) & 0xff;
-            if ((b & 0x7f) == 0x7f) blocks |= 1u << (part * (VALUES / 16) + j), scales[j / 4] &= ~(0xffu << (8 * (j % 4)));
-          }
-          if (blocks)
-            for (int t = 0; t < S::TILES; ++t) {
-              if (!s.set.both && S::TILES == 2 && t != ((i - s.lo) & 1)) continue;
-              for (int r = 0; r < 128; ++r) {
-                const int m = s.tile * S::QUERIES + (s.set.both ? 128 * t : 0) + r;
-                if (m < s.set.queries && decode_entries(s.set.kv, p.next_n, m / p.group, p.ratio, p.capacity) > e)
-                  atomicOr(&nans[(segments[t] % S::NAN_SLOTS * S::TILES + t) * 128 + r], blocks);
-              }
-            }
-        }
-      }
-      const uint32_t to = tiles + slot * S::KV_BYTES + tile_row * 128;
-      uint32_t codes[4];
-#pragma unroll
-      for (int c16 = 0; c16 < VALUES / 32; ++c16) {  // 32 values: 16 bytes of codes, two blocks
-        const uint4 v = *reinterpret_cast<const uint4*>(raw + part * (VALUES / 2) + c16 * 16);
-        codes[0] = v.x, codes[1] = v.y, codes[2] = v.z, codes[3] = v.w;
-        const uint32_t two = e4m3x2_to_f16x2(scales[c16 / 2] >> (16 * (c16 % 2)));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t h[4];
-          e2m1_to_f16x2(codes[j], h);
-          const uint32_t x = splat(two, j / 2);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) h[y] = hmul2(h[y], x);
-          const int piece = part * (VALUES / 8) + c16 * 4 + j;  // of 8 values
-          const uint32_t dst = to + piece / 8 * (S::N * 128) + ((piece % 8) ^ (tile_row & 7)) * 16;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-        }
-      }
-      if (!V && lane == 0) {  // which entries are there, for those who take the scores
-        if (R == 32) masks[(count & 3) * 4 + w] = there;
-        else reinterpret_cast<uint16_t*>(masks)[(count & 3) * 8 + w] = uint16_t(there);
-      }
-      gvr::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) gvr::mbar_arrive(V ? &bars->v_full[slot] : &bars->k_full[slot]);
-      ++turn.used;
-    }
-    ++segments[0];
-    if (!one) ++segments[1];
-  }
-  copy_wait<0>();
-  return ok;
+// Waits for the phase with parity `parity` to complete, giving up after 2^30 clocks, half a second.  (In one piece, so that
+// a warp that waits counts as going the same way in all lanes, and what it computes as the same in all of them.)
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u64 t0, t1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t0, %%clock64;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t1, %%clock64;\n\t"
+      "sub.u64 t1, t1, t0;\n\t"
+      "setp.lt.u64 q, t1, 0x40000000;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(gvr::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
-// Issues the products of all of the CTA's steps; by one thread.
+constexpr int SEGMENTS = 4;  // noted ahead
+constexpr int STEP_NOTES = 4;
+
+// Uses of two buffers in turn.
+struct Turn {
+  uint32_t used = 0;
+  __device__ __forceinline__ int slot() const { return int(used & 1); }
+  __device__ __forceinline__ uint32_t parity() const { return used >> 1 & 1; }
+};
+
+struct SharedBars {
+  uint64_t raw_full[3], raw_free[3], k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint64_t seg_full[SEGMENTS], seg_free[SEGMENTS];
+};
+
+// A step, for those who expand its rows and take its scores.
+struct __align__(16) StepNote {
+  uint32_t there[4];  // which of its entries exist
+  int border;         // its first entry if some rows of its unit do not see all of it, else -1; -2: no more steps
+  int set, where;     // of a border step: its set; its query tile << 12 | tiles' numbers of segments << 8, 4 | parity in the segment
+  int pad;
+};
+
+// What the warps of a CTA tell each other beside the operands.
+struct SharedNotes {
+  Segment segments[SEGMENTS];
+  StepNote steps[STEP_NOTES];  // a step's is written once the one four before it is through with
+};
+
+__device__ __forceinline__ bool next_segment(SharedBars* bars, uint32_t count) { return bar_wait(&bars->seg_full[count % SEGMENTS], count / SEGMENTS & 1); }
+__device__ __forceinline__ void leave_segment(SharedBars* bars, uint32_t count) { gvr::mbar_arrive(&bars->seg_free[count % SEGMENTS]); }
+
+// The rows [y, ...) of a page, of one head: as many as the map's box has.
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap* map, int x, int y, int page, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to), "l"(map), "r"(x),
+               "r"(y), "r"(page), "r"(gvr::smem_u32(bar))
+               : "memory");
+}
+
+// Walks over the CTA's share: notes segments and steps, starts the copies of their rows.  By one warp; lane i finds the pages
+// of a step's i-th box (or, where pages are too small for boxes, which begin on multiples of 128 bytes, of entries i, i + 32, ...).
 template <int D>
-__device__ __forceinline__ bool multiply(const SharedParams& p, const Plan& plan, SharedBars* bars, uint32_t tmem, uint32_t q_at, uint32_t k_at, uint32_t v_at) {
+__device__ __forceinline__ bool walk(const SharedParams& p, const CUtensorMap* map, const Plan& plan, SharedNotes* notes, SharedBars* bars, uint32_t raw_at) {
   using S = SharedShape<D>;
-  constexpr uint32_t QK = product_f16(S::N, false), PV = product_f16(D, true);
-  Walker walk(p, plan);
-  Segment s;
-  Turn k_turn, v_turn;
-  uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
-  int buffer = 0;  // one tile: of S, in turn
-  while (walk.next(s, p.kv_heads)) {
-    const bool both = S::TILES == 2 && s.set.both;
-    const int tasks = (s.hi - s.lo) << (both ? 1 : 0);
-    // task i: step i (both: i / 2), tile i % 2, scores in buffer i % 2 (one tile: in turn)
-    auto scores = [&](int i) -> bool {
-      const int tile = S::TILES == 2 ? i & 1 : 0, b = S::TILES == 2 ? tile : (buffer + i) & 1;
-      if (i < S::TILES) {
-        if (!gvr::mbar_wait_bounded(&bars->q_full[tile], q_used[tile] & 1, GIVE_UP_NS)) return false;
-        ++q_used[tile];
-      }
-      const bool last = !both || tile == 1;  // that needs the step's K
-      const int slot = k_turn.slot(S::KBUF);
-      if (!both || tile == 0)
-        if (!gvr::mbar_wait_bounded(&bars->k_full[slot], k_turn.parity(S::KBUF), GIVE_UP_NS)) return false;
-      tc_fence_after();
-      const uint32_t a = q_at + tile * S::Q_BYTES, k = k_at + slot * S::KV_BYTES;
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x)
-        tc_mma(tmem + S::S_AT + b * S::N, operand_k_major(a + x / 4 * (128 * 128) + x % 4 * 32), operand_k_major(k + x / 4 * (S::N * 128) + x % 4 * 32), QK, x > 0);
-      tc_commit(&bars->s_full[b]);
-      if (last) {
-        tc_commit(&bars->k_free[slot]);
-        ++k_turn.used;
-      }
-      return true;
-    };
-    auto values = [&](int i) -> bool {
-      const int tile = S::TILES == 2 ? i & 1 : 0, b = S::TILES == 2 ? tile : (buffer + i) & 1;
-      const int slot = v_turn.slot(S::VBUF);
-      if (!both || tile == 0)
-        if (!gvr::mbar_wait_bounded(&bars->v_full[slot], v_turn.parity(S::VBUF), GIVE_UP_NS)) return false;
-      if (!gvr::mbar_wait_bounded(&bars->p_full[b], p_used[b] & 1, GIVE_UP_NS)) return false;
-      ++p_used[b];
-      tc_fence_after();
-      const uint32_t v = v_at + slot * S::KV_BYTES;
-#pragma unroll
-      for (int x = 0; x < S::N / 16; ++x)
-        tc_mma_tmem(tmem + S::O_AT + tile * D, tmem + S::S_AT + b * S::N + x * 8, operand_mn_major(v + x * (16 * 128), S::N * 128), PV, i >= S::TILES || x > 0);
-      tc_commit(&bars->o_full[b]);
-      if (!both || tile == 1) {
-        tc_commit(&bars->v_free[slot]);
-        ++v_turn.used;
-      }
-      return true;
-    };
-    if (!scores(0)) return false;
-    if (tasks > 1 && !scores(1)) return false;
-    for (int i = 0; i < tasks; ++i) {
-      if (!values(i)) return false;
-      if (i + 2 < tasks && !scores(i + 2)) return false;
-    }
-    if (S::TILES == 1) buffer = (buffer + tasks) & 1;
+  const int lane = threadIdx.x & 31;
+  const bool boxes = p.page_shift >= 3;
+  const int box_shift = min(p.page_shift, S::N == 128 ? 7 : 6), per_step = S::N >> box_shift;  // rows of a box, boxes of a step
+  int at = 0, last = 0, next_set = 0;
+  int4 a, b, c;  // the next set, on its way
+  a = b = c = make_int4(0, 0, 0, 0);
+  auto ask = [&]() {
+    const int4* from = reinterpret_cast<const int4*>(p.sets + next_set);
+    a = from[0], b = from[1], c = from[2];
+  };
+  Set set = {};
+  if (int(blockIdx.x) < plan.ctas && plan.total > 0) {
+    at = p.cta_start[blockIdx.x], last = p.cta_start[blockIdx.x + 1];
+    next_set = p.cta_set[blockIdx.x];
+    ask();
   }
-  return true;
+  bool fresh = true;
+  uint32_t steps = 0, stage = 0, turn = 0, first_only = 0;
+  for (uint32_t count = 0;; ++count) {
+    Segment s = {};
+    while (at < last) {
+      if (fresh) {
+        set = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+        if (++next_set < plan.sets) ask();
+      }
+      const int work = unit_work(set), unit = (at - set.start) / work, start = set.start + unit * work, to = min(last, start + work);
+      s.lo = step_of(at, start, set.both, set.steps), s.hi = step_of(to, start, set.both, set.steps);
+      fresh = unit + 1 == set.units && to == start + work;
+      at = to;
+      if (s.hi <= s.lo) continue;
+      s.end = set.end, s.kv = set.kv;
+      s.first = (set.first & -S::N) + s.lo * S::N;
+      s.row0 = set.row0, s.queries = set.queries, s.both = set.both;
+      s.tile = unit / p.kv_heads;
+      s.head = unit - s.tile * p.kv_heads;
+      const int64_t piece = int(blockIdx.x) + set.unit0 + unit;
+      s.piece = set.kv < 0 ? p.prefix_pieces + piece * S::PIECE : p.suffix_pieces + piece * (S::TILES * p.suffix_rows * (D + 2));
+      break;
+    }
+    const int slot = count % SEGMENTS;
+    if (!__all_sync(0xffffffffu, bar_wait(&bars->seg_free[slot], (count / SEGMENTS & 1) ^ 1))) return false;
+    if (lane == 0) {
+      notes->segments[slot] = s;
+      gvr::mbar_arrive(&bars->seg_full[slot]);
+    }
+    const int left = s.hi - s.lo;
+    const int sure = set.kv < 0 ? set.end : decode_entries(set.kv, p.next_n, 0, p.ratio, p.capacity);
+    const int where = s.tile << 12 | int((count - first_only) % S::NAN_SLOTS) << 8 | int(count % S::NAN_SLOTS) << 4;
+    first_only += left == 1 && !s.both;
+    const int32_t* table = p.table + set.request * p.table_stride;
+    const int x = s.head * (S::RB / 4);  // in words
+    auto page_of = [&](int i) {  // of this lane's box of the segment's i-th step
+      const int e = s.first + i * S::N + (lane << box_shift);
+      return boxes && lane < per_step && i < left && e < set.end ? table[e >> p.page_shift] : -1;
+    };
+    int page = page_of(0);
+    for (int i = 0; i < left || (left == 0 && i == 0); ++i) {  // without steps: the note that there are no more
+      const int next_page = page_of(i + 1);
+      if (!__all_sync(0xffffffffu, bar_wait(&bars->raw_free[stage], turn ^ 1))) return false;
+      StepNote& note = notes->steps[steps & (STEP_NOTES - 1)];
+      const int e0 = s.first + i * S::N;
+      const uint32_t to = raw_at + stage * S::RAW;
+      uint64_t* full = &bars->raw_full[stage];
+      if (lane == 0) {
+        note.border = left == 0 ? -2 : e0 + S::N > sure ? e0 : -1;
+        note.set = next_set - 1, note.where = where | (i & 1);
+      }
+      if (boxes) {
+        const bool is = uint32_t(page) < uint32_t(p.num_pages);
+        const uint32_t got = __ballot_sync(0xffffffffu, is);
+#pragma unroll
+        for (int w = 0; w < S::N / 32; ++w) {  // entry 32 w + lane
+          const int e = e0 + 32 * w + lane;
+          const uint32_t there = __ballot_sync(0xffffffffu, got >> ((32 * w + lane) >> box_shift) & 1 && e >= set.first && e < set.end);
+          if (lane == 0) note.there[w] = there;
+        }
+        if (lane == 0) gvr::mbar_arrive_expect_tx(full, uint32_t(__popc(got)) * (S::RB << box_shift));
+        __syncwarp();
+        if (is) copy_box(to + lane * (S::RB << box_shift), map, x, (e0 + (lane << box_shift)) & ((1 << p.page_shift) - 1), page, full);
+      } else {
+        int rows = 0, pages[S::N / 32];
+#pragma unroll
+        for (int w = 0; w < S::N / 32; ++w) {
+          const int e = e0 + 32 * w + lane;
+          pages[w] = left > 0 && e >= set.first && e < set.end ? table[e >> p.page_shift] : -1;
+          const uint32_t there = __ballot_sync(0xffffffffu, uint32_t(pages[w]) < uint32_t(p.num_pages));
+          if (lane == 0) note.there[w] = there;
+          rows += __popc(there);
+        }
+        if (lane == 0) gvr::mbar_arrive_expect_tx(full, rows * S::RB);
+        __syncwarp();
+#pragma unroll
+        for (int w = 0; w < S::N / 32; ++w)
+          if (uint32_t(pages[w]) < uint32_t(p.num_pages)) {
+            const uint32_t of = row_unit(pages[w], e0 + 32 * w + lane, p.page_shift, p.page_units, p.entry_units, uint32_t(s.head) * p.row_units);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to + (32 * w + lane) * S::RB),
+                         "l"(p.data + uint64_t(of) * p.unit), "r"(S::RB), "r"(gvr::smem_u32(full))
+                         : "memory");
+          }
+      }
+      page = next_page;
+      ++steps;
+      if (++stage == S::STAGES) stage = 0, turn ^= 1;
+    }
+    if (left == 0) return true;
+  }
+}
+
+// A NaN that only some rows of a unit see is taken out of V, and put into those rows' results: `blocks` of 16 values of
+// entry e, which the rows whose limit lies behind it note.
+template <int D>
+__device__ __noinline__ void note_nan(const Set* set, int next_n, int group, int ratio, int capacity, int where, int e, uint32_t blocks, uint32_t* nans) {
+  using S = SharedShape<D>;
+  const Set of = *set;
+  for (int t = 0; t < S::TILES; ++t) {
+    if (!of.both && S::TILES == 2 && t != (where & 1)) continue;
+    const int slot = where >> (t ? 8 : 4) & 15;
+    for (int x = 0; x < 128; ++x) {
+      const int m = (where >> 12) * S::QUERIES + (of.both ? 128 * t : 0) + x;
+      const int seen = of.kv < 0 ? of.end : decode_entries(of.kv, next_n, m / group, ratio, capacity);
+      if (m < of.queries && seen > e) atomicOr(&nans[(slot * S::TILES + t) * 128 + x], blocks);
+    }
+  }
+}
+
+// Expands K or V, a quarter of each step's rows a warp.  A lane has a row (head_dim 256: half of one); 16-byte reads and
+// stores of eight lanes fall on different banks.
+template <int D>
+__device__ __forceinline__ bool bring(const SharedParams& p, SharedBars* bars, const uint8_t* raw, uint32_t tiles, int w, bool is_v, const SharedNotes* notes, uint32_t* nans) {
+  using S = SharedShape<D>;
+  constexpr int R = S::ROWS, LANES = 32 / R, VALUES = D / LANES;  // of a lane
+  const int lane = threadIdx.x & 31, part = R == 32 ? 0 : lane & 1;
+  const int row = w * R + (R == 32 ? lane : lane >> 1), half = w / 2;  // V's one buffer goes by halves
+  const uint8_t* from = raw + row * S::RB + (is_v ? D / 2 : 0) + part * (VALUES / 2);
+  const uint8_t* scales_from = raw + row * S::RB + D + (is_v ? D / 16 : 0) + part * (VALUES / 16);
+  const uint32_t to = tiles + row * 128 + part * (VALUES / 64) * (S::N * 128) + ((row & 7) << 4);
+  uint32_t stage = 0, turn = 0;
+  for (uint32_t step = 0;; ++step) {
+    if (!__all_sync(0xffffffffu, bar_wait(&bars->raw_full[stage], turn))) return false;
+    const StepNote& note = notes->steps[step & (STEP_NOTES - 1)];
+    const int border = note.border;
+    if (border == -2) return true;
+    uint32_t scales[VALUES / 64];  // four a word
+    load_words<VALUES / 64>(scales_from + stage * S::RAW, scales);
+    if (!(note.there[row / 32] >> (row % 32) & 1)) {
+#pragma unroll
+      for (int j = 0; j < VALUES / 64; ++j) scales[j] = 0;  // P is 0 there, and 0 x NaN is not
+    } else if (is_v && border >= 0) {
+      uint32_t blocks = 0;
+#pragma unroll
+      for (int j = 0; j < VALUES / 16; ++j)
+        if ((scales[j / 4] >> (8 * (j % 4)) & 0x7f) == 0x7f) blocks |= 1u << (part * (VALUES / 16) + j), scales[j / 4] &= ~(0xffu << (8 * (j % 4)));
+      if (blocks) note_nan<D>(p.sets + note.set, p.next_n, p.group, p.ratio, p.capacity, note.where, border + row, blocks, nans);
+    }
+    const int slot = is_v ? 0 : int(step & 1);
+    if (!__all_sync(0xffffffffu, bar_wait(is_v ? &bars->v_free[half] : &bars->k_free[slot], (is_v ? step & 1 : step >> 1 & 1) ^ 1))) return false;
+    const uint8_t* at = from + stage * S::RAW;
+    uint32_t dst = to + slot * S::KV_BYTES;
+#pragma unroll 1
+    for (int x = 0; x < VALUES / 32; x += 2) {  // 64 values, a panel: 32 bytes of codes, four scales
+      const uint4 v0 = *reinterpret_cast<const uint4*>(at + x * 16), v1 = *reinterpret_cast<const uint4*>(at + x * 16 + 16);
+      const uint32_t codes[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+      const uint32_t four = VALUES == 64 || x == 0 ? scales[0] : scales[VALUES / 64 - 1];
+      const uint32_t two[2] = {e4m3x2_to_f16x2(four), e4m3x2_to_f16x2(four >> 16)};
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        uint32_t h[4];
+        e2m1_to_f16x2(codes[y], h);
+        const uint32_t f = splat(two[y / 4], y / 2 & 1);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) h[z] = hmul2(h[z], f);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ (y << 4)), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+      }
+      dst += S::N * 128;
+    }
+    gvr::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      gvr::mbar_arrive(is_v ? &bars->v_full[half] : &bars->k_full[slot]);
+      gvr::mbar_arrive(&bars->raw_free[stage]);
+    }
+    if (++stage == S::STAGES) stage = 0, turn ^= 1;
+  }
 }
 
 // By a whole warp, all of whose lanes go on, or give up.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, gvr::mbar_wait_bounded(bar, parity, GIVE_UP_NS));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity)); }
+
+// Issues the products of all of the CTA's steps; by one warp, of which one lane does.
+template <int D>
+__device__ __forceinline__ bool multiply(SharedBars* bars, const SharedNotes* notes, uint32_t tmem, uint32_t q_at, uint32_t k_at, uint32_t v_at) {
+  using S = SharedShape<D>;
+  constexpr uint32_t QK = product_f16(S::N, false), PV = product_f16(D, true);
+  const int lane = threadIdx.x & 31;
+  Turn k_turn;
+  uint32_t v_used = 0;
+  uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
+  int buffer = 0;  // one tile: of S, in turn
+  for (uint32_t count = 0;; ++count) {
+    if (!warp_wait(&bars->seg_full[count % SEGMENTS], count / SEGMENTS & 1)) return false;
+    const Segment& s = notes->segments[count % SEGMENTS];
+    const bool both = S::TILES == 2 && __shfl_sync(0xffffffffu, s.both, 0);
+    const int tasks = __shfl_sync(0xffffffffu, s.hi - s.lo, 0) << (both ? 1 : 0);
+    __syncwarp();
+    if (lane == 0) leave_segment(bars, count);
+    __syncwarp();
+    if (tasks == 0) return true;
+    // task i: step i (both: i / 2), tile i % 2, scores in buffer i % 2 (one tile: in turn)
+    bool ok = true;
+    auto scores = [&](int i) {
+      const int tile = S::TILES == 2 ? i & 1 : 0, b = S::TILES == 2 ? tile : (buffer + i) & 1;
+      if (i < S::TILES) {
+        ok &= bar_wait(&bars->q_full[tile], q_used[tile] & 1);
+        ++q_used[tile];
+      }
+      const bool last = !both || tile == 1;  // that needs the step's K
+      const int slot = k_turn.slot();
+      const uint64_t a = operand_k_major(q_at + tile * S::Q_BYTES), k = operand_k_major(k_at + slot * S::KV_BYTES);
+      if (!both || tile == 0) ok &= bar_wait(&bars->k_full[slot], k_turn.parity());
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          tc_mma(tmem + S::S_AT + b * S::N, a + ((x / 4 * (128 * 128) + x % 4 * 32) >> 4), k + ((x / 4 * (S::N * 128) + x % 4 * 32) >> 4), QK, x > 0);
+        tc_commit(&bars->s_full[b]);
+        if (last) tc_commit(&bars->k_free[slot]);
+      }
+      __syncwarp();
+      if (last) ++k_turn.used;
+    };
+    auto values = [&](int i) {
+      const int tile = S::TILES == 2 ? i & 1 : 0, b = S::TILES == 2 ? tile : (buffer + i) & 1;
+      const bool first = !both || tile == 0, last = !both || tile == 1;  // that needs the step's V
+      const uint64_t v = operand_mn_major(v_at, S::N * 128);
+      ok &= bar_wait(&bars->p_full[b], p_used[b] & 1);
+      ++p_used[b];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (first) ok &= bar_wait(&bars->v_full[half], v_used & 1);
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int x = half * (S::N / 32); x < (half + 1) * (S::N / 32); ++x)
+            tc_mma_tmem(tmem + S::O_AT + tile * D, tmem + S::S_AT + b * S::N + x * 8, v + ((x * (16 * 128)) >> 4), PV, i >= S::TILES || x > 0);
+          if (last) tc_commit(&bars->v_free[half]);
+          if (half == 1) tc_commit(&bars->o_full[b]);
+        }
+        __syncwarp();
+      }
+      if (last) ++v_used;
+    };
+    scores(0);
+    if (tasks > 1) scores(1);
+    for (int i = 0; i < tasks; ++i) {
+      values(i);
+      if (i + 2 < tasks) scores(i + 2);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+    }
+    if (S::TILES == 1) buffer = (buffer + tasks) & 1;
+  }
+}
+
+__device__ __forceinline__ uint64_t two_f32(uint32_t lo, uint32_t hi) { return uint64_t(lo) | uint64_t(hi) << 32; }
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t exp2_two(uint64_t x) {
+  return two_f32(__float_as_uint(exp2_fast(__uint_as_float(uint32_t(x)))), __float_as_uint(exp2_fast(__uint_as_float(uint32_t(x >> 32)))));
 }
 
 // Takes the scores of a tile, a query a thread: P, bases and sums, and at the end of each segment its piece.
 template <int D>
-__device__ __forceinline__ bool soften(const SharedParams& p, const Plan& plan, SharedBars* bars, uint32_t tmem, uint32_t q_at, int tile, const uint32_t* masks, uint32_t* nans) {
+__device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, uint32_t tmem, uint32_t q_at, int tile, SharedNotes* notes, uint32_t* nans) {
   using S = SharedShape<D>;
   constexpr int WORDS = S::N / 32;
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;  // in the tile, and lane of tensor memory
   const uint32_t lanes = uint32_t(quarter) << 21;  // 32 quarter << 16
   const uint32_t q_row_at = q_at + tile * S::Q_BYTES + row * 128;
-  Walker walk(p, plan);
-  Segment s, next;
   uint32_t s_used[2] = {0, 0}, o_used[2] = {0, 0};
   uint32_t steps = 0, segments = 0;  // K steps of the segments before, and segments with work for this tile
+  uint32_t count = 0;                // segments so far
   int buffer = 0;
 
   // Segment-wide facts of this thread's query.
   struct Query {
     float factor;
     int limit;    // entries that it sees
-    int index;    // among the set's queries; -1: none
+    int first;    // entry of the segment's first step
+    bool live;
     bool warp;    // some thread of the warp has one
-    int tasks;
+    bool both;
+    int steps;    // of the segment; 0: no more
+    int tasks;    // of them this tile's
+    int height;   // rows of the piece
+    int at;       // its place among them
+    float* piece;  // of that place
   };
-  auto begin_segment = [&](const Segment& g) -> Query {
-    Query x;
-    const bool both = S::TILES == 2 && g.set.both;
-    const int n = g.hi - g.lo;
-    x.tasks = S::TILES == 1 || both ? n : (n + 1 - tile) >> 1;
-    const int m = g.tile * S::QUERIES + (both ? 128 * tile : 0) + row;
-    bool live = m < g.set.queries;
+  auto begin_segment = [&](Query& x) -> bool {
+    if (!warp_wait(&bars->seg_full[count % SEGMENTS], count / SEGMENTS & 1)) return false;
+    const Segment g = notes->segments[count % SEGMENTS];
+    __syncwarp();
+    if (lane == 0) leave_segment(bars, count);
+    ++count;
+    x.both = S::TILES == 2 && g.both;
+    x.steps = g.hi - g.lo;
+    x.tasks = S::TILES == 1 || x.both ? x.steps : (x.steps + 1 - tile) >> 1;
+    x.first = g.first;
+    const int m = g.tile * S::QUERIES + (x.both ? 128 * tile : 0) + row;
+    bool live = m < g.queries;
     const int rel = m / p.group;
-    const int64_t at = int64_t(g.set.row0) + rel;
-    x.limit = g.set.end;
+    const int64_t at = int64_t(g.row0) + rel;
+    x.limit = g.end;
     if (live) {
-      if (g.set.kv >= 0) x.limit = decode_entries(g.set.kv, p.next_n, rel, p.ratio, p.capacity);
+      if (g.kv >= 0) x.limit = decode_entries(g.kv, p.next_n, rel, p.ratio, p.capacity);
       else live = p.joined[at / p.next_n].prefix >= 0;
     }
-    x.index = live ? m : -1;
+    x.live = live;
     x.factor = 1.f;
     x.warp = __any_sync(0xffffffffu, live);
-    if (x.tasks == 0) return x;
+    const int rows = g.kv < 0 ? 128 : p.suffix_rows;  // of a tile
+    x.height = S::TILES * rows;
+    x.at = tile * rows + row;
+    x.piece = g.piece + x.at;
+    if (x.tasks == 0) return true;
     if (x.warp) {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + at * p.q_row + int64_t(g.head * p.group + m - rel * p.group) * p.q_head);
       float mul = p.q_sign, back = 1.f;
@@ -599,88 +702,91 @@ __device__ __forceinline__ bool soften(const SharedParams& p, const Plan& plan, 
     gvr::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) gvr::mbar_arrive(&bars->q_full[tile]);
-    return x;
+    return true;
   };
 
-  bool more = walk.next(s, p.kv_heads);
   Query x, x_next;
-  if (more) x = begin_segment(s);
-  while (more) {
-    const bool both = S::TILES == 2 && s.set.both;
+  if (!begin_segment(x)) return false;
+  while (x.steps > 0) {
     float top = NO_TOP, total = 0.f;
     for (int i = 0; i < x.tasks; ++i) {
       const int b = S::TILES == 2 ? tile : (buffer + i) & 1;
       if (!warp_wait(&bars->s_full[b], s_used[b] & 1)) return false;
       ++s_used[b];
       tc_fence_after();
-      const int step = S::TILES == 1 || both ? i : 2 * i + tile;
+      const int step = S::TILES == 1 || x.both ? i : 2 * i + tile;
       if (x.warp) {
         const uint32_t scores = tmem + lanes + S::S_AT + b * S::N;
+        const uint64_t factor = two_f32(__float_as_uint(x.factor), __float_as_uint(x.factor));
         uint32_t there[WORDS];  // entries that this query sees
         bool all = true;
-        const int e0 = s.set.first + (s.lo + step) * S::N;
+        const int e0 = x.first + step * S::N;
 #pragma unroll
         for (int w = 0; w < WORDS; ++w) {
-          there[w] = reinterpret_cast<const volatile uint32_t*>(masks)[((steps + step) & 3) * 4 + w];
+          there[w] = *const_cast<const volatile uint32_t*>(&notes->steps[(steps + step) & (STEP_NOTES - 1)].there[w]);
           const int seen = x.limit - (e0 + 32 * w);
           if (seen < 32) there[w] &= seen <= 0 ? 0u : (1u << seen) - 1;
           all &= there[w] == 0xffffffffu;
         }
-        const bool whole = __all_sync(0xffffffffu, all || x.index < 0);
-        // the largest score
-        float high = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < WORDS; ++c) {
-          uint32_t v[32];
-          tmem_load(scores + 32 * c, v);
-          tmem_load_wait();
+        const bool whole = __all_sync(0xffffffffu, all || !x.live);
+        auto mask = [&](uint32_t seen, uint32_t(&s32)[32]) {
           if (!whole) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!(there[c] >> j & 1)) v[j] = 0xff800000u;
+              if (!(seen >> j & 1)) s32[j] = 0xff800000u;
           }
+        };
+        // (Loops stay loops here and in bring(): unrolled, the warps' code at a time is more than the instruction caches feed
+        // four kinds of warps from.)
+        float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < WORDS; c += 2) {
+          uint32_t v[2][32];
+          tmem_load(scores + 32 * c, v[0]);
+          tmem_load(scores + 32 * c + 32, v[1]);
+          tmem_load_wait();
+          mask(c == 0 ? there[0] : there[WORDS - 2], v[0]);
+          mask(c == 0 ? there[1] : there[WORDS - 1], v[1]);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) high = fmaxf(high, __uint_as_float(v[j]));
+          for (int j = 0; j < 32; ++j) high[j & 3] = fmaxf(fmaxf(high[j & 3], __uint_as_float(v[0][j])), __uint_as_float(v[1][j]));
         }
-        high *= x.factor;
-        if (__any_sync(0xffffffffu, high > top + ABOVE)) {
-          const float base = fmaxf(top, high - BELOW), down = exp2_fast(top - base);
-          top = base, total *= down;
-          if (i > 0) {  // O so far: all products of this tile are complete, as the next one waits for this P
+        const float most = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3])) * x.factor;
+        if (__any_sync(0xffffffffu, most > top + ABOVE)) {
+          const float next_top = fmaxf(top, most - BELOW), down = exp2_fast(top - next_top);
+          top = next_top, total *= down;
+          if (i > 0) {  // O so far: all products of this tile are complete but for those that wait for this P
             const int ob = S::TILES == 2 ? tile : b ^ 1;
             if (!warp_wait(&bars->o_full[ob], (o_used[ob] - 1) & 1)) return false;
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tmem_load(tmem + lanes + S::O_AT + tile * D + 32 * c, v);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_load(tmem + lanes + S::O_AT + tile * D + 16 * c, o);
               tmem_load_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * down);
-              tmem_store(tmem + lanes + S::O_AT + tile * D + 32 * c, v);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * down);
+              tmem_store(tmem + lanes + S::O_AT + tile * D + 16 * c, o);
             }
           }
         }
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+        const uint64_t base = two_f32(__float_as_uint(-top), __float_as_uint(-top));
+        uint64_t part[2] = {0, 0};
+#pragma unroll 1
         for (int c = 0; c < WORDS; ++c) {
           uint32_t v[32], h[16];
           tmem_load(scores + 32 * c, v);
           tmem_load_wait();
-          if (!whole) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(there[c] >> j & 1)) v[j] = 0xff800000u;
-          }
+          if (!whole) mask(c == 0 ? there[0] : c == 1 ? there[1] : c == 2 ? there[WORDS - 2] : there[WORDS - 1], v);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float e0 = exp2_fast(fmaf(__uint_as_float(v[2 * j]), x.factor, -top)), e1 = exp2_fast(fmaf(__uint_as_float(v[2 * j + 1]), x.factor, -top));
-            part[2 * j & 3] += e0, part[(2 * j + 1) & 3] += e1;
-            h[j] = pack_f16(e0, e1);
+            const uint64_t e = exp2_two(fma_two(two_f32(v[2 * j], v[2 * j + 1]), factor, base));
+            part[j & 1] = add_two(part[j & 1], e);
+            h[j] = pack_f16(__uint_as_float(uint32_t(e)), __uint_as_float(uint32_t(e >> 32)));
           }
           tmem_store(scores + 16 * c, h);  // over scores that have been read
         }
-        total += (part[0] + part[1]) + (part[2] + part[3]);
+        const uint64_t sum = add_two(part[0], part[1]);
+        total += __uint_as_float(uint32_t(sum)) + __uint_as_float(uint32_t(sum >> 32));
         tmem_store_wait();
         tc_fence_before();
       }
@@ -689,19 +795,11 @@ __device__ __forceinline__ bool soften(const SharedParams& p, const Plan& plan, 
       ++o_used[b];
     }
     if (S::TILES == 1) buffer = (buffer + x.tasks) & 1;
-    steps += s.hi - s.lo;
-
-    more = walk.next(next, p.kv_heads);
-    if (more) x_next = begin_segment(next);  // its Q may be laid down: this segment's products with Q are complete
+    steps += x.steps;
+    if (!begin_segment(x_next)) return false;  // its Q may be laid down: this segment's products with Q are complete
 
     // ---- the piece
     if (x.warp) {
-      const bool prefix = s.set.kv < 0;
-      const int rows = prefix ? 128 : p.suffix_rows;  // of a tile
-      const int64_t floats = prefix ? S::PIECE : S::TILES * rows * (D + 2);
-      float* piece = (prefix ? p.prefix_pieces : p.suffix_pieces) + int64_t(int(blockIdx.x) + s.set.unit0 + s.unit) * floats;
-      const int at = tile * rows + row, height = S::TILES * rows;
-      float* sums = piece + int64_t(height) * D;
       uint32_t nan = 0;
       if (x.tasks > 0) {
         const int ob = S::TILES == 2 ? tile : buffer ^ 1;
@@ -711,9 +809,10 @@ __device__ __forceinline__ bool soften(const SharedParams& p, const Plan& plan, 
         nan = *reinterpret_cast<volatile uint32_t*>(mine);
         if (nan) *mine = 0;
       }
-      if (x.index >= 0) sums[at] = top, sums[height + at] = total;
+      if (x.live) x.piece[int64_t(x.height) * D] = top, x.piece[int64_t(x.height) * (D + 1)] = total;
       if (x.tasks > 0) {
-#pragma unroll
+        // four values of a query lie together, those of neighbouring queries next to each other
+        float* to = x.piece + 3 * x.at;
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           tmem_load(tmem + lanes + S::O_AT + tile * D + 32 * c, v);
@@ -723,44 +822,52 @@ __device__ __forceinline__ bool soften(const SharedParams& p, const Plan& plan, 
             for (int j = 0; j < 32; ++j)
               if (nan >> (2 * c + j / 16) & 1) v[j] = 0x7fc00000u;
           }
-          if (x.index >= 0) {
+          if (x.live) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(piece + (int64_t(8 * c + j) * height + at) * 4) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+              *reinterpret_cast<uint4*>(to + int64_t(8 * c + j) * x.height * 4) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
         }
         tc_fence_before();
       }
     }
     if (x.tasks > 0) ++segments;
-    s = next, x = x_next;
+    x = x_next;
   }
   return true;
 }
 
+template <int REGS, bool MORE>
+__device__ __forceinline__ void registers() {
+  if (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 template <int D>
-__global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(SharedParams p) {
+__global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(SharedParams p, const __grid_constant__ CUtensorMap map) {
   using S = SharedShape<D>;
   extern __shared__ uint8_t dynamic[];
   __shared__ SharedBars bars;
-  __shared__ uint32_t tmem_at, masks[4 * 4], nans[S::NAN_SLOTS * S::TILES * 128];
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ SharedNotes notes;
+  __shared__ uint32_t tmem_at, nans[S::NAN_SLOTS * S::TILES * 128];
+  const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  uint8_t* base = dynamic + ((1024 - (gvr::smem_u32(dynamic) & 1023)) & 1023);
-  const uint32_t q_at = gvr::smem_u32(base), k_at = q_at + S::TILES * S::Q_BYTES, v_at = k_at + S::KBUF * S::KV_BYTES;
-  uint8_t* rings = base + S::TILES * S::Q_BYTES + (S::KBUF + S::VBUF) * S::KV_BYTES;
+  const uint32_t q_at = (gvr::smem_u32(dynamic) + 1023) & ~1023u, k_at = q_at + S::TILES * S::Q_BYTES, v_at = k_at + 2 * S::KV_BYTES, raw_at = v_at + S::KV_BYTES;
+  const uint8_t* raw = dynamic + (raw_at - gvr::smem_u32(dynamic));
   if (tid == 0) {
+    for (int i = 0; i < 3; ++i) gvr::mbar_init(&bars.raw_full[i], 1), gvr::mbar_init(&bars.raw_free[i], 8);
     for (int i = 0; i < 2; ++i) {
       gvr::mbar_init(&bars.k_full[i], 4), gvr::mbar_init(&bars.k_free[i], 1);
-      gvr::mbar_init(&bars.v_full[i], 4), gvr::mbar_init(&bars.v_free[i], 1);
+      gvr::mbar_init(&bars.v_full[i], 2), gvr::mbar_init(&bars.v_free[i], 1);
       gvr::mbar_init(&bars.q_full[i], 4), gvr::mbar_init(&bars.s_full[i], 1);
       gvr::mbar_init(&bars.p_full[i], 4), gvr::mbar_init(&bars.o_full[i], 1);
     }
     gvr::mbar_init(&bars.done, 1);
+    for (int i = 0; i < SEGMENTS; ++i) gvr::mbar_init(&bars.seg_full[i], 1), gvr::mbar_init(&bars.seg_free[i], 4 * S::TILES + 1);
     gvr::mbar_init_fence();
   }
   for (int i = tid; i < S::NAN_SLOTS * S::TILES * 128; i += S::THREADS) nans[i] = 0;
-  constexpr int FIRST_K = 4 * S::TILES, FIRST_V = FIRST_K + 4, ISSUER = FIRST_V + 4;
+  constexpr int BRINGERS = 4 * S::TILES, ISSUER = BRINGERS + 8, WALKER = ISSUER + 1;
   if (warp == ISSUER) tmem_alloc_all(gvr::smem_u32(&tmem_at));
   tc_fence_before();
   __syncthreads();
@@ -769,21 +876,26 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
   begin();
   const int4 held = *reinterpret_cast<const int4*>(p.plan);
   const Plan plan = {held.x, held.y, held.z, held.w};
+  constexpr bool EXCHANGE = S::TILES == 2;
   bool ok;
-  if (warp < FIRST_K) {
-    ok = soften<D>(p, plan, &bars, tmem, q_at, warp / 4, masks, nans);
-  } else if (warp < FIRST_V) {
-    ok = bring<D, false>(p, plan, &bars, rings + (warp - FIRST_K) * S::RING, k_at, warp - FIRST_K, masks, nans);
+  if (warp < BRINGERS) {
+    if (EXCHANGE) registers<S::SOFT_REGS, true>();
+    ok = soften<D>(p, &bars, tmem, q_at, warp / 4, &notes, nans);
   } else if (warp < ISSUER) {
-    ok = bring<D, true>(p, plan, &bars, rings + (warp - FIRST_K) * S::RING, v_at, warp - FIRST_V, masks, nans);
+    if (EXCHANGE) registers<S::BRING_REGS, false>();
+    const bool is_v = warp >= BRINGERS + 4;
+    ok = bring<D>(p, &bars, raw, is_v ? v_at : k_at, (warp - BRINGERS) & 3, is_v, &notes, nans);
   } else {
+    if (EXCHANGE) registers<S::REST_REGS, false>();
     ok = true;
-    if (lane == 0) {
-      ok = multiply<D>(p, plan, &bars, tmem, q_at, k_at, v_at);
-      tc_commit(&bars.done);  // whatever has been issued is complete before its memory is given up
-      ok &= gvr::mbar_wait_bounded(&bars.done, 0, GIVE_UP_NS);
+    if (warp == ISSUER) {
+      ok = multiply<D>(&bars, &notes, __shfl_sync(0xffffffffu, tmem, 0), q_at, k_at, v_at);
+      if (elect_one()) tc_commit(&bars.done);  // whatever has been issued is complete before its memory is given up
+      __syncwarp();
+      ok &= warp_wait(&bars.done, 0);
+    } else if (warp == WALKER) {
+      ok = walk<D>(p, &map, plan, &notes, &bars, raw_at);
     }
-    __syncwarp();
   }
   if (!ok) p.plan->failed = 1;
   tc_fence_before();
@@ -794,6 +906,8 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
 
 // ------------------------------------------------------------------------------------------------ the join
 constexpr int JOIN_SHARED_THREADS = 128;
+constexpr int JOIN_WAYS = 4;    // lanes that take every fourth piece of the same values
+constexpr int JOIN_AT_ONCE = 4;  // pieces under way
 
 // Sums of one query at four neighbouring dimensions.
 struct Joining {
@@ -807,36 +921,48 @@ struct Joining {
   }
 };
 
-// All pieces of query m of a set's KV head.
+// Every JOIN_WAYS-th piece of query m of a set's KV head.
 template <int D>
-__device__ __forceinline__ void join_set(const SharedParams& p, const Plan& plan, int which, int head, int m, int d4, Joining& j) {
+__device__ __forceinline__ void join_set(const SharedParams& p, const Plan& plan, int which, int head, int m, int d4, int way, Joining& j) {
   using S = SharedShape<D>;
   const int4* from = reinterpret_cast<const int4*>(p.sets + which);
   const int4 a = from[0], b = from[1], c = from[2];
   const Set set = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
   const bool prefix = set.kv < 0;
   const int tile = m / S::QUERIES, in = m - tile * S::QUERIES, unit = tile * p.kv_heads + head;
-  const int work = set.steps << set.both, start = set.start + unit * work;
+  const int work = unit_work(set), start = set.start + unit * work;
   // the last CTA whose share begins at or before x is ((x + 1) ctas - 1) / total
   const int c0 = int((int64_t(start + 1) * plan.ctas - 1) / plan.total), c1 = int((int64_t(start + work) * plan.ctas - 1) / plan.total);
   const int rows = prefix ? 128 : p.suffix_rows, height = S::TILES * rows;
   const int64_t floats = prefix ? S::PIECE : height * (D + 2);
-  const float* pieces = (prefix ? p.prefix_pieces : p.suffix_pieces) + int64_t(set.unit0 + unit) * floats;
   const int at = set.both ? in / 128 * rows + in % 128 : in;
+  const float* pieces = (prefix ? p.prefix_pieces : p.suffix_pieces) + int64_t(set.unit0 + unit) * floats;
   const bool twice = S::TILES == 2 && !set.both;  // even steps in one tile, odd ones in the other
-  for (int x = c0; x <= c1; ++x) {
-    const int lo = step_of(range_start(x, plan.ctas, plan.total), start, set.both, set.steps);
-    const int hi = step_of(range_start(x + 1, plan.ctas, plan.total), start, set.both, set.steps);
-    if (hi <= lo) continue;
-    const float* piece = pieces + int64_t(x) * floats;
-    const float* sums = piece + int64_t(height) * D;
-    j.add(sums[at], sums[height + at], *reinterpret_cast<const float4*>(piece + (int64_t(d4) * height + at) * 4));
-    if (twice && hi - lo > 1)
-      j.add(sums[rows + at], sums[height + rows + at], *reinterpret_cast<const float4*>(piece + (int64_t(d4) * height + rows + at) * 4));
+  const int per = twice ? 2 : 1, count = (c1 - c0 + 1) * per;
+  for (int x0 = way; x0 < count; x0 += JOIN_WAYS * JOIN_AT_ONCE) {
+    float t[JOIN_AT_ONCE], s[JOIN_AT_ONCE];
+    float4 v[JOIN_AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < JOIN_AT_ONCE; ++i) {
+      const int x = x0 + i * JOIN_WAYS, cta = c0 + (twice ? x >> 1 : x), second = twice ? x & 1 : 0;
+      s[i] = 0.f;
+      if (x < count) {
+        const int lo = step_of(p.cta_start[cta], start, set.both, set.steps), hi = step_of(p.cta_start[cta + 1], start, set.both, set.steps);
+        if (hi - lo > second) {
+          const float* piece = pieces + int64_t(cta) * floats;
+          const int row = at + second * rows;
+          t[i] = piece[int64_t(height) * D + row], s[i] = piece[int64_t(height) * (D + 1) + row];
+          v[i] = *reinterpret_cast<const float4*>(piece + (int64_t(d4) * height + row) * 4);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < JOIN_AT_ONCE; ++i) j.add(t[i], s[i], v[i]);
   }
 }
 
-// blockIdx.x: requests x KV heads; y: parts of the request's queries x dimensions, four dimensions a thread.
+// blockIdx.x: requests x KV heads; y: parts of the request's queries x dimensions.  JOIN_WAYS neighbouring lanes have four
+// dimensions of a query, neighbouring groups of lanes neighbouring queries, as they lie in a piece.
 template <int D>
 __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(SharedParams p) {
   const int r = blockIdx.x / p.kv_heads, h = blockIdx.x - r * p.kv_heads, members = p.next_n * p.group;
@@ -845,13 +971,30 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
   const Plan plan = {held.x, held.y, held.z, held.w};
   const Joined join = p.joined[r];
   const int prefix_row0 = join.prefix >= 0 ? p.sets[join.prefix].row0 : 0;
-  for (int i = blockIdx.y * JOIN_SHARED_THREADS + threadIdx.x; i < members * (D / 4); i += gridDim.y * JOIN_SHARED_THREADS) {
+  const int way = threadIdx.x % JOIN_WAYS, items = members * (D / 4);
+  constexpr int AT_ONCE = JOIN_SHARED_THREADS / JOIN_WAYS;
+  for (int i0 = blockIdx.y * AT_ONCE; i0 < items; i0 += gridDim.y * AT_ONCE) {  // the same number of turns in all lanes
+    const int i = min(i0 + int(threadIdx.x) / JOIN_WAYS, items - 1);
     const int d4 = i / members, m = i - d4 * members, rel = m / p.group;
     const int64_t row = int64_t(r) * p.next_n + rel;
-    if (row >= p.num_rows) continue;
     Joining j;
-    if (join.prefix >= 0) join_set<D>(p, plan, join.prefix, h, int(int64_t(r) * p.next_n - prefix_row0) * p.group + m, d4, j);
-    if (join.suffix >= 0) join_set<D>(p, plan, join.suffix, h, m, d4, j);
+    if (row < p.num_rows) {
+      if (join.prefix >= 0) join_set<D>(p, plan, join.prefix, h, int(int64_t(r) * p.next_n - prefix_row0) * p.group + m, d4, way, j);
+      if (join.suffix >= 0) join_set<D>(p, plan, join.suffix, h, m, d4, way, j);
+    }
+#pragma unroll
+    for (int x = 1; x < JOIN_WAYS; x <<= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, j.top, x), next = fmaxf(j.top, other);
+      const float scale = exp2_fast(j.top - next);  // of both sides the same base: every lane ends with the same sums
+      j.top = next, j.sum *= scale;
+      j.sum += __shfl_xor_sync(0xffffffffu, j.sum, x);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        j.acc[y] *= scale;
+        j.acc[y] += __shfl_xor_sync(0xffffffffu, j.acc[y], x);
+      }
+    }
+    if (way != 0 || row >= p.num_rows) continue;
     if (plan.failed) j.sum = NAN;
     const float norm = j.sum == 0.f ? 0.f : 1.f / j.sum;
     uint32_t packed[2];

@@ -27,13 +27,12 @@ __device__ __forceinline__ void tmem_load(uint32_t tmem, uint32_t (&r)[32]) {
       : "r"(tmem)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store(uint32_t tmem, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_load(uint32_t tmem, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
-      "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(tmem)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(tmem)
       : "memory");
 }
 __device__ __forceinline__ void tmem_store(uint32_t tmem, const uint32_t (&r)[16]) {
@@ -63,6 +62,15 @@ __device__ __forceinline__ uint64_t operand_mn_major(uint32_t at, uint32_t panel
 // Kind of a product: f16 operands, fp32 accumulators, 128 rows of M, N columns; B with K across its rows or along them.
 __host__ __device__ constexpr uint32_t product_f16(int n, bool b_mn_major) {
   return 1u << 4 | (b_mn_major ? 1u << 16 : 0u) | uint32_t(n >> 3) << 17 | uint32_t(128 >> 4) << 24;
+}
+
+// True in one lane of a converged warp, always the same.  The products are issued by a whole warp's code this way: what
+// they take then lies in registers that the warp shares, where each product issued by a lone thread's code spends
+// about 100 clocks on bringing its operands there.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
 }
 
 // D (+)= A B, 16 of K; A in shared memory.  By one thread.
