@@ -12,9 +12,9 @@
 // A CTA.  One warp walks over the share: it notes the segments for the others and starts the copies of their rows, a
 // page's rows of a head (up to a step's) a bulk tensor copy.  Four warps expand K and four V (e2m1 times e4m3 is exact
 // in f16), from there into matrix operands in shared memory.  One thread issues the products
-// S = Q K^T and O += P V on the fifth-generation tensor cores, 128 queries a tile: S and O lie in tensor memory.  Four warps a
-// tile take S, a query a thread, so that maximum, base and sum need no exchange, and write P, in f16, over it; P is read
-// from there as an operand.  Two tiles take turns: while one's P is made, the other's products run.  Where a unit
+// S = Q K^T and O += P V on the fifth-generation tensor cores, 128 queries a tile: S and O lie in tensor memory.  Eight warps a
+// tile take S, two threads a query, each half of the step's entries, and write P, in f16, over it; P is read from there as an
+// operand.  Two tiles take turns: while one's P is made, the other's products run.  Where a unit
 // has up to 128 queries both tiles hold them, one taking the even steps, one the odd ones.
 #pragma once
 
@@ -86,14 +86,14 @@ struct SharedShape {
   static constexpr int ROWS = N / 4;                 // rows a warp expands in a step
   static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = N * D * 2;
   static constexpr int RB = row_bytes(D), RAW = N * RB, STAGES = 3;  // rows as they are, of the steps under way
-  static constexpr int WARPS = 4 * TILES + 12, THREADS = 32 * WARPS;  // S takers, K and V, and the issuer, the walker and two idle ones
+  static constexpr int WARPS = 8 * TILES + 12, THREADS = 32 * WARPS;  // S takers, K and V, and the issuer, the walker and two idle ones
   static constexpr int PIECE = QUERIES * (D + 2);    // floats of a prefix piece
-  static constexpr int S_AT = 0, O_AT = 2 * N;  // columns; P lies over its scores
+  static constexpr int S_AT = 0, O_AT = 2 * N;  // columns; P lies over its scores, the halves' where theirs begin
   static constexpr int NAN_SLOTS = 4;
   static constexpr int SMEM = TILES * Q_BYTES + 3 * KV_BYTES + STAGES * RAW + 1024;  // two of K, one of V; 1024 to align
-  // Registers of a thread: those who take S hold a row of it.  Their sum is what the CTA is launched with (640 threads of
-  // 96; head_dim 256: 512 of 128, which need no exchange).
-  static constexpr int SOFT_REGS = 152, BRING_REGS = 64, REST_REGS = 48;
+  // Registers of a thread: those who take S hold half a row of it.  Their sum is what the CTA is launched with (896 threads of
+  // 72; head_dim 256: 640 of 96, which need no exchange).
+  static constexpr int SOFT_REGS = 88, BRING_REGS = 56, REST_REGS = 40;
 };
 
 // ------------------------------------------------------------------------------------------------ the plan
@@ -581,7 +581,7 @@ __device__ __forceinline__ bool multiply(SharedBars* bars, const SharedNotes* no
         if (elect_one()) {
 #pragma unroll
           for (int x = half * (S::N / 32); x < (half + 1) * (S::N / 32); ++x)
-            tc_mma_tmem(tmem + S::O_AT + tile * D, tmem + S::S_AT + b * S::N + x * 8, v + ((x * (16 * 128)) >> 4), PV, i >= S::TILES || x > 0);
+            tc_mma_tmem(tmem + S::O_AT + tile * D, tmem + S::S_AT + b * S::N + x / (S::N / 32) * (S::N / 2) + x % (S::N / 32) * 8, v + ((x * (16 * 128)) >> 4), PV, i >= S::TILES || x > 0);
           if (last) tc_commit(&bars->v_free[half]);
           if (half == 1) tc_commit(&bars->o_full[b]);
         }
@@ -616,24 +616,44 @@ __device__ __forceinline__ uint64_t exp2_two(uint64_t x) {
   return two_f32(__float_as_uint(exp2_fast(__uint_as_float(uint32_t(x)))), __float_as_uint(exp2_fast(__uint_as_float(uint32_t(x >> 32)))));
 }
 
-// Takes the scores of a tile, a query a thread: P, bases and sums, and at the end of each segment its piece.
+// Meets the warp that has the other half of the same rows; true for both if `is` is for a thread of either.
+__device__ __forceinline__ bool meet(int pair, bool is) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"(pair + 1), "r"(uint32_t(is))
+               : "memory");
+  return r != 0;
+}
+
+// Takes the scores of a tile, half of a step's entries of a query a thread: P, bases and sums, and at the end of each segment
+// its piece, half of the dimensions a thread.
 template <int D>
-__device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, uint32_t tmem, uint32_t q_at, int tile, SharedNotes* notes, uint32_t* nans) {
+__device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, uint32_t tmem, uint32_t q_at, int warp, SharedNotes* notes, uint32_t* nans, float* exchange) {
   using S = SharedShape<D>;
-  constexpr int WORDS = S::N / 32;
-  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;  // in the tile, and lane of tensor memory
+  constexpr int COLUMNS = S::N / 2, WORDS = COLUMNS / 32;  // of this thread
+  const int tile = warp >> 3, half = warp >> 2 & 1, quarter = warp & 3;
+  const int lane = threadIdx.x & 31, row = quarter * 32 + lane;  // in the tile, and lane of tensor memory
+  const int pair = tile * 4 + quarter;
+  float* mine = exchange + (tile * 2 + half) * 128 + row;
+  const float* other = exchange + (tile * 2 + (half ^ 1)) * 128 + row;
   const uint32_t lanes = uint32_t(quarter) << 21;  // 32 quarter << 16
   const uint32_t q_row_at = q_at + tile * S::Q_BYTES + row * 128;
   uint32_t s_used[2] = {0, 0}, o_used[2] = {0, 0};
   uint32_t steps = 0, segments = 0;  // K steps of the segments before, and segments with work for this tile
   uint32_t count = 0;                // segments so far
   int buffer = 0;
+  // A wait that gave up: this warp goes on without waiting until it meets the other one, and both end.
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = warp_wait(bar, parity);
+  };
 
   // Segment-wide facts of this thread's query.
   struct Query {
     float factor;
     int limit;    // entries that it sees
-    int first;    // entry of the segment's first step
+    int first;    // this thread's first entry of the segment's first step
     bool live;
     bool warp;    // some thread of the warp has one
     bool both;
@@ -643,8 +663,13 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     int at;       // its place among them
     float* piece;  // of that place
   };
-  auto begin_segment = [&](Query& x) -> bool {
-    if (!warp_wait(&bars->seg_full[count % SEGMENTS], count / SEGMENTS & 1)) return false;
+  auto begin_segment = [&](Query& x) {
+    wait(&bars->seg_full[count % SEGMENTS], count / SEGMENTS & 1);
+    if (meet(pair, !ok)) {
+      ok = false;
+      x.steps = x.tasks = 0;
+      return;
+    }
     const Segment g = notes->segments[count % SEGMENTS];
     __syncwarp();
     if (lane == 0) leave_segment(bars, count);
@@ -652,7 +677,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     x.both = S::TILES == 2 && g.both;
     x.steps = g.hi - g.lo;
     x.tasks = S::TILES == 1 || x.both ? x.steps : (x.steps + 1 - tile) >> 1;
-    x.first = g.first;
+    x.first = g.first + half * COLUMNS;
     const int m = g.tile * S::QUERIES + (x.both ? 128 * tile : 0) + row;
     bool live = m < g.queries;
     const int rel = m / p.group;
@@ -669,7 +694,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     x.height = S::TILES * rows;
     x.at = tile * rows + row;
     x.piece = g.piece + x.at;
-    if (x.tasks == 0) return true;
+    if (x.tasks == 0) return;
     if (x.warp) {
       const uint4* src = reinterpret_cast<const uint4*>(p.q + at * p.q_row + int64_t(g.head * p.group + m - rel * p.group) * p.q_head);
       float mul = p.q_sign, back = 1.f;
@@ -687,8 +712,8 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
         back = __uint_as_float(uint32_t(127 - up) << 23);
       }
       const uint32_t sign = pack_f16(p.q_sign, p.q_sign);
-#pragma unroll 8
-      for (int j = 0; j < D / 8; ++j) {
+#pragma unroll 4
+      for (int j = half * (D / 16); j < (half + 1) * (D / 16); ++j) {  // half of the query's values
         const uint4 v = live ? src[j] : make_uint4(0, 0, 0, 0);
         uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -702,35 +727,35 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     gvr::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) gvr::mbar_arrive(&bars->q_full[tile]);
-    return true;
   };
 
   Query x, x_next;
-  if (!begin_segment(x)) return false;
+  begin_segment(x);
   while (x.steps > 0) {
     float top = NO_TOP, total = 0.f;
     for (int i = 0; i < x.tasks; ++i) {
       const int b = S::TILES == 2 ? tile : (buffer + i) & 1;
-      if (!warp_wait(&bars->s_full[b], s_used[b] & 1)) return false;
+      wait(&bars->s_full[b], s_used[b] & 1);
       ++s_used[b];
       tc_fence_after();
       const int step = S::TILES == 1 || x.both ? i : 2 * i + tile;
       if (x.warp) {
-        const uint32_t scores = tmem + lanes + S::S_AT + b * S::N;
+        const uint32_t scores = tmem + lanes + S::S_AT + b * S::N + half * COLUMNS;
         const uint64_t factor = two_f32(__float_as_uint(x.factor), __float_as_uint(x.factor));
         uint32_t there[WORDS];  // entries that this query sees
         bool all = true;
         const int e0 = x.first + step * S::N;
 #pragma unroll
         for (int w = 0; w < WORDS; ++w) {
-          there[w] = *const_cast<const volatile uint32_t*>(&notes->steps[(steps + step) & (STEP_NOTES - 1)].there[w]);
+          there[w] = *const_cast<const volatile uint32_t*>(&notes->steps[(steps + step) & (STEP_NOTES - 1)].there[half * WORDS + w]);
           const int seen = x.limit - (e0 + 32 * w);
           if (seen < 32) there[w] &= seen <= 0 ? 0u : (1u << seen) - 1;
           all &= there[w] == 0xffffffffu;
         }
         const bool whole = __all_sync(0xffffffffu, all || !x.live);
-        auto mask = [&](uint32_t seen, uint32_t(&s32)[32]) {
+        auto mask = [&](int c, uint32_t(&s32)[32]) {
           if (!whole) {
+            const uint32_t seen = c == 0 ? there[0] : there[WORDS - 1];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!(seen >> j & 1)) s32[j] = 0xff800000u;
@@ -740,26 +765,29 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
         // four kinds of warps from.)
         float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-        for (int c = 0; c < WORDS; c += 2) {
-          uint32_t v[2][32];
-          tmem_load(scores + 32 * c, v[0]);
-          tmem_load(scores + 32 * c + 32, v[1]);
+        for (int c = 0; c < WORDS; ++c) {
+          uint32_t v[32];
+          tmem_load(scores + 32 * c, v);
           tmem_load_wait();
-          mask(c == 0 ? there[0] : there[WORDS - 2], v[0]);
-          mask(c == 0 ? there[1] : there[WORDS - 1], v[1]);
+          mask(c, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) high[j & 3] = fmaxf(fmaxf(high[j & 3], __uint_as_float(v[0][j])), __uint_as_float(v[1][j]));
+          for (int j = 0; j < 32; j += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) high[y] = fmaxf(fmaxf(high[y], __uint_as_float(v[j + 2 * y])), __uint_as_float(v[j + 2 * y + 1]));
         }
-        const float most = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3])) * x.factor;
-        if (__any_sync(0xffffffffu, most > top + ABOVE)) {
+        float most = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3])) * x.factor;
+        if (meet(pair, most > top + ABOVE)) {
+          *mine = most;
+          meet(pair, false);
+          most = fmaxf(most, *const_cast<const volatile float*>(other));
           const float next_top = fmaxf(top, most - BELOW), down = exp2_fast(top - next_top);
           top = next_top, total *= down;
           if (i > 0) {  // O so far: all products of this tile are complete but for those that wait for this P
             const int ob = S::TILES == 2 ? tile : b ^ 1;
-            if (!warp_wait(&bars->o_full[ob], (o_used[ob] - 1) & 1)) return false;
+            wait(&bars->o_full[ob], (o_used[ob] - 1) & 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
               uint32_t o[16];
               tmem_load(tmem + lanes + S::O_AT + tile * D + 16 * c, o);
               tmem_load_wait();
@@ -776,7 +804,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
           uint32_t v[32], h[16];
           tmem_load(scores + 32 * c, v);
           tmem_load_wait();
-          if (!whole) mask(c == 0 ? there[0] : c == 1 ? there[1] : c == 2 ? there[WORDS - 2] : there[WORDS - 1], v);
+          mask(c, v);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint64_t e = exp2_two(fma_two(two_f32(v[2 * j], v[2 * j + 1]), factor, base));
@@ -796,24 +824,27 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     }
     if (S::TILES == 1) buffer = (buffer + x.tasks) & 1;
     steps += x.steps;
-    if (!begin_segment(x_next)) return false;  // its Q may be laid down: this segment's products with Q are complete
+    if (x.warp && half == 1) *mine = total;
+    begin_segment(x_next);  // meets the other warp; its Q may be laid down: this segment's products with Q are complete
 
     // ---- the piece
     if (x.warp) {
       uint32_t nan = 0;
       if (x.tasks > 0) {
         const int ob = S::TILES == 2 ? tile : buffer ^ 1;
-        if (!warp_wait(&bars->o_full[ob], (o_used[ob] - 1) & 1)) return false;
+        wait(&bars->o_full[ob], (o_used[ob] - 1) & 1);
         tc_fence_after();
-        uint32_t* mine = nans + (segments % S::NAN_SLOTS * S::TILES + tile) * 128 + row;
-        nan = *reinterpret_cast<volatile uint32_t*>(mine);
-        if (nan) *mine = 0;
+        nan = *const_cast<volatile uint32_t*>(nans + (segments % S::NAN_SLOTS * S::TILES + tile) * 128 + row);
       }
-      if (x.live) x.piece[int64_t(x.height) * D] = top, x.piece[int64_t(x.height) * (D + 1)] = total;
+      if (half == 0 && x.live) {
+        x.piece[int64_t(x.height) * D] = top;
+        x.piece[int64_t(x.height) * (D + 1)] = total + *const_cast<const volatile float*>(other);
+      }
       if (x.tasks > 0) {
         // four values of a query lie together, those of neighbouring queries next to each other
         float* to = x.piece + 3 * x.at;
-        for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+        for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
           uint32_t v[32];
           tmem_load(tmem + lanes + S::O_AT + tile * D + 32 * c, v);
           tmem_load_wait();
@@ -830,11 +861,14 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
         }
         tc_fence_before();
       }
+      // both have read them before they are used again
+      meet(pair, false);
+      if (nan && half == 0) nans[(segments % S::NAN_SLOTS * S::TILES + tile) * 128 + row] = 0;
     }
     if (x.tasks > 0) ++segments;
     x = x_next;
   }
-  return true;
+  return ok;
 }
 
 template <int REGS, bool MORE>
@@ -850,6 +884,7 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
   __shared__ SharedBars bars;
   __shared__ SharedNotes notes;
   __shared__ uint32_t tmem_at, nans[S::NAN_SLOTS * S::TILES * 128];
+  __shared__ float exchange[S::TILES * 2 * 128];  // of the two threads of a query
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t q_at = (gvr::smem_u32(dynamic) + 1023) & ~1023u, k_at = q_at + S::TILES * S::Q_BYTES, v_at = k_at + 2 * S::KV_BYTES, raw_at = v_at + S::KV_BYTES;
@@ -859,15 +894,15 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
     for (int i = 0; i < 2; ++i) {
       gvr::mbar_init(&bars.k_full[i], 4), gvr::mbar_init(&bars.k_free[i], 1);
       gvr::mbar_init(&bars.v_full[i], 2), gvr::mbar_init(&bars.v_free[i], 1);
-      gvr::mbar_init(&bars.q_full[i], 4), gvr::mbar_init(&bars.s_full[i], 1);
-      gvr::mbar_init(&bars.p_full[i], 4), gvr::mbar_init(&bars.o_full[i], 1);
+      gvr::mbar_init(&bars.q_full[i], 8), gvr::mbar_init(&bars.s_full[i], 1);
+      gvr::mbar_init(&bars.p_full[i], 8), gvr::mbar_init(&bars.o_full[i], 1);
     }
     gvr::mbar_init(&bars.done, 1);
-    for (int i = 0; i < SEGMENTS; ++i) gvr::mbar_init(&bars.seg_full[i], 1), gvr::mbar_init(&bars.seg_free[i], 4 * S::TILES + 1);
+    for (int i = 0; i < SEGMENTS; ++i) gvr::mbar_init(&bars.seg_full[i], 1), gvr::mbar_init(&bars.seg_free[i], 8 * S::TILES + 1);
     gvr::mbar_init_fence();
   }
   for (int i = tid; i < S::NAN_SLOTS * S::TILES * 128; i += S::THREADS) nans[i] = 0;
-  constexpr int BRINGERS = 4 * S::TILES, ISSUER = BRINGERS + 8, WALKER = ISSUER + 1;
+  constexpr int BRINGERS = 8 * S::TILES, ISSUER = BRINGERS + 8, WALKER = ISSUER + 1;
   if (warp == ISSUER) tmem_alloc_all(gvr::smem_u32(&tmem_at));
   tc_fence_before();
   __syncthreads();
@@ -880,7 +915,7 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
   bool ok;
   if (warp < BRINGERS) {
     if (EXCHANGE) registers<S::SOFT_REGS, true>();
-    ok = soften<D>(p, &bars, tmem, q_at, warp / 4, &notes, nans);
+    ok = soften<D>(p, &bars, tmem, q_at, warp, &notes, nans, exchange);
   } else if (warp < ISSUER) {
     if (EXCHANGE) registers<S::BRING_REGS, false>();
     const bool is_v = warp >= BRINGERS + 4;
