@@ -32,7 +32,7 @@ extern "C" {
  * A request whose rows do not all see the whole prefix, and a request alone in its group, is attended as one in no
  * group.  num_groups 0 to GVR_LONG_MAX_REQUESTS (0: the pointers may be NULL), and as many requests.
  * Result, roundings and everything else are as in attend_decode without indices; next_n times num_heads /
- * num_kv_heads is at most 2^20.
+ * num_kv_heads is at most 2^19.
  *   workspace       16-byte aligned, attend_shared_workspace's bytes.
  * Every wait inside the kernel is bounded (0.5 s): should one give up, which is not expected on a healthy GPU, all of
  * out and lse are NaN.

@@ -17,7 +17,7 @@ inline gvr_status check_rows(const gvr_cache* cache, const void* q, int64_t q_ro
   if ((dtype != GVR_BF16 && dtype != GVR_F16) || num_rows < 0 || num_heads < 1 || num_heads % cache->num_kv_heads != 0 ||
       num_heads > GVR_ATTEND_MAX_HEADS || !std::isfinite(float(double(scale) * cache->k_scale * 1.4426950408889634)) || table_width < 0 ||
       table_width > kIntMax / cache->page_size || next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N || ratio < 1 ||
-      int64_t(next_n) * (num_heads / cache->num_kv_heads) > (1 << 20) || (num_rows + next_n - 1) / next_n > GVR_LONG_MAX_REQUESTS)
+      int64_t(next_n) * (num_heads / cache->num_kv_heads) > (1 << 19) || (num_rows + next_n - 1) / next_n > GVR_LONG_MAX_REQUESTS)
     return GVR_ERR_ARG;
   if (q_row_stride < 0 || q_head_stride < 0 || q_row_stride % 8 != 0 || q_head_stride % 8 != 0 || q_row_stride > kIntMax ||
       q_head_stride > kIntMax || table_stride < table_width || table_stride > kIntMax)

@@ -82,7 +82,7 @@ gvr_status attend_shared_workspace(int32_t num_kv_heads, int32_t head_dim, int64
   if (!bytes) return GVR_ERR_NULL;
   if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || num_kv_heads < 1 || num_kv_heads > 65535 || num_rows < 0 || num_heads < 1 ||
       num_heads % num_kv_heads != 0 || num_heads > GVR_ATTEND_MAX_HEADS || next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N ||
-      int64_t(next_n) * (num_heads / num_kv_heads) > (1 << 20) || num_groups < 0 || num_groups > GVR_LONG_MAX_REQUESTS ||
+      int64_t(next_n) * (num_heads / num_kv_heads) > (1 << 19) || num_groups < 0 || num_groups > GVR_LONG_MAX_REQUESTS ||
       num_rows > int64_t(GVR_LONG_MAX_REQUESTS) * next_n)
     return GVR_ERR_ARG;
   int sms = 0;
@@ -125,10 +125,11 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   if (fits != GVR_OK) return fits;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < size_t(l.bytes)) return GVR_ERR_WORKSPACE;
   SharedDevice& d = g_shared_devices[dev];  // sm_count has checked dev
-  std::call_once(d.once, [&d]() {
+  std::call_once(d.once, [&d, sms]() {
     for (int each : {64, 128, 256}) {
       const SharedInfo& i = shared_kernels(each);
       if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(i.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, i.smem);
+      if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(i.join, cudaFuncAttributeMaxDynamicSharedMemorySize, join_smem(sms));
       if (d.err == cudaSuccess)
         d.err = cudaFuncSetAttribute(i.plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (5 * GVR_LONG_MAX_REQUESTS + 1) * 4);
     }
@@ -176,8 +177,8 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   cudaError_t e = launch(k.plan, dim3(1), PLAN_THREADS, plan_smem, 1, args, stream);
   if (e == cudaSuccess) e = launch(k.kernel, dim3(uint32_t(sms)), k.threads, k.smem, 1, args, stream);
   if (e == cudaSuccess) {
-    const int64_t at_once = JOIN_SHARED_THREADS / JOIN_WAYS, parts = (members * (dim / 4) + at_once - 1) / at_once;
-    e = launch(k.join, dim3(uint32_t(p.requests) * uint32_t(p.kv_heads), uint32_t(std::min<int64_t>(parts, 65535))), JOIN_SHARED_THREADS, 0, 1, args, stream);
+    const dim3 grid(uint32_t(p.requests) * uint32_t(p.kv_heads), uint32_t((members + JOIN_ROWS - 1) / JOIN_ROWS), uint32_t(dim / JOIN_WIDTH));
+    e = launch(k.join, grid, JOIN_SHARED_THREADS, join_smem(sms), 1, args, stream);
   }
   return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
 }

@@ -89,7 +89,7 @@ struct SharedShape {
   static constexpr int WARPS = 8 * TILES + 12, THREADS = 32 * WARPS;  // S takers, K and V, and the issuer, the walker and two idle ones
   static constexpr int PIECE = QUERIES * (D + 2);    // floats of a prefix piece
   static constexpr int S_AT = 0, O_AT = 2 * N;  // columns; P lies over its scores, the halves' where theirs begin
-  static constexpr int NAN_SLOTS = 4;
+  static constexpr int NAN_SLOTS = 2;
   static constexpr int SMEM = TILES * Q_BYTES + 3 * KV_BYTES + STAGES * RAW + 1024;  // two of K, one of V; 1024 to align
   // Registers of a thread: those who take S hold half a row of it.  Their sum is what the CTA is launched with (896 threads of
   // 72; head_dim 256: 640 of 96, which need no exchange).
@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
   __shared__ int flags[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   begin();
+  let_next_start();  // its CTAs, one an SM, set up meanwhile
   // groups begin where their start says, but not before the one before them
   int most = 0;
   for (int i0 = 0; i0 <= p.groups && p.groups > 0; i0 += PLAN_THREADS) {
@@ -280,7 +281,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
       "@p bra DONE;\n\t"
       "mov.u64 t0, %%clock64;\n\t"
       "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "@p bra DONE;\n\t"
       "mov.u64 t1, %%clock64;\n\t"
       "sub.u64 t1, t1, t0;\n\t"
@@ -289,7 +290,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(gvr::smem_u32(bar)), "r"(parity)
+      : "r"(gvr::smem_u32(bar)), "r"(parity), "r"(1000000)  // ns that a try may sleep
       : "memory");
   return ok != 0;
 }
@@ -545,55 +546,50 @@ __device__ __forceinline__ bool multiply(SharedBars* bars, const SharedNotes* no
     if (lane == 0) leave_segment(bars, count);
     __syncwarp();
     if (tasks == 0) return true;
-    // task i: step i (both: i / 2), tile i % 2, scores in buffer i % 2 (one tile: in turn)
+    // Task i: step i (both: i / 2), tile i % 2, scores in buffer i % 2 (one tile: in turn).  Behind the values of task i
+    // come the scores of task i + 2, which take the place of its P.
     bool ok = true;
-    auto scores = [&](int i) {
-      const int tile = S::TILES == 2 ? i & 1 : 0, b = S::TILES == 2 ? tile : (buffer + i) & 1;
-      if (i < S::TILES) {
-        ok &= bar_wait(&bars->q_full[tile], q_used[tile] & 1);
-        ++q_used[tile];
-      }
-      const bool last = !both || tile == 1;  // that needs the step's K
+    for (int i = -2; i < tasks; ++i) {
+      const int next = i + 2, tile = S::TILES == 2 ? i & 1 : 0, b = S::TILES == 2 ? tile : (buffer + i) & 1;
+      const bool weigh = i >= 0, score = next < tasks;
+      const bool first = !both || tile == 0, last = !both || tile == 1;  // that needs a step's K and V
       const int slot = k_turn.slot();
-      const uint64_t a = operand_k_major(q_at + tile * S::Q_BYTES), k = operand_k_major(k_at + slot * S::KV_BYTES);
-      if (!both || tile == 0) ok &= bar_wait(&bars->k_full[slot], k_turn.parity());
-      tc_fence_after();
-      if (elect_one()) {
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          tc_mma(tmem + S::S_AT + b * S::N, a + ((x / 4 * (128 * 128) + x % 4 * 32) >> 4), k + ((x / 4 * (S::N * 128) + x % 4 * 32) >> 4), QK, x > 0);
-        tc_commit(&bars->s_full[b]);
-        if (last) tc_commit(&bars->k_free[slot]);
-      }
-      __syncwarp();
-      if (last) ++k_turn.used;
-    };
-    auto values = [&](int i) {
-      const int tile = S::TILES == 2 ? i & 1 : 0, b = S::TILES == 2 ? tile : (buffer + i) & 1;
-      const bool first = !both || tile == 0, last = !both || tile == 1;  // that needs the step's V
-      const uint64_t v = operand_mn_major(v_at, S::N * 128);
-      ok &= bar_wait(&bars->p_full[b], p_used[b] & 1);
-      ++p_used[b];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (first) ok &= bar_wait(&bars->v_full[half], v_used & 1);
+      const uint64_t q = operand_k_major(q_at + tile * S::Q_BYTES), k = operand_k_major(k_at + slot * S::KV_BYTES), v = operand_mn_major(v_at, S::N * 128);
+      const uint32_t scores = tmem + S::S_AT + b * S::N, sums = tmem + S::O_AT + tile * D;
+      if (weigh) {
+        if (first) ok &= bar_wait(&bars->v_full[0], v_used & 1) & bar_wait(&bars->v_full[1], v_used & 1);
+        ok &= bar_wait(&bars->p_full[b], p_used[b] & 1);
+        ++p_used[b];
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int x = half * (S::N / 32); x < (half + 1) * (S::N / 32); ++x)
-            tc_mma_tmem(tmem + S::O_AT + tile * D, tmem + S::S_AT + b * S::N + x / (S::N / 32) * (S::N / 2) + x % (S::N / 32) * 8, v + ((x * (16 * 128)) >> 4), PV, i >= S::TILES || x > 0);
-          if (last) tc_commit(&bars->v_free[half]);
-          if (half == 1) tc_commit(&bars->o_full[b]);
+          for (int x = 0; x < S::N / 16; ++x) {
+            tc_mma_tmem(sums, scores + x / (S::N / 32) * (S::N / 2) + x % (S::N / 32) * 8, v + ((x * (16 * 128)) >> 4), PV, i >= S::TILES || x > 0);
+            if (x == S::N / 32 - 1 && last) tc_commit(&bars->v_free[0]);
+          }
+          if (last) tc_commit(&bars->v_free[1]);
+          tc_commit(&bars->o_full[b]);
         }
         __syncwarp();
       }
-      if (last) ++v_used;
-    };
-    scores(0);
-    if (tasks > 1) scores(1);
-    for (int i = 0; i < tasks; ++i) {
-      values(i);
-      if (i + 2 < tasks) scores(i + 2);
+      if (score) {
+        if (next < S::TILES) {
+          ok &= bar_wait(&bars->q_full[tile], q_used[tile] & 1);
+          ++q_used[tile];
+        }
+        if (first) ok &= bar_wait(&bars->k_full[slot], k_turn.parity());
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            tc_mma(scores, q + ((x / 4 * (128 * 128) + x % 4 * 32) >> 4), k + ((x / 4 * (S::N * 128) + x % 4 * 32) >> 4), QK, x > 0);
+          tc_commit(&bars->s_full[b]);
+          if (last) tc_commit(&bars->k_free[slot]);
+        }
+        __syncwarp();
+      }
+      if (last && weigh) ++v_used;
+      if (last && score) ++k_turn.used;
       if (!__all_sync(0xffffffffu, ok)) return false;
     }
     if (S::TILES == 1) buffer = (buffer + tasks) & 1;
@@ -614,6 +610,12 @@ __device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
 
 __device__ __forceinline__ uint64_t exp2_two(uint64_t x) {
   return two_f32(__float_as_uint(exp2_fast(__uint_as_float(uint32_t(x)))), __float_as_uint(exp2_fast(__uint_as_float(uint32_t(x >> 32)))));
+}
+
+__device__ __forceinline__ float max_three(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // Meets the warp that has the other half of the same rows; true for both if `is` is for a thread of either.
@@ -637,6 +639,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
   const int pair = tile * 4 + quarter;
   float* mine = exchange + (tile * 2 + half) * 128 + row;
   const float* other = exchange + (tile * 2 + (half ^ 1)) * 128 + row;
+  float* totals = exchange + S::TILES * 2 * 128;  // of the second halves
   const uint32_t lanes = uint32_t(quarter) << 21;  // 32 quarter << 16
   const uint32_t q_row_at = q_at + tile * S::Q_BYTES + row * 128;
   uint32_t s_used[2] = {0, 0}, o_used[2] = {0, 0};
@@ -771,9 +774,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
           tmem_load_wait();
           mask(c, v);
 #pragma unroll
-          for (int j = 0; j < 32; j += 8)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) high[y] = fmaxf(fmaxf(high[y], __uint_as_float(v[j + 2 * y])), __uint_as_float(v[j + 2 * y + 1]));
+          for (int j = 0; j < 32; j += 2) high[j / 2 & 3] = max_three(high[j / 2 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
         }
         float most = fmaxf(fmaxf(high[0], high[1]), fmaxf(high[2], high[3])) * x.factor;
         if (meet(pair, most > top + ABOVE)) {
@@ -824,7 +825,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     }
     if (S::TILES == 1) buffer = (buffer + x.tasks) & 1;
     steps += x.steps;
-    if (x.warp && half == 1) *mine = total;
+    if (x.warp && half == 1) totals[tile * 128 + row] = total;
     begin_segment(x_next);  // meets the other warp; its Q may be laid down: this segment's products with Q are complete
 
     // ---- the piece
@@ -838,7 +839,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
       }
       if (half == 0 && x.live) {
         x.piece[int64_t(x.height) * D] = top;
-        x.piece[int64_t(x.height) * (D + 1)] = total + *const_cast<const volatile float*>(other);
+        x.piece[int64_t(x.height) * (D + 1)] = total + *const_cast<const volatile float*>(totals + tile * 128 + row);
       }
       if (x.tasks > 0) {
         // four values of a query lie together, those of neighbouring queries next to each other
@@ -884,7 +885,7 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
   __shared__ SharedBars bars;
   __shared__ SharedNotes notes;
   __shared__ uint32_t tmem_at, nans[S::NAN_SLOTS * S::TILES * 128];
-  __shared__ float exchange[S::TILES * 2 * 128];  // of the two threads of a query
+  __shared__ float exchange[S::TILES * 3 * 128];  // of the two threads of a query: maxima, sums
   const int tid = threadIdx.x;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t q_at = (gvr::smem_u32(dynamic) + 1023) & ~1023u, k_at = q_at + S::TILES * S::Q_BYTES, v_at = k_at + 2 * S::KV_BYTES, raw_at = v_at + S::KV_BYTES;
@@ -940,109 +941,133 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
 }
 
 // ------------------------------------------------------------------------------------------------ the join
-constexpr int JOIN_SHARED_THREADS = 128;
-constexpr int JOIN_WAYS = 4;    // lanes that take every fourth piece of the same values
-constexpr int JOIN_AT_ONCE = 4;  // pieces under way
+constexpr int JOIN_ROWS = 16, JOIN_SHARED_THREADS = 256;         // queries and threads of a CTA
+constexpr int JOIN_WIDTH = JOIN_SHARED_THREADS / JOIN_ROWS * 4;  // its dimensions
+constexpr int JOIN_AT_ONCE = 8;                                  // pieces under way
 
-// Sums of one query at four neighbouring dimensions.
-struct Joining {
-  float top = NO_TOP, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-
-  __device__ __forceinline__ void add(float t, float s, const float4& v) {
-    if (s == 0.f) return;  // saw nothing there (and what it holds may be a NaN of entries that it does not see)
-    const float next = fmaxf(top, t), down = exp2_fast(top - next), up = exp2_fast(t - next);
-    top = next, sum = sum * down + s * up;
-    acc[0] = acc[0] * down + v.x * up, acc[1] = acc[1] * down + v.y * up, acc[2] = acc[2] * down + v.z * up, acc[3] = acc[3] * down + v.w * up;
-  }
+// A piece, for the CTA's queries.
+struct Listed {
+  const float* piece;  // nullptr: none
+  int height, at;      // its rows; that of the CTA's first query
 };
 
-// Every JOIN_WAYS-th piece of query m of a set's KV head.
-template <int D>
-__device__ __forceinline__ void join_set(const SharedParams& p, const Plan& plan, int which, int head, int m, int d4, int way, Joining& j) {
-  using S = SharedShape<D>;
-  const int4* from = reinterpret_cast<const int4*>(p.sets + which);
-  const int4 a = from[0], b = from[1], c = from[2];
-  const Set set = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
-  const bool prefix = set.kv < 0;
-  const int tile = m / S::QUERIES, in = m - tile * S::QUERIES, unit = tile * p.kv_heads + head;
-  const int work = unit_work(set), start = set.start + unit * work;
-  // the last CTA whose share begins at or before x is ((x + 1) ctas - 1) / total
-  const int c0 = int((int64_t(start + 1) * plan.ctas - 1) / plan.total), c1 = int((int64_t(start + work) * plan.ctas - 1) / plan.total);
-  const int rows = prefix ? 128 : p.suffix_rows, height = S::TILES * rows;
-  const int64_t floats = prefix ? S::PIECE : height * (D + 2);
-  const int at = set.both ? in / 128 * rows + in % 128 : in;
-  const float* pieces = (prefix ? p.prefix_pieces : p.suffix_pieces) + int64_t(set.unit0 + unit) * floats;
-  const bool twice = S::TILES == 2 && !set.both;  // even steps in one tile, odd ones in the other
-  const int per = twice ? 2 : 1, count = (c1 - c0 + 1) * per;
-  for (int x0 = way; x0 < count; x0 += JOIN_WAYS * JOIN_AT_ONCE) {
-    float t[JOIN_AT_ONCE], s[JOIN_AT_ONCE];
-    float4 v[JOIN_AT_ONCE];
-#pragma unroll
-    for (int i = 0; i < JOIN_AT_ONCE; ++i) {
-      const int x = x0 + i * JOIN_WAYS, cta = c0 + (twice ? x >> 1 : x), second = twice ? x & 1 : 0;
-      s[i] = 0.f;
-      if (x < count) {
-        const int lo = step_of(p.cta_start[cta], start, set.both, set.steps), hi = step_of(p.cta_start[cta + 1], start, set.both, set.steps);
-        if (hi - lo > second) {
-          const float* piece = pieces + int64_t(cta) * floats;
-          const int row = at + second * rows;
-          t[i] = piece[int64_t(height) * D + row], s[i] = piece[int64_t(height) * (D + 1) + row];
-          v[i] = *reinterpret_cast<const float4*>(piece + (int64_t(d4) * height + row) * 4);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < JOIN_AT_ONCE; ++i) j.add(t[i], s[i], v[i]);
-  }
-}
+// Pieces of a query at most: the units that it is in are cut where CTAs' shares end, and of each CTA it has up to two.
+__host__ __device__ constexpr int join_pieces(int grid) { return 2 * (grid + 3); }
+__host__ __device__ constexpr int join_smem(int grid) { return join_pieces(grid) * (JOIN_ROWS * 8 + int(sizeof(Listed))); }
 
-// blockIdx.x: requests x KV heads; y: parts of the request's queries x dimensions.  JOIN_WAYS neighbouring lanes have four
-// dimensions of a query, neighbouring groups of lanes neighbouring queries, as they lie in a piece.
+// blockIdx.x: requests x KV heads; y: JOIN_ROWS of the request's queries; z: JOIN_WIDTH dimensions, four a thread.  Neighbouring
+// threads have neighbouring queries, as they lie in a piece.  The pieces of the CTA's queries are listed first, and each one's
+// factor found, once for all dimensions; then a thread adds up its values, JOIN_AT_ONCE loads under way.
 template <int D>
 __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(SharedParams p) {
-  const int r = blockIdx.x / p.kv_heads, h = blockIdx.x - r * p.kv_heads, members = p.next_n * p.group;
+  using S = SharedShape<D>;
+  extern __shared__ __align__(16) uint8_t join_memory[];
+  const int most = join_pieces(p.grid);
+  float* factors = reinterpret_cast<float*>(join_memory);  // [most][JOIN_ROWS]: bases, then factors; -1: not this query's
+  float* sums = factors + most * JOIN_ROWS;                // [most][JOIN_ROWS]
+  Listed* list = reinterpret_cast<Listed*>(sums + most * JOIN_ROWS);
+  __shared__ float tops[JOIN_ROWS], totals[JOIN_ROWS];
+  const int tid = threadIdx.x, lane = tid & 31, r = blockIdx.x / p.kv_heads, head = blockIdx.x - r * p.kv_heads, members = p.next_n * p.group;
+  const int m0 = blockIdx.y * JOIN_ROWS;
   begin();
   const int4 held = *reinterpret_cast<const int4*>(p.plan);
   const Plan plan = {held.x, held.y, held.z, held.w};
   const Joined join = p.joined[r];
-  const int prefix_row0 = join.prefix >= 0 ? p.sets[join.prefix].row0 : 0;
-  const int way = threadIdx.x % JOIN_WAYS, items = members * (D / 4);
-  constexpr int AT_ONCE = JOIN_SHARED_THREADS / JOIN_WAYS;
-  for (int i0 = blockIdx.y * AT_ONCE; i0 < items; i0 += gridDim.y * AT_ONCE) {  // the same number of turns in all lanes
-    const int i = min(i0 + int(threadIdx.x) / JOIN_WAYS, items - 1);
-    const int d4 = i / members, m = i - d4 * members, rel = m / p.group;
-    const int64_t row = int64_t(r) * p.next_n + rel;
-    Joining j;
-    if (row < p.num_rows) {
-      if (join.prefix >= 0) join_set<D>(p, plan, join.prefix, h, int(int64_t(r) * p.next_n - prefix_row0) * p.group + m, d4, way, j);
-      if (join.suffix >= 0) join_set<D>(p, plan, join.suffix, h, m, d4, way, j);
-    }
+  // ---- the list, by part: the prefix's unit of the first query, the unit behind that (the CTA's queries can lie in two),
+  // and the request's own
+  int count = 0, ends[3], border = members;  // queries from the border on are in the prefix's second unit
 #pragma unroll
-    for (int x = 1; x < JOIN_WAYS; x <<= 1) {
-      const float other = __shfl_xor_sync(0xffffffffu, j.top, x), next = fmaxf(j.top, other);
-      const float scale = exp2_fast(j.top - next);  // of both sides the same base: every lane ends with the same sums
-      j.top = next, j.sum *= scale;
-      j.sum += __shfl_xor_sync(0xffffffffu, j.sum, x);
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        j.acc[y] *= scale;
-        j.acc[y] += __shfl_xor_sync(0xffffffffu, j.acc[y], x);
+  for (int part = 0; part < 3; ++part) {
+    const int which = part < 2 ? join.prefix : join.suffix;
+    if (which >= 0) {
+      const int4* from = reinterpret_cast<const int4*>(p.sets + which);
+      const int4 a = from[0], b = from[1], c = from[2];
+      const Set set = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+      const int offset = part < 2 ? (r * p.next_n - set.row0) * p.group : 0;  // of the request's queries in the set
+      const int tile = (offset + m0) / S::QUERIES + (part == 1);
+      if (part == 0) border = (tile + 1) * S::QUERIES - offset;
+      if (part != 1 || border < min(m0 + JOIN_ROWS, members)) {
+        const int unit = tile * p.kv_heads + head, work = unit_work(set), start = set.start + unit * work;
+        // the last CTA whose share begins at or before x is ((x + 1) ctas - 1) / total
+        const int c0 = int((int64_t(start + 1) * plan.ctas - 1) / plan.total), c1 = int((int64_t(start + work) * plan.ctas - 1) / plan.total);
+        const int rows = part < 2 ? 128 : p.suffix_rows, height = S::TILES * rows;
+        const int64_t floats = part < 2 ? S::PIECE : height * (D + 2);
+        const int twice = S::TILES == 2 && !set.both;  // even steps in one tile, odd ones in the other
+        const float* pieces = (part < 2 ? p.prefix_pieces : p.suffix_pieces) + int64_t(set.unit0 + unit) * floats;
+        const int here = (c1 - c0 + 1) << twice;
+        for (int x = tid; x < here; x += JOIN_SHARED_THREADS) {
+          const int cta = c0 + (x >> twice), second = twice ? x & 1 : 0;
+          const int lo = step_of(range_start(cta, plan.ctas, plan.total), start, set.both, set.steps);
+          const int hi = step_of(range_start(cta + 1, plan.ctas, plan.total), start, set.both, set.steps);
+          list[count + x] = {hi - lo > second ? pieces + int64_t(cta) * floats : nullptr, height, offset + m0 - tile * S::QUERIES + second * rows};
+        }
+        count += here;
       }
     }
-    if (way != 0 || row >= p.num_rows) continue;
-    if (plan.failed) j.sum = NAN;
-    const float norm = j.sum == 0.f ? 0.f : 1.f / j.sum;
-    uint32_t packed[2];
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const float lo = j.acc[2 * y] * norm * p.v_scale, hi = j.acc[2 * y + 1] * norm * p.v_scale;
-      if (p.bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed[y]) : "f"(hi), "f"(lo));
-      else packed[y] = pack_f16(lo, hi);
-    }
-    const int64_t at = row * (int64_t(p.kv_heads) * p.group) + h * p.group + (m - rel * p.group);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D + d4 * 4) = make_uint2(packed[0], packed[1]);
-    if (p.lse && d4 == 0) p.lse[at] = j.sum == 0.f ? -INFINITY : (j.top + log2f(j.sum)) * 0.69314718055994531f;
+    ends[part] = count;
   }
+  __syncthreads();
+  for (int i = tid; i < count * JOIN_ROWS; i += JOIN_SHARED_THREADS) {
+    const int k = i / JOIN_ROWS, row = i % JOIN_ROWS, m = m0 + row;
+    const bool own = m < members && (k >= ends[1] || (k >= ends[0]) == (m >= border));
+    float top = NO_TOP, sum = 0.f;
+    if (own && list[k].piece) {
+      const float* at = list[k].piece + int64_t(list[k].height) * D + list[k].at + row;
+      top = at[0], sum = at[list[k].height];
+    }
+    factors[i] = top, sums[i] = sum;
+  }
+  __syncthreads();
+  // ---- each query's base, factors and sum, by a warp, two queries each
+  for (int row = tid >> 5; row < JOIN_ROWS; row += JOIN_SHARED_THREADS / 32) {
+    float top = NO_TOP, total = 0.f;
+    for (int k = lane; k < count; k += 32)
+      if (sums[k * JOIN_ROWS + row] != 0.f) top = fmaxf(top, factors[k * JOIN_ROWS + row]);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    for (int k = lane; k < count; k += 32) {
+      const float sum = sums[k * JOIN_ROWS + row], factor = exp2_fast(factors[k * JOIN_ROWS + row] - top);
+      // a sum of 0 saw nothing there (and what it holds may be a NaN of entries that it does not see)
+      factors[k * JOIN_ROWS + row] = sum == 0.f ? -1.f : factor;
+      if (sum != 0.f) total += sum * factor;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    if (lane == 0) tops[row] = top, totals[row] = total;
+  }
+  __syncthreads();
+  // ---- the values
+  const int row = tid % JOIN_ROWS, m = m0 + row, d4 = blockIdx.z * (JOIN_WIDTH / 4) + tid / JOIN_ROWS, rel = m / p.group;
+  const int64_t row_at = int64_t(r) * p.next_n + rel;
+  if (m >= members || row_at >= p.num_rows) return;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < count; k0 += JOIN_AT_ONCE) {
+    float4 v[JOIN_AT_ONCE];
+    float f[JOIN_AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < JOIN_AT_ONCE; ++i) {
+      f[i] = k0 + i < count ? factors[(k0 + i) * JOIN_ROWS + row] : -1.f;
+      if (f[i] >= 0.f) {
+        const Listed l = list[k0 + i];
+        v[i] = *reinterpret_cast<const float4*>(l.piece + (int64_t(d4) * l.height + l.at + row) * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < JOIN_AT_ONCE; ++i)
+      if (f[i] >= 0.f) acc[0] += f[i] * v[i].x, acc[1] += f[i] * v[i].y, acc[2] += f[i] * v[i].z, acc[3] += f[i] * v[i].w;
+  }
+  const float total = plan.failed ? NAN : totals[row], norm = total == 0.f ? 0.f : 1.f / total;
+  uint32_t packed[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    // v_scale last: v_scale / total would lose bits, or all, of a small factor over many entries
+    const float lo = acc[2 * y] * norm * p.v_scale, hi = acc[2 * y + 1] * norm * p.v_scale;
+    if (p.bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(packed[y]) : "f"(hi), "f"(lo));
+    else packed[y] = pack_f16(lo, hi);
+  }
+  const int64_t at = row_at * (int64_t(p.kv_heads) * p.group) + head * p.group + (m - rel * p.group);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at * D + d4 * 4) = make_uint2(packed[0], packed[1]);
+  if (p.lse && d4 == 0) p.lse[at] = total == 0.f ? -INFINITY : (tops[row] + log2f(total)) * 0.69314718055994531f;
 }
 
 // What the host needs to know of a head dimension's kernels.
