@@ -21,6 +21,7 @@ namespace {
 constexpr int WEIGHT_WARPS = 8, WEIGHT_THREADS = 32 * WEIGHT_WARPS;
 constexpr int AHEAD = 3;              // stages of a warp's ring
 constexpr int QUERY_BYTES = 1 << 16;  // of queries in shared memory, at most
+constexpr int MANY = 4;               // steps of 32 entries a warp
 
 struct WeightParams {
   const uint8_t* data;
@@ -46,16 +47,19 @@ struct Query {
   int pad;
 };
 
-template <int D>
+// MT tiles of 16 entries a step: two, or one where steps of two are too few for the device's warps.
+template <int D, int MT>
 struct WeightShape {
+  static constexpr int STEP = 16 * MT;
   static constexpr int PITCH = (D / 2 + D / 16 + 15) / 16 * 16 | 16;  // of a row's K codes and scales: an odd multiple of 16
   static constexpr int STAGE = STEP * PITCH, RING = AHEAD * STAGE;
   static constexpr int TILE = 8 * D * 2;  // bytes of 8 queries
 };
 
-template <int D>
+template <int D, int MT>
 __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams p) {
-  using S = WeightShape<D>;
+  using S = WeightShape<D, MT>;
+  constexpr int STEP = S::STEP;
   constexpr int CODES = D / 32;  // 16-byte pieces of a row's K codes
   constexpr int KW = D / 32;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -74,7 +78,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
   int before = 0;
   for (int r0 = 0; r0 < p.requests; r0 += WEIGHT_THREADS) {
     const int r = r0 + tid;
-    int x = r < p.requests ? steps_of(uint32_t(entries(r))) : 0;
+    int x = r < p.requests ? (entries(r) + STEP - 1) / STEP : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -120,18 +124,30 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
         const int heads = min(p.part_heads, p.kv_heads - head0), tiles = min(p.part_tiles, p.tiles - tile0);
         // ---- the queries: lane (g, c) of a tile holds D / 4 values of query g
         __syncthreads();  // the last part is used up
-        for (int i = warp; i < heads * tiles; i += WEIGHT_WARPS) {
+        // (loaded a turn ahead)
+        uint32_t raw[D / 8], next[D / 8];
+        float sum = 0.f, next_sum = 0.f;
+        auto fetch_query = [&](int i, uint32_t(&to)[D / 8], float& log_sum) {
           const int h = head0 + i / tiles, m = (tile0 + i % tiles) * 8 + g;
           const int64_t row = int64_t(request) * p.next_n + m / p.group;
           const int head = h * p.group + m % p.group;
-          const bool live = m < members && row < p.num_rows;
+          const bool live = i < heads * tiles && m < members && row < p.num_rows;
           const uint4* src = reinterpret_cast<const uint4*>(p.q + row * p.q_row + head * p.q_head + c * (D / 4));
-          uint32_t raw[D / 8];
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
             const uint4 v = live ? src[j] : make_uint4(0, 0, 0, 0);
-            raw[4 * j] = v.x, raw[4 * j + 1] = v.y, raw[4 * j + 2] = v.z, raw[4 * j + 3] = v.w;
+            to[4 * j] = v.x, to[4 * j + 1] = v.y, to[4 * j + 2] = v.z, to[4 * j + 3] = v.w;
           }
+          log_sum = live ? p.lse[row * (int64_t(p.kv_heads) * p.group) + head] : 0.f;
+        };
+        fetch_query(warp, next, next_sum);
+        for (int i = warp; i < heads * tiles; i += WEIGHT_WARPS) {
+          const int m = (tile0 + i % tiles) * 8 + g;
+          const bool live = m < members && int64_t(request) * p.next_n + m / p.group < p.num_rows;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) raw[j] = next[j];
+          sum = next_sum;
+          fetch_query(i + WEIGHT_WARPS, next, next_sum);
           float back = 1.f;
           if (p.bf16) {  // exactly to f16, by a power of two per query (gvr_attend.cuh)
             uint32_t big = 0;
@@ -157,7 +173,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
           if (c == 0) {
             Query x;
             x.factor = fmaxf(back * p.scale_log2, 1.17549435e-38f);
-            x.off = live ? p.lse[row * (int64_t(p.kv_heads) * p.group) + head] * 1.4426950408889634f : 0.f;
+            x.off = sum * 1.4426950408889634f;
             x.limit = live ? decode_entries(kv, p.next_n, m / p.group, p.ratio, p.capacity) : 0;  // 0: adds nothing
             queries[i * 8 + g] = x;
           }
@@ -167,7 +183,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
         // ---- this warp's steps, KV head by KV head
         const int mine = segment > warp ? (segment - warp + WEIGHT_WARPS - 1) / WEIGHT_WARPS : 0, items = mine * heads;
         int ahead_step = 0, ahead_head = 0;  // of the next item to fetch
-        auto entry_of = [&](int step) { return (first + warp + step * WEIGHT_WARPS) * STEP + lane; };
+        auto entry_of = [&](int step) { return (first + warp + step * WEIGHT_WARPS) * STEP + lane % STEP; };
         auto page_of = [&](int step) {
           const int e = entry_of(step);
           return step < mine && e < n ? table[e >> p.page_shift] : -1;
@@ -192,14 +208,15 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
               const uint32_t to = ring_at + stage * S::STAGE;
               const uint32_t here = from + uint32_t(ahead_head) * p.row_units;
 #pragma unroll
-              for (int j = 0; j < CODES; ++j) {  // CODES neighbouring lanes copy a row's codes
+              for (int j = 0; j < CODES * MT / 2; ++j) {  // CODES neighbouring lanes copy a row's codes
                 const int row = j * (32 / CODES) + lane / CODES;
                 const uint32_t of = __shfl_sync(0xffffffffu, here, row);
                 copy16(to + row * S::PITCH + lane % CODES * 16, p.data + uint64_t(of) * p.unit + lane % CODES * 16);
               }
               const uint8_t* scales = p.data + uint64_t(here) * p.unit + D;
               const uint32_t scales_to = to + lane * S::PITCH + D / 2;
-              if (D == 256) copy16(scales_to, scales);
+              if (MT == 1 && lane >= STEP) {
+              } else if (D == 256) copy16(scales_to, scales);
               else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(scales_to), "l"(scales), "n"(D == 128 ? 8 : 4) : "memory");
             }
             if (++ahead_head == heads) ahead_head = 0, ++ahead_step;
@@ -210,7 +227,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
 #pragma unroll
         for (int i = 0; i < AHEAD - 1; ++i) there_of[i] = fetch(i);
 
-        float acc[2][2] = {};  // of entries tile_entry(g), tile_entry(g + 8) of both tiles
+        float acc[MT][2] = {};  // of entries tile_entry(g), tile_entry(g + 8) of both tiles
         int step = 0, h = 0, stage = 0;
         const int k_at = tile_entry(g) * S::PITCH;
         for (int item = 0; item < items; ++item) {
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
             const bool border = e0 + STEP > sure;
             const uint8_t* st = ring + stage * S::STAGE;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
               const uint8_t *r0 = st + k_at + 16 * mt * S::PITCH, *r1 = r0 + S::PITCH;
               uint32_t k0[KW], k1[KW], a[2 * KW][4];  // operands of 2 KW 16-wide steps
               load_words<KW>(r0 + c * (D / 8), k0);
@@ -245,15 +262,18 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[2 * w + j / 2][j % 2 * 2] = hmul2(x[j], x0), a[2 * w + j / 2][j % 2 * 2 + 1] = hmul2(y[j], y0);
               }
+#pragma unroll 2
               for (int t = 0; t < tiles; ++t) {
                 const int tile = h * tiles + t;
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
+                float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of sums
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {
                   const uint4 b = operands[(tile * (D / 32) + j) * 32 + lane];
                   mma(s, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], b.x, b.y);
-                  mma(s, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], b.z, b.w);
+                  mma(s2, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], b.z, b.w);
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] += s2[j];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   const Query q = queries[tile * 8 + 2 * c + j];
@@ -272,7 +292,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
           if (++h == heads) {  // the step's last head: lane i's is entry i
             h = 0, ++step;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 acc[mt][j] += __shfl_xor_sync(0xffffffffu, acc[mt][j], 1);
@@ -280,12 +300,13 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
               }
             // entry y of a tile is tile_entry(x + 8 (y & 1)) of x = y & ~1 below 8, and of the x that (x + 3) & 7 leads to it above
             const int y = lane & 15, even = y & ~1, x = even < 8 ? even : (even + 5) & 7;
-            float v[4];
+            float v[2 * MT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = __shfl_sync(0xffffffffu, acc[j >> 1][j & 1], 4 * x);
-            const float w = lane < 16 ? (y & 1 ? v[1] : v[0]) : (y & 1 ? v[3] : v[2]);
-            if (there >> lane & 1) weights[e0 + lane] += w;
-            acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = 0.f;
+            for (int j = 0; j < 2 * MT; ++j) v[j] = __shfl_sync(0xffffffffu, acc[j >> 1][j & 1], 4 * x);
+            const float w = lane < 16 ? (y & 1 ? v[1] : v[0]) : (y & 1 ? v[2 * MT - 1] : v[2 * MT - 2]);
+            if (lane < STEP && (there >> lane & 1)) weights[e0 + lane] += w;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = 0.f;
           }
         }
         copy_wait<0>();
@@ -294,12 +315,19 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
   }
 }
 
-const void* weights_kernel_of(int dim) {
-  return dim == 64 ? reinterpret_cast<const void*>(weights_kernel<64>) : dim == 128 ? reinterpret_cast<const void*>(weights_kernel<128>)
-                                                                                     : reinterpret_cast<const void*>(weights_kernel<256>);
+struct WeightInfo {
+  const void* kernel;
+  int ring;  // bytes of all warps
+};
+template <int D, int MT>
+WeightInfo weight_info() {
+  return {reinterpret_cast<const void*>(weights_kernel<D, MT>), WEIGHT_WARPS * WeightShape<D, MT>::RING};
 }
-
-int ring_bytes(int dim) { return WEIGHT_WARPS * (dim == 64 ? WeightShape<64>::RING : dim == 128 ? WeightShape<128>::RING : WeightShape<256>::RING); }
+WeightInfo weights_kernel_of(int dim, int tiles) {
+  if (dim == 64) return tiles == 1 ? weight_info<64, 1>() : weight_info<64, 2>();
+  if (dim == 128) return tiles == 1 ? weight_info<128, 1>() : weight_info<128, 2>();
+  return tiles == 1 ? weight_info<256, 1>() : weight_info<256, 2>();
+}
 
 struct WeightDevice {
   std::once_flag once;
@@ -332,7 +360,8 @@ gvr_status attend_weights(const gvr_cache* cache, const void* q, int64_t q_row_s
     int most = 0;
     d.err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     for (int dim : {64, 128, 256})
-      if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(weights_kernel_of(dim), cudaFuncAttributeMaxDynamicSharedMemorySize, most - 1024);
+      for (int tiles : {1, 2})
+        if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(weights_kernel_of(dim, tiles).kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - 1024);
   });
   if (d.err != cudaSuccess) return GVR_ERR_LAUNCH;
   WeightParams p = {};
@@ -362,19 +391,24 @@ gvr_status attend_weights(const gvr_cache* cache, const void* q, int64_t q_row_s
   p.bf16 = dtype == GVR_BF16;
   p.requests = int32_t((num_rows + next_n - 1) / next_n);
   // steps are counted in 32 bits
-  const int64_t steps = (int64_t(p.capacity) + STEP - 1) / STEP;
-  if (steps * p.requests > kIntMax) return GVR_ERR_ARG;
+  const int64_t halves = (int64_t(p.capacity) + 15) / 16;
+  if (halves * p.requests > kIntMax) return GVR_ERR_ARG;
+  // steps of 32 entries, or of 16 where a warp has fewer than MANY of those, by the table's width
+  const int64_t warps = int64_t(2) * sms * WEIGHT_WARPS;
+  const int mt = halves * p.requests < 2 * MANY * warps ? 1 : 2;
+  const int64_t steps = (halves + mt - 1) / mt;
+  const WeightInfo info = weights_kernel_of(dim, mt);
   p.tiles = (next_n * p.group + 7) / 8;
   const int most = QUERY_BYTES / (16 * dim);  // tiles that shared memory holds
   p.part_tiles = std::min(p.tiles, most);
   p.part_heads = std::max(1, std::min(p.kv_heads, most / p.part_tiles));
   p.scale_log2 = scale == 0.f ? 1.f : float(std::fabs(double(scale)) * cache->k_scale * 1.4426950408889634);
   p.q_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
-  const int smem = ring_bytes(dim) + p.part_tiles * p.part_heads * (16 * dim + 8 * int(sizeof(Query))) + (p.requests + 1) * 4;
+  const int smem = info.ring + p.part_tiles * p.part_heads * (16 * dim + 8 * int(sizeof(Query))) + (p.requests + 1) * 4;
   const int64_t grid = std::min<int64_t>(2 * sms, (steps * p.requests + WEIGHT_WARPS - 1) / WEIGHT_WARPS);
   if (grid == 0) return GVR_OK;
   void* args[] = {&p};
-  return launch(weights_kernel_of(dim), dim3(uint32_t(grid)), WEIGHT_THREADS, smem, 1, args, stream) == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
+  return launch(info.kernel, dim3(uint32_t(grid)), WEIGHT_THREADS, smem, 1, args, stream) == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
 }
 
 }  // extern "C"
