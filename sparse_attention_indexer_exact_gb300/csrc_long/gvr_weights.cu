@@ -39,12 +39,10 @@ struct WeightParams {
   float scale_log2, q_sign;
 };
 
-// A query in shared memory, beside its operand.
-struct Query {
-  float factor;  // of its scores, to log2 units
-  float off;     // its log-sum in log2 units
-  int limit;     // entries that it sees
-  int pad;
+// Two neighbouring queries in shared memory, beside their operands: the factors of their scores, to log2 units, and their
+// log-sums in those (infinite for no query: it adds nothing); the entries that they see.
+struct Queries {
+  float factor0, off0, factor1, off1;
 };
 
 // MT tiles of 16 entries a step: two, or one where steps of two are too few for the device's warps.
@@ -68,13 +66,17 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
   const int part = p.part_heads * p.part_tiles;
   uint8_t* ring = smem + warp * S::RING;
   uint4* operands = reinterpret_cast<uint4*>(smem + WEIGHT_WARPS * S::RING);  // [part][D / 32][32 lanes]
-  Query* queries = reinterpret_cast<Query*>(smem + WEIGHT_WARPS * S::RING + part * S::TILE);  // [part][8]
-  int* start = reinterpret_cast<int*>(queries + part * 8);  // [requests + 1]: the steps before each request
+  Queries* queries = reinterpret_cast<Queries*>(smem + WEIGHT_WARPS * S::RING + part * S::TILE);  // [part][4]
+  int2* limits = reinterpret_cast<int2*>(queries + part * 4);  // [part][4]
+  int* start = reinterpret_cast<int*>(limits + part * 4);  // [requests + 1]: the steps before each request
   __shared__ int sums[WEIGHT_WARPS];
 
   begin();
   // ---- steps of all requests
-  auto entries = [&](int r) { return decode_entries(p.lens[r], p.next_n, p.next_n - 1, p.ratio, p.capacity); };
+  // entries that some row of the request sees (the last request may have fewer rows)
+  auto entries = [&](int r) {
+    return decode_entries(p.lens[r], p.next_n, int(min(int64_t(p.next_n), p.num_rows - int64_t(r) * p.next_n)) - 1, p.ratio, p.capacity);
+  };
   int before = 0;
   for (int r0 = 0; r0 < p.requests; r0 += WEIGHT_THREADS) {
     const int r = r0 + tid;
@@ -171,11 +173,10 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
           for (int j = 0; j < D / 32; ++j)
             operands[(i * (D / 32) + j) * 32 + lane] = make_uint4(raw[4 * j], raw[4 * j + 1], raw[4 * j + 2], raw[4 * j + 3]);
           if (c == 0) {
-            Query x;
-            x.factor = fmaxf(back * p.scale_log2, 1.17549435e-38f);
-            x.off = sum * 1.4426950408889634f;
-            x.limit = live ? decode_entries(kv, p.next_n, m / p.group, p.ratio, p.capacity) : 0;  // 0: adds nothing
-            queries[i * 8 + g] = x;
+            float* query = reinterpret_cast<float*>(queries + i * 4) + 2 * g;
+            query[0] = fmaxf(back * p.scale_log2, 1.17549435e-38f);
+            query[1] = live ? sum * 1.4426950408889634f : INFINITY;
+            reinterpret_cast<int*>(limits + i * 4)[g] = live ? decode_entries(kv, p.next_n, m / p.group, p.ratio, p.capacity) : 0;
           }
         }
         __syncthreads();
@@ -262,30 +263,38 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[2 * w + j / 2][j % 2 * 2] = hmul2(x[j], x0), a[2 * w + j / 2][j % 2 * 2 + 1] = hmul2(y[j], y0);
               }
-#pragma unroll 2
-              for (int t = 0; t < tiles; ++t) {
-                const int tile = h * tiles + t;
-                float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of sums
+              auto add_up = [&](auto bordering) {
+                constexpr int AT_ONCE = D == 64 && !decltype(bordering)::value ? 2 : 1;
+#pragma unroll AT_ONCE
+                for (int t = 0; t < tiles; ++t) {
+                  const int tile = h * tiles + t;
+                  float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                  const uint4 b = operands[(tile * (D / 32) + j) * 32 + lane];
-                  mma(s, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], b.x, b.y);
-                  mma(s2, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], b.z, b.w);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] += s2[j];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const Query q = queries[tile * 8 + 2 * c + j];
-                  float w0 = exp2_fast(fmaf(s[j], q.factor, -q.off)), w1 = exp2_fast(fmaf(s[j + 2], q.factor, -q.off));
-                  if (border || q.limit == 0) {
-                    const int e = e0 + 16 * mt + tile_entry(g);  // the other one is e + 1
-                    if (e >= q.limit) w0 = 0.f;
-                    if (e + 1 >= q.limit) w1 = 0.f;
+                  for (int j = 0; j < D / 32; ++j) {
+                    const uint4 b = operands[(tile * (D / 32) + j) * 32 + lane];
+                    mma(s, a[2 * j][0], a[2 * j][1], a[2 * j][2], a[2 * j][3], b.x, b.y);
+                    mma(D > 64 ? s2 : s, a[2 * j + 1][0], a[2 * j + 1][1], a[2 * j + 1][2], a[2 * j + 1][3], b.z, b.w);
                   }
-                  acc[mt][0] += w0, acc[mt][1] += w1;
+                  if (D > 64) {  // long chains in two
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] += s2[j];
+                  }
+                  const Queries q = queries[tile * 4 + c];
+                  float w0 = exp2_fast(fmaf(s[0], q.factor0, -q.off0)), w1 = exp2_fast(fmaf(s[1], q.factor1, -q.off1));
+                  float w2 = exp2_fast(fmaf(s[2], q.factor0, -q.off0)), w3 = exp2_fast(fmaf(s[3], q.factor1, -q.off1));
+                  if (decltype(bordering)::value) {
+                    const int2 limit = limits[tile * 4 + c];
+                    const int e = e0 + 16 * mt + tile_entry(g);  // the tile's other row is e + 1
+                    if (e >= limit.x) w0 = 0.f;
+                    if (e >= limit.y) w1 = 0.f;
+                    if (e + 1 >= limit.x) w2 = 0.f;
+                    if (e + 1 >= limit.y) w3 = 0.f;
+                  }
+                  acc[mt][0] += w0 + w1, acc[mt][1] += w2 + w3;
                 }
-              }
+              };
+              if (border) add_up(std::true_type());
+              else add_up(std::false_type());
             }
           }
           stage = stage == AHEAD - 1 ? 0 : stage + 1;
@@ -404,7 +413,7 @@ gvr_status attend_weights(const gvr_cache* cache, const void* q, int64_t q_row_s
   p.part_heads = std::max(1, std::min(p.kv_heads, most / p.part_tiles));
   p.scale_log2 = scale == 0.f ? 1.f : float(std::fabs(double(scale)) * cache->k_scale * 1.4426950408889634);
   p.q_sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
-  const int smem = info.ring + p.part_tiles * p.part_heads * (16 * dim + 8 * int(sizeof(Query))) + (p.requests + 1) * 4;
+  const int smem = info.ring + p.part_tiles * p.part_heads * (16 * dim + 4 * int(sizeof(Queries) + sizeof(int2))) + (p.requests + 1) * 4;
   const int64_t grid = std::min<int64_t>(2 * sms, (steps * p.requests + WEIGHT_WARPS - 1) / WEIGHT_WARPS);
   if (grid == 0) return GVR_OK;
   void* args[] = {&p};
