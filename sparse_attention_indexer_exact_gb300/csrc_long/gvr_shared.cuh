@@ -85,7 +85,7 @@ struct SharedShape {
   static constexpr int QUERIES = 128 * TILES;        // of a unit
   static constexpr int ROWS = N / 4;                 // rows a warp expands in a step
   static constexpr int Q_BYTES = 128 * D * 2, KV_BYTES = N * D * 2;
-  static constexpr int RB = row_bytes(D), RAW = N * RB, STAGES = 3;  // rows as they are, of the steps under way
+  static constexpr int RB = row_bytes(D), RAW = N * RB, STAGES = D == 64 ? 6 : 3;  // rows as they are, of the steps under way
   static constexpr int WARPS = 8 * TILES + 12, THREADS = 32 * WARPS;  // S takers, K and V, and the issuer, the walker and two idle ones
   static constexpr int PIECE = QUERIES * (D + 2);    // floats of a prefix piece
   static constexpr int S_AT = 0, O_AT = 2 * N;  // columns; P lies over its scores, the halves' where theirs begin
@@ -296,7 +296,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
 }
 
 constexpr int SEGMENTS = 4;  // noted ahead
-constexpr int STEP_NOTES = 4;
+constexpr int STEP_NOTES = 8, MOST_STAGES = 6;
 
 // Uses of two buffers in turn.
 struct Turn {
@@ -306,7 +306,7 @@ struct Turn {
 };
 
 struct SharedBars {
-  uint64_t raw_full[3], raw_free[3], k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint64_t raw_full[MOST_STAGES], raw_free[MOST_STAGES], k_full[2], k_free[2], v_full[2], v_free[2], q_full[2], s_full[2], p_full[2], o_full[2], done;
   uint64_t seg_full[SEGMENTS], seg_free[SEGMENTS];
 };
 
@@ -321,7 +321,7 @@ struct __align__(16) StepNote {
 // What the warps of a CTA tell each other beside the operands.
 struct SharedNotes {
   Segment segments[SEGMENTS];
-  StepNote steps[STEP_NOTES];  // a step's is written once the one four before it is through with
+  StepNote steps[STEP_NOTES];  // rows are loaded at most STAGES + 1 steps before their scores are through with
 };
 
 __device__ __forceinline__ bool next_segment(SharedBars* bars, uint32_t count) { return bar_wait(&bars->seg_full[count % SEGMENTS], count / SEGMENTS & 1); }
@@ -535,8 +535,8 @@ __device__ __forceinline__ bool multiply(SharedBars* bars, const SharedNotes* no
   const int lane = threadIdx.x & 31;
   Turn k_turn;
   uint32_t v_used = 0;
-  uint32_t q_used[2] = {0, 0}, p_used[2] = {0, 0};
-  int buffer = 0;  // one tile: of S, in turn
+  uint32_t q_phase = 0, p_phase = 0;  // a bit a tile, a bit a buffer of S  (arrays would be in memory, between every two products)
+  int buffer = 0;                     // one tile: of S, in turn
   for (uint32_t count = 0;; ++count) {
     if (!warp_wait(&bars->seg_full[count % SEGMENTS], count / SEGMENTS & 1)) return false;
     const Segment& s = notes->segments[count % SEGMENTS];
@@ -558,8 +558,8 @@ __device__ __forceinline__ bool multiply(SharedBars* bars, const SharedNotes* no
       const uint32_t scores = tmem + S::S_AT + b * S::N, sums = tmem + S::O_AT + tile * D;
       if (weigh) {
         if (first) ok &= bar_wait(&bars->v_full[0], v_used & 1) & bar_wait(&bars->v_full[1], v_used & 1);
-        ok &= bar_wait(&bars->p_full[b], p_used[b] & 1);
-        ++p_used[b];
+        ok &= bar_wait(&bars->p_full[b], p_phase >> b & 1);
+        p_phase ^= 1u << b;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -574,8 +574,8 @@ __device__ __forceinline__ bool multiply(SharedBars* bars, const SharedNotes* no
       }
       if (score) {
         if (next < S::TILES) {
-          ok &= bar_wait(&bars->q_full[tile], q_used[tile] & 1);
-          ++q_used[tile];
+          ok &= bar_wait(&bars->q_full[tile], q_phase >> tile & 1);
+          q_phase ^= 1u << tile;
         }
         if (first) ok &= bar_wait(&bars->k_full[slot], k_turn.parity());
         tc_fence_after();
@@ -642,14 +642,18 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
   float* totals = exchange + S::TILES * 2 * 128;  // of the second halves
   const uint32_t lanes = uint32_t(quarter) << 21;  // 32 quarter << 16
   const uint32_t q_row_at = q_at + tile * S::Q_BYTES + row * 128;
-  uint32_t s_used[2] = {0, 0}, o_used[2] = {0, 0};
+  uint32_t done = 0;                 // tasks of this tile so far: theirs are S and O in turn (one tile: in two buffers)
   uint32_t steps = 0, segments = 0;  // K steps of the segments before, and segments with work for this tile
   uint32_t count = 0;                // segments so far
-  int buffer = 0;
   // A wait that gave up: this warp goes on without waiting until it meets the other one, and both end.
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = warp_wait(bar, parity);
+  };
+
+  auto wait_products = [&]() {  // with V, of the last task
+    const uint32_t last = done - 1;
+    wait(&bars->o_full[S::TILES == 2 ? tile : int(last & 1)], (S::TILES == 2 ? last : last >> 1) & 1);
   };
 
   // Segment-wide facts of this thread's query.
@@ -737,9 +741,8 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
   while (x.steps > 0) {
     float top = NO_TOP, total = 0.f;
     for (int i = 0; i < x.tasks; ++i) {
-      const int b = S::TILES == 2 ? tile : (buffer + i) & 1;
-      wait(&bars->s_full[b], s_used[b] & 1);
-      ++s_used[b];
+      const int b = S::TILES == 2 ? tile : int(done & 1);
+      wait(&bars->s_full[b], (S::TILES == 2 ? done : done >> 1) & 1);
       tc_fence_after();
       const int step = S::TILES == 1 || x.both ? i : 2 * i + tile;
       if (x.warp) {
@@ -784,8 +787,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
           const float next_top = fmaxf(top, most - BELOW), down = exp2_fast(top - next_top);
           top = next_top, total *= down;
           if (i > 0) {  // O so far: all products of this tile are complete but for those that wait for this P
-            const int ob = S::TILES == 2 ? tile : b ^ 1;
-            wait(&bars->o_full[ob], (o_used[ob] - 1) & 1);
+            wait_products();
             tc_fence_after();
 #pragma unroll 1
             for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
@@ -821,9 +823,8 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
       }
       __syncwarp();
       if (lane == 0) gvr::mbar_arrive(&bars->p_full[b]);
-      ++o_used[b];
+      ++done;
     }
-    if (S::TILES == 1) buffer = (buffer + x.tasks) & 1;
     steps += x.steps;
     if (x.warp && half == 1) totals[tile * 128 + row] = total;
     begin_segment(x_next);  // meets the other warp; its Q may be laid down: this segment's products with Q are complete
@@ -832,8 +833,7 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     if (x.warp) {
       uint32_t nan = 0;
       if (x.tasks > 0) {
-        const int ob = S::TILES == 2 ? tile : buffer ^ 1;
-        wait(&bars->o_full[ob], (o_used[ob] - 1) & 1);
+        wait_products();
         tc_fence_after();
         nan = *const_cast<volatile uint32_t*>(nans + (segments % S::NAN_SLOTS * S::TILES + tile) * 128 + row);
       }
@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
   const uint32_t q_at = (gvr::smem_u32(dynamic) + 1023) & ~1023u, k_at = q_at + S::TILES * S::Q_BYTES, v_at = k_at + 2 * S::KV_BYTES, raw_at = v_at + S::KV_BYTES;
   const uint8_t* raw = dynamic + (raw_at - gvr::smem_u32(dynamic));
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) gvr::mbar_init(&bars.raw_full[i], 1), gvr::mbar_init(&bars.raw_free[i], 8);
+    for (int i = 0; i < S::STAGES; ++i) gvr::mbar_init(&bars.raw_full[i], 1), gvr::mbar_init(&bars.raw_free[i], 8);
     for (int i = 0; i < 2; ++i) {
       gvr::mbar_init(&bars.k_full[i], 4), gvr::mbar_init(&bars.k_free[i], 1);
       gvr::mbar_init(&bars.v_full[i], 2), gvr::mbar_init(&bars.v_free[i], 1);
