@@ -3,10 +3,10 @@
  * gvr_cache.h: attention of requests that share long prefixes, the attention weight that each cached
  * entry draws, and eviction of the entries that draw least.
  *
- * Entries, cache, block tables, conventions and statuses are those of gvr_cache.h, with two
- * differences: a call enqueues two or three kernels (attend_weights: one), and workspaces, where there are
- * any, are required.  Their content is not kept between calls: calls that can overlap on the GPU, or graphs whose
- * replays can, need one each.
+ * Entries, cache, block tables, conventions and statuses are those of gvr_cache.h, with three differences.  A call
+ * enqueues two or three kernels (attend_weights: one).  A row of the block table has at most 2^31 - 2^16 entries
+ * (table_width * page_size).  Workspaces, where there are any, are required; their content is not kept between calls:
+ * calls that can overlap on the GPU, or graphs whose replays can, need one each.
  */
 #ifndef GVR_LONG_H
 #define GVR_LONG_H
@@ -32,7 +32,7 @@ extern "C" {
  * A request whose rows do not all see the whole prefix, and a request alone in its group, is attended as one in no
  * group.  num_groups 0 to GVR_LONG_MAX_REQUESTS (0: the pointers may be NULL), and as many requests.
  * Result, roundings and everything else are as in attend_decode without indices; next_n times num_heads /
- * num_kv_heads is at most 2^19.
+ * num_kv_heads is at most 2^19, and num_rows times that quotient at most 2^26.
  *   workspace       16-byte aligned, attend_shared_workspace's bytes.
  * Every wait inside the kernel is bounded (0.5 s): should one give up, which is not expected on a healthy GPU, all of
  * out and lse are NaN.
@@ -82,9 +82,9 @@ gvr_status attend_weights(const gvr_cache* cache, const void* q, int64_t q_row_s
  *   counts       int32 [3]: pages taken from free_pages, pages released, requests that were left as they were although n > keep:
  *                those from the first one on that free_pages has no pages for (in order, none later is served), and requests with
  *                an entry on no page.  Their row of kept is -1 alone.
- * 1 <= keep < 2^31 / compress_ratio, 0 <= recent <= keep; num_requests at most GVR_LONG_MAX_REQUESTS, num_requests * table_width and
+ * 1 <= keep < 2^31 / compress_ratio and at most 2^31 - 2^16, 0 <= recent <= keep; num_requests at most GVR_LONG_MAX_REQUESTS, num_requests * table_width and
  * num_requests * keep below 2^31.  free_pages: distinct page numbers not in use.  workspace: 16-byte aligned, cache_evict_workspace's bytes.
- * weights, block_table, kept, new_lens, released and counts must not overlap.
+ * What is written overlaps nothing else that the call reads or writes, but for new_lens, which may be kv_lens.
  */
 gvr_status cache_evict(const gvr_cache* cache, float* weights, int64_t weights_stride, int32_t* block_table,
                        int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int64_t num_requests,

@@ -30,6 +30,7 @@ struct Cut {
   int32_t need;     // pages to take
   int32_t release;  // pages to release
   int32_t state;    // WHOLE: n <= keep; CUT; UNPAGED: an entry lies on no page
+  int32_t entries;  // n  (new_lens may lie over kv_lens)
 };
 enum { WHOLE = 0, CUT = 1, UNPAGED = 2 };
 
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_s
   int32_t* kept = p.kept + int64_t(r) * p.keep;
   if (n <= p.keep) {  // by all CTAs of the cluster alike
     for (int i = rank * SELECT_THREADS + tid; i < p.keep; i += cs * SELECT_THREADS) kept[i] = i < n ? i : -1;
-    if (rank == 0 && tid == 0) p.cuts[r] = {0, 0, 0, WHOLE};
+    if (rank == 0 && tid == 0) p.cuts[r] = {0, 0, 0, WHOLE, n};
     return;
   }
   const int32_t* table = p.table + r * p.table_stride;
@@ -248,8 +249,8 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_s
     // (keep, where the first that goes lies behind: the entries added next are not written into a page that
     // another request may hold)
     const int first = min(int(goes), p.keep) >> p.page_shift;
-    if (lacks) p.cuts[r] = {0, 0, 0, UNPAGED};
-    else p.cuts[r] = {first, pages_of(p.keep, p.page_shift) - first, pages - first, CUT};
+    if (lacks) p.cuts[r] = {0, 0, 0, UNPAGED, n};
+    else p.cuts[r] = {first, pages_of(p.keep, p.page_shift) - first, pages - first, CUT, n};
   }
   if (cs > 1) gvr::cluster_sync();  // no CTA leaves while another reads its shared memory
 }
@@ -273,7 +274,6 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictParams p)
   const int tid = threadIdx.x, r = blockIdx.y, chunk0 = blockIdx.x * p.chunk, chunk1 = min(chunk0 + p.chunk, p.keep);
   begin();
   const Cut cut = p.cuts[r];
-  const int n = entries_of(p, r);
   if (blockIdx.x == 0 && tid == 0 && cut.state == WHOLE) p.new_lens[r] = p.lens[r];
   int64_t before = 0, gone = 0;  // pages that the requests before this one take, and release
   const bool lists = blockIdx.x == 0;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictParams p)
     int64_t taken = 0, back = 0, left = 0, so_far = 0;
     for (int i0 = 0; i0 < p.requests; i0 += MOVE_THREADS) {
       const int i = i0 + tid;
-      const Cut c = i < p.requests ? p.cuts[i] : Cut{0, 0, 0, WHOLE};
+      const Cut c = i < p.requests ? p.cuts[i] : Cut{0, 0, 0, WHOLE, 0};
       int64_t x = c.need;  // inclusive sum over the threads
       const int lane = tid & 31;
 #pragma unroll
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictParams p)
   // weights: this chunk's kept ones, and its share of the zeros behind them
   float* weights = p.weights + r * p.weights_stride;
   for (int i = chunk0 + tid; i < chunk1; i += MOVE_THREADS) weights[i] = p.few[int64_t(r) * p.keep + i];
-  for (int64_t i = int64_t(p.keep) + blockIdx.x * MOVE_THREADS + tid; i < n; i += gridDim.x * MOVE_THREADS) weights[i] = 0.f;
+  for (int64_t i = p.keep + int64_t(blockIdx.x) * MOVE_THREADS + tid; i < cut.entries; i += int64_t(gridDim.x) * MOVE_THREADS) weights[i] = 0.f;
 
   // rows: an entry's rows of all heads lie next to each other
   const int start = max(chunk0, cut.first << p.page_shift), count = chunk1 - start, page_mask = (1 << p.page_shift) - 1;
@@ -381,7 +381,7 @@ extern "C" {
 gvr_status cache_evict_workspace(int64_t num_requests, int32_t keep, size_t* bytes) {
   using namespace gvrc;
   if (!bytes) return GVR_ERR_NULL;
-  if (num_requests < 0 || num_requests > GVR_LONG_MAX_REQUESTS || keep < 1 || (num_requests > 0 && keep > kIntMax / num_requests)) return GVR_ERR_ARG;
+  if (num_requests < 0 || num_requests > GVR_LONG_MAX_REQUESTS || keep < 1 || keep > MAX_ENTRIES || (num_requests > 0 && keep > kIntMax / num_requests)) return GVR_ERR_ARG;
   *bytes = size_t(align16(num_requests * int64_t(sizeof(Cut))) + 2 * align16(num_requests * keep * 4));
   return GVR_OK;
 }
@@ -398,7 +398,7 @@ gvr_status cache_evict(const gvr_cache* cache, float* weights, int64_t weights_s
   const gvr_status w = cache_evict_workspace(num_requests, keep, &least);
   if (w != GVR_OK) return w;
   if (compress_ratio < 1 || keep > kIntMax / compress_ratio || recent < 0 || recent > keep || num_free < 0 || num_free > kIntMax ||
-      max_released < 0 || max_released > kIntMax || table_width < 0 || table_width > kIntMax / cache->page_size ||
+      max_released < 0 || max_released > kIntMax || table_width < 0 || table_width > MAX_ENTRIES / cache->page_size ||
       (num_requests > 0 && table_width > kIntMax / num_requests))
     return GVR_ERR_ARG;
   // the last length is keep * ratio + ratio - 1

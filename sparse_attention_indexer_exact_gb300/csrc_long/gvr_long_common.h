@@ -8,6 +8,9 @@
 
 namespace gvrc {
 
+// Entries of a row of the block table, and of what cache_evict keeps: loops may count past them by a turn in 32 bits.
+constexpr int64_t MAX_ENTRIES = (int64_t(1) << 31) - (1 << 16);
+
 // The arguments that attend_shared and attend_weights have in common, as attend_decode checks them.
 inline gvr_status check_rows(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t dtype,
                              int64_t num_rows, int32_t num_heads, const int32_t* table, int64_t table_stride,
@@ -16,8 +19,8 @@ inline gvr_status check_rows(const gvr_cache* cache, const void* q, int64_t q_ro
   if (s != GVR_OK) return s;
   if ((dtype != GVR_BF16 && dtype != GVR_F16) || num_rows < 0 || num_heads < 1 || num_heads % cache->num_kv_heads != 0 ||
       num_heads > GVR_ATTEND_MAX_HEADS || !std::isfinite(float(double(scale) * cache->k_scale * 1.4426950408889634)) || table_width < 0 ||
-      table_width > kIntMax / cache->page_size || next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N || ratio < 1 ||
-      int64_t(next_n) * (num_heads / cache->num_kv_heads) > (1 << 19) || (num_rows + next_n - 1) / next_n > GVR_LONG_MAX_REQUESTS)
+      table_width > MAX_ENTRIES / cache->page_size || next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N || ratio < 1 ||
+      int64_t(next_n) * (num_heads / cache->num_kv_heads) > (1 << 19) || num_rows > int64_t(GVR_LONG_MAX_REQUESTS) * next_n)
     return GVR_ERR_ARG;
   if (q_row_stride < 0 || q_head_stride < 0 || q_row_stride % 8 != 0 || q_head_stride % 8 != 0 || q_row_stride > kIntMax ||
       q_head_stride > kIntMax || table_stride < table_width || table_stride > kIntMax)

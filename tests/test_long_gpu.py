@@ -321,6 +321,21 @@ def test_evict_outputs_streams_and_graphs(gvr):
         check()
 
 
+def test_evict_writes_lengths_in_place(gvr):
+    """new_lens may be kv_lens: many chunks a request, which all need its old length."""
+    rng = np.random.default_rng(23)
+    lens = [9000, 700, 5001, 12000, 4999]
+    table, spare = paged(rng, lens, 16, extra=5 * 320)
+    cache = rng.integers(0, 256, (int(max(table.max(), spare.max())) + 1, 16, 1, 80), dtype=np.uint8)
+    w = rng.exponential(size=(5, table.shape[1] * 16)).astype(np.float32)
+    want = longcheck.evict(w, cache, table, lens, 1, spare, 5000, 10, 0)
+    cd, td, wd, ld = dev(cache), dev(table), dev(w), dev(np.array(lens, np.int32))
+    kept, new, _, counts = gvr.cache_evict(wd, cd, td, ld, dev(spare), 5000, 10, new_lens=ld)
+    assert new.data_ptr() == ld.data_ptr()
+    for a, b in zip((wd, cd, td, kept, ld, counts), (*want[:5], want[6])):
+        assert np.array_equal(host(a), b)
+
+
 def test_evict_of_no_requests(gvr):
     cache = gvr.cache_alloc(4, 16, 2, 64)
     empty = torch.zeros(0, dtype=torch.int32, device="cuda")
