@@ -19,6 +19,8 @@ struct SharedDevice {
 };
 SharedDevice g_shared_devices[kMaxDevices];
 
+constexpr int64_t MAX_QUERIES = 1 << 26;  // of a KV head: their tiles' numbers share words with flags
+
 // Where everything lies in the workspace.
 struct Layout {
   int64_t plan, sets, joined, cta_set, cta_start, prefix, suffix, bytes;
@@ -83,7 +85,7 @@ gvr_status attend_shared_workspace(int32_t num_kv_heads, int32_t head_dim, int64
   if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || num_kv_heads < 1 || num_kv_heads > 65535 || num_rows < 0 || num_heads < 1 ||
       num_heads % num_kv_heads != 0 || num_heads > GVR_ATTEND_MAX_HEADS || next_n < 1 || next_n > GVR_ATTEND_MAX_NEXT_N ||
       int64_t(next_n) * (num_heads / num_kv_heads) > (1 << 19) || num_groups < 0 || num_groups > GVR_LONG_MAX_REQUESTS ||
-      num_rows > int64_t(GVR_LONG_MAX_REQUESTS) * next_n)
+      num_rows > int64_t(GVR_LONG_MAX_REQUESTS) * next_n || num_rows * (num_heads / num_kv_heads) > MAX_QUERIES)
     return GVR_ERR_ARG;
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) return GVR_ERR_LAUNCH;
@@ -103,7 +105,7 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   const gvr_status s = check_rows(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table, table_stride, table_width,
                                   kv_lens, next_n, compress_ratio, scale);
   if (s != GVR_OK) return s;
-  if (num_groups < 0 || num_groups > GVR_LONG_MAX_REQUESTS) return GVR_ERR_ARG;
+  if (num_groups < 0 || num_groups > GVR_LONG_MAX_REQUESTS || num_rows * (num_heads / cache->num_kv_heads) > MAX_QUERIES) return GVR_ERR_ARG;
   if (num_rows == 0) return GVR_OK;
   if (!out || (num_groups > 0 && (!group_starts || !prefix_entries))) return GVR_ERR_NULL;
   if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(group_starts, 4) || !aligned(prefix_entries, 4)) return GVR_ERR_ALIGN;

@@ -22,6 +22,7 @@
 
 #include "../csrc_cache/gvr_attend.cuh"
 #include "gvr_long_common.h"
+#include "gvr_shares.h"
 #include "gvr_tcgen05.cuh"
 
 namespace gvrc {
@@ -99,9 +100,6 @@ struct SharedShape {
 // ------------------------------------------------------------------------------------------------ the plan
 constexpr int PLAN_THREADS = 1024;
 constexpr int LEAST_WORK = 2;  // tile steps worth a CTA
-constexpr int UNIT_WORK = 4;   // what a unit costs beside its steps (queries, first pages, its piece), in tile steps
-
-__device__ __forceinline__ int unit_work(const Set& s) { return UNIT_WORK + (s.steps << s.both); }
 
 struct Sum2 {
   int work, units;
@@ -194,7 +192,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
     set.units = is ? p.kv_heads * tiles : 0;
     const int first = set.first & -S::N;  // steps begin at multiples of N
     set.steps = is && set.end > set.first ? (set.end - first + S::N - 1) / S::N : 0;
-    const int work = set.steps ? set.units * unit_work(set) : 0;
+    const int work = set.steps ? set.units * unit_work(set.steps, set.both) : 0;
     int at, flag_total;
     int2 total;
     const Sum2 x = plan_scan(work, work > 0, set.units, sums, flags, at, total, flag_total);
@@ -244,7 +242,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
   const int total = before.x, ctas = max(1, min(p.grid, total / LEAST_WORK));
   if (tid == 0) *p.plan = {total, ctas, sets, 0};
   for (int c = tid; c <= ctas; c += PLAN_THREADS) {
-    const int at = range_start(c, ctas, total);
+    const int at = share_start(c, ctas, total);
     p.cta_start[c] = at;
     if (c == ctas) break;
     int lo = 0;
@@ -264,12 +262,6 @@ struct __align__(16) Segment {
   int32_t lo, hi, head, tile;   // KV head, and number of the unit among the set's query tiles
   float* piece;
 };
-
-// The steps before `at` of the work of a unit that begins at `start`: a step of work 2 belongs to where its first half lies.
-__device__ __forceinline__ int step_of(int at, int start, int both, int steps) {
-  const int x = max(at - start - UNIT_WORK, 0);
-  return min(both ? (x + 1) >> 1 : x, steps);
-}
 
 // Waits for the phase with parity `parity` to complete, giving up after 2^30 clocks, half a second.  (In one piece, so that
 // a warp that waits counts as going the same way in all lanes, and what it computes as the same in all of them.)
@@ -364,7 +356,7 @@ __device__ __forceinline__ bool walk(const SharedParams& p, const CUtensorMap* m
         set = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
         if (++next_set < plan.sets) ask();
       }
-      const int work = unit_work(set), unit = (at - set.start) / work, start = set.start + unit * work, to = min(last, start + work);
+      const int work = unit_work(set.steps, set.both), unit = (at - set.start) / work, start = set.start + unit * work, to = min(last, start + work);
       s.lo = step_of(at, start, set.both, set.steps), s.hi = step_of(to, start, set.both, set.steps);
       fresh = unit + 1 == set.units && to == start + work;
       at = to;
@@ -967,9 +959,11 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
   float* sums = factors + most * JOIN_ROWS;                // [most][JOIN_ROWS]
   Listed* list = reinterpret_cast<Listed*>(sums + most * JOIN_ROWS);
   __shared__ float tops[JOIN_ROWS], totals[JOIN_ROWS];
-  const int tid = threadIdx.x, lane = tid & 31, r = blockIdx.x / p.kv_heads, head = blockIdx.x - r * p.kv_heads, members = p.next_n * p.group;
-  const int m0 = blockIdx.y * JOIN_ROWS;
+  const int tid = threadIdx.x, lane = tid & 31, r = blockIdx.x / p.kv_heads, head = blockIdx.x - r * p.kv_heads;
+  // queries of the request (the last one may have fewer rows: their units and pieces end with them)
+  const int members = int(min(int64_t(p.next_n), p.num_rows - int64_t(r) * p.next_n)) * p.group, m0 = blockIdx.y * JOIN_ROWS;
   begin();
+  if (m0 >= members) return;
   const int4 held = *reinterpret_cast<const int4*>(p.plan);
   const Plan plan = {held.x, held.y, held.z, held.w};
   const Joined join = p.joined[r];
@@ -987,9 +981,8 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
       const int tile = (offset + m0) / S::QUERIES + (part == 1);
       if (part == 0) border = (tile + 1) * S::QUERIES - offset;
       if (part != 1 || border < min(m0 + JOIN_ROWS, members)) {
-        const int unit = tile * p.kv_heads + head, work = unit_work(set), start = set.start + unit * work;
-        // the last CTA whose share begins at or before x is ((x + 1) ctas - 1) / total
-        const int c0 = int((int64_t(start + 1) * plan.ctas - 1) / plan.total), c1 = int((int64_t(start + work) * plan.ctas - 1) / plan.total);
+        const int unit = tile * p.kv_heads + head, work = unit_work(set.steps, set.both), start = set.start + unit * work;
+        const int c0 = share_of(start, plan.ctas, plan.total), c1 = share_of(start + work - 1, plan.ctas, plan.total);
         const int rows = part < 2 ? 128 : p.suffix_rows, height = S::TILES * rows;
         const int64_t floats = part < 2 ? S::PIECE : height * (D + 2);
         const int twice = S::TILES == 2 && !set.both;  // even steps in one tile, odd ones in the other
@@ -997,8 +990,8 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
         const int here = (c1 - c0 + 1) << twice;
         for (int x = tid; x < here; x += JOIN_SHARED_THREADS) {
           const int cta = c0 + (x >> twice), second = twice ? x & 1 : 0;
-          const int lo = step_of(range_start(cta, plan.ctas, plan.total), start, set.both, set.steps);
-          const int hi = step_of(range_start(cta + 1, plan.ctas, plan.total), start, set.both, set.steps);
+          const int lo = step_of(share_start(cta, plan.ctas, plan.total), start, set.both, set.steps);
+          const int hi = step_of(share_start(cta + 1, plan.ctas, plan.total), start, set.both, set.steps);
           list[count + x] = {hi - lo > second ? pieces + int64_t(cta) * floats : nullptr, height, offset + m0 - tile * S::QUERIES + second * rows};
         }
         count += here;
@@ -1039,7 +1032,7 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
   // ---- the values
   const int row = tid % JOIN_ROWS, m = m0 + row, d4 = blockIdx.z * (JOIN_WIDTH / 4) + tid / JOIN_ROWS, rel = m / p.group;
   const int64_t row_at = int64_t(r) * p.next_n + rel;
-  if (m >= members || row_at >= p.num_rows) return;
+  if (m >= members) return;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int k0 = 0; k0 < count; k0 += JOIN_AT_ONCE) {
     float4 v[JOIN_AT_ONCE];

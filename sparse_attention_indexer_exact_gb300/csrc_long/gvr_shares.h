@@ -1,0 +1,31 @@
+// gvr_shares.h -- how attend_shared's work is cut into shares: the work of all units lies on one line, which CTAs take
+// equal ranges of.  Plain C++ as well, so that those who walk over a share and those who join its pieces are tested
+// against each other on the host.
+#pragma once
+
+#include "../csrc_cache/gvr_cache_index.h"
+
+namespace gvrc {
+
+// What a unit costs beside its steps (queries, first pages, its piece), in tile steps.  With 2, 4, 7 and 10 the benchmark's
+// batch of long prompts took 210, 175, 182 and 188 us, its small groups 41, 43, 46 and 50 us.
+constexpr int UNIT_WORK = 4;
+
+// The work of a unit of `steps` steps, each taken by one tile or by both.
+GVRC_FN int unit_work(int steps, int both) { return UNIT_WORK + (steps << both); }
+
+// Where share c begins, of `total` work cut into `ctas` shares.
+GVRC_FN int share_start(int c, int ctas, int total) { return int(int64_t(c) * total / ctas); }
+
+// The share that `at` lies in: the last one that begins at or before it.
+GVRC_FN int share_of(int at, int ctas, int total) { return int((int64_t(at + 1) * ctas - 1) / total); }
+
+// The steps before `at` of a unit whose work begins at `start`: a step of work 2 belongs to where its first half lies.
+GVRC_FN int step_of(int at, int start, int both, int steps) {
+  const int x = at - start - UNIT_WORK;
+  if (x <= 0) return 0;
+  const int step = both ? (x + 1) >> 1 : x;
+  return step < steps ? step : steps;
+}
+
+}  // namespace gvrc

@@ -128,6 +128,14 @@ def test_many_queries_a_request(gvr, next_n, group):
     check(gvr, next_n, [(256, [150, 200 + next_n]), (100, [next_n, 300, 131])], group=group, kv_heads=1, dim=128, next_n=next_n, cut_rows=1)
 
 
+@pytest.mark.parametrize("next_n,group,left", [(300, 1, 10), (40, 8, 3), (1000, 1, 1), (130, 2, 129)])
+@pytest.mark.parametrize("dim", [64, 256])
+def test_a_last_request_of_fewer_rows(gvr, next_n, group, left, dim):
+    """Of its query tiles only the first ones exist, alone and behind a prefix."""
+    check(gvr, next_n, [(0, [next_n + 40])], group=group, kv_heads=2, dim=dim, next_n=next_n, cut_rows=next_n - left)
+    check(gvr, next_n, [(100, [next_n + 40, next_n])], group=group, kv_heads=1, dim=dim, next_n=next_n, cut_rows=next_n - left)
+
+
 @pytest.mark.parametrize("ps,cr", [(1, 1), (2, 4), (64, 4), (1024, 1), (4096, 2)])
 def test_pages_and_ratios(gvr, ps, cr):
     check(gvr, ps, [(130, [5, 60, 300]), (1100, [1, 2])], ps=ps, cr=cr, next_n=2)
