@@ -131,9 +131,10 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
     for (int each : {64, 128, 256}) {
       const SharedInfo& i = shared_kernels(each);
       if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(i.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, i.smem);
-      if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(i.join, cudaFuncAttributeMaxDynamicSharedMemorySize, join_smem(sms));
+      for (const void* join : i.join)
+        if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, join_smem(sms));
       if (d.err == cudaSuccess)
-        d.err = cudaFuncSetAttribute(i.plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (5 * GVR_LONG_MAX_REQUESTS + 1) * 4);
+        d.err = cudaFuncSetAttribute(i.plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (7 * GVR_LONG_MAX_REQUESTS + 1) * 4);
     }
   });
   if (d.err != cudaSuccess) return GVR_ERR_LAUNCH;
@@ -175,12 +176,18 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   CUtensorMap map = {};
   if (p.page_shift >= 3 && p.num_pages > 0 && !tensor_map(cache, k.step, &map)) return GVR_ERR_LAUNCH;
   void* args[] = {&p, &map};
-  const int plan_smem = int(4 * num_groups + 1 + p.requests) * 4;
+  const int plan_smem = int(5 * num_groups + 1 + 2 * p.requests) * 4;
   cudaError_t e = launch(k.plan, dim3(1), PLAN_THREADS, plan_smem, 1, args, stream);
   if (e == cudaSuccess) e = launch(k.kernel, dim3(uint32_t(sms)), k.threads, k.smem, 1, args, stream);
   if (e == cudaSuccess) {
-    const dim3 grid(uint32_t(p.requests) * uint32_t(p.kv_heads), uint32_t((members + JOIN_ROWS - 1) / JOIN_ROWS), uint32_t(dim / JOIN_WIDTH));
-    e = launch(k.join, grid, JOIN_SHARED_THREADS, join_smem(sms), 1, args, stream);
+    const int64_t tasks = int64_t(p.requests) * p.kv_heads, blocks = (members + JOIN_ROWS - 1) / JOIN_ROWS;
+    // A value's pieces are shared out among 4 threads where CTAs are fewer than SMs (640 queries of one KV head behind 131071
+    // entries 65.0 -> 61.5 us, two requests of 700 entries 20.0 -> 19.0; 196 and 216 CTAs took 3 us more), among 16 where
+    // they are very few and the pieces can be many (8 queries of one KV head over 194560 entries 49 -> 40 us; with few pieces 2 us more).
+    const int64_t ctas = tasks * blocks * (dim / join_width(1));
+    const int which = ctas >= sms ? 0 : ctas * 8 < sms && p.capacity >= 64 * k.step ? 2 : 1, split = 1 << (2 * which);
+    const dim3 grid(uint32_t(tasks), uint32_t(blocks), uint32_t(dim / join_width(split)));
+    e = launch(k.join[which], grid, JOIN_SHARED_THREADS, join_smem(sms), 1, args, stream);
   }
   return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
 }

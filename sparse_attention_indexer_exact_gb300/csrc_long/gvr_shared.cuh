@@ -16,6 +16,8 @@
 // tile take S, two threads a query, each half of the step's entries, and write P, in f16, over it; P is read from there as an
 // operand.  Two tiles take turns: while one's P is made, the other's products run.  Where a unit
 // has up to 128 queries both tiles hold them, one taking the even steps, one the odd ones.
+// The joining kernel is not let start early: its CTAs, few of which read most, would gather on the SMs that are through first
+// (66 us became 80 where 128 queries share 131071 entries).
 #pragma once
 
 #include <cuda.h>
@@ -32,7 +34,7 @@ struct Set {
   int32_t start;    // work before it, in tile steps
   int32_t steps;    // of N entries, of each unit
   int32_t units;    // KV heads x query tiles
-  int32_t both;     // each step is taken by both tiles (more than 128 queries)
+  int32_t full;     // of them those of more than 128 queries, the first ones: both tiles take each step
   int32_t first;    // entries [first, end)
   int32_t end;
   int32_t request;  // whose block table
@@ -139,17 +141,21 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
   int* from = plan_smem;              // [groups + 1]: first request of each group, non-decreasing
   int* sharing = from + p.groups + 1;  // [groups]: requests that share the prefix; later the group's set
   int* lead = sharing + p.groups;     // [groups]: the first of them
-  int* starts = lead + p.groups;      // [groups + requests]: of the sets that have work
+  int* prefixes = lead + p.groups;    // [groups]
+  int* lens = prefixes + p.groups;    // [requests]
+  int* starts = lens + p.requests;    // [groups + requests]: of the sets that have work
   __shared__ int2 sums[32];
   __shared__ int flags[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   begin();
   let_next_start();  // its CTAs, one an SM, set up meanwhile
+  for (int r = tid; r < p.requests; r += PLAN_THREADS) lens[r] = p.lens[r];  // all reads on their way at once
   // groups begin where their start says, but not before the one before them
   int most = 0;
   for (int i0 = 0; i0 <= p.groups && p.groups > 0; i0 += PLAN_THREADS) {
     const int i = i0 + tid;
     int x = i <= p.groups ? min(max(p.group_starts[i], 0), p.requests) : 0;
+    const int prefix = i < p.groups ? min(max(p.prefix_entries[i], 0), p.capacity) : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -162,10 +168,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
     x = max(x, most);
     for (int w = 0; w < 32; ++w) most = max(most, flags[w]);
     if (i <= p.groups) from[i] = x;
-    if (i < p.groups) sharing[i] = 0, lead[i] = p.requests;
+    if (i < p.groups) sharing[i] = 0, lead[i] = p.requests, prefixes[i] = prefix;
   }
   __syncthreads();
-  auto prefix_of = [&](int g) { return min(max(p.prefix_entries[g], 0), p.capacity); };
   // the group whose prefix all rows of request r see, -1: none
   auto group_of = [&](int r, int kv) {
     if (p.groups == 0 || r < from[0] || r >= from[p.groups]) return -1;
@@ -174,11 +179,11 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
       const int mid = (lo + hi) >> 1;
       if (from[mid] <= r) lo = mid; else hi = mid;
     }
-    const int prefix = prefix_of(lo);
+    const int prefix = prefixes[lo];
     return prefix > 0 && decode_entries(kv, p.next_n, 0, p.ratio, p.capacity) >= prefix ? lo : -1;
   };
   for (int r = tid; r < p.requests; r += PLAN_THREADS) {
-    const int g = group_of(r, p.lens[r]);
+    const int g = group_of(r, lens[r]);
     if (g >= 0) atomicAdd(&sharing[g], 1), atomicMin(&lead[g], r);
   }
   __syncthreads();
@@ -188,11 +193,11 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
   // `set` with all but its sums: takes its place if it has work; returns the place or -1
   auto place = [&](bool is, Set set) -> int {
     const int tiles = (set.queries + S::QUERIES - 1) / S::QUERIES;
-    set.both = S::TILES == 2 && set.queries > 128;
     set.units = is ? p.kv_heads * tiles : 0;
+    set.full = S::TILES == 2 && is ? p.kv_heads * ((set.queries + 127) / S::QUERIES) : 0;
     const int first = set.first & -S::N;  // steps begin at multiples of N
     set.steps = is && set.end > set.first ? (set.end - first + S::N - 1) / S::N : 0;
-    const int work = set.steps ? set.units * unit_work(set.steps, set.both) : 0;
+    const int work = set.steps ? unit_start(set.units, set.full, set.steps) : 0;
     int at, flag_total;
     int2 total;
     const Sum2 x = plan_scan(work, work > 0, set.units, sums, flags, at, total, flag_total);
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
     const bool is = g < p.groups && sharing[g] >= 2;
     set.kv = -1;
     if (is) {
-      set.end = prefix_of(g);
+      set.end = prefixes[g];
       set.request = lead[g];
       set.row0 = from[g] * p.next_n;
       set.queries = int(min(int64_t(from[g + 1]) * p.next_n, p.num_rows) - set.row0) * p.group;
@@ -225,11 +230,11 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
     Set set = {};
     Joined join = {-1, -1};
     if (r < p.requests) {
-      set.kv = max(p.lens[r], 0);
-      const int g = group_of(r, p.lens[r]);
+      set.kv = max(lens[r], 0);
+      const int g = group_of(r, lens[r]);
       join.prefix = g < 0 ? -1 : sharing[g];
-      set.first = join.prefix < 0 ? 0 : prefix_of(g);
-      set.end = decode_entries(p.lens[r], p.next_n, p.next_n - 1, p.ratio, p.capacity);
+      set.first = join.prefix < 0 ? 0 : prefixes[g];
+      set.end = decode_entries(lens[r], p.next_n, p.next_n - 1, p.ratio, p.capacity);
       set.request = r;
       set.row0 = r * p.next_n;
       set.queries = int(min(int64_t(p.next_n), p.num_rows - set.row0)) * p.group;
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
 // A CTA's part of a unit: steps [lo, hi) of its set's; 0 steps: no more.
 struct __align__(16) Segment {
   int32_t first, end, kv;       // entry of the first step; the set's last entry, and its length (-1: a prefix)
-  int32_t row0, queries, both;  // of the set
+  int32_t row0, queries, both;  // of the set; whether both tiles take each step
   int32_t lo, hi, head, tile;   // KV head, and number of the unit among the set's query tiles
   float* piece;
 };
@@ -306,7 +311,7 @@ struct SharedBars {
 struct __align__(16) StepNote {
   uint32_t there[4];  // which of its entries exist
   int border;         // its first entry if some rows of its unit do not see all of it, else -1; -2: no more steps
-  int set, where;     // of a border step: its set; its query tile << 12 | tiles' numbers of segments << 8, 4 | parity in the segment
+  int set, where;     // of a border step: its set; its query tile << 12 | tiles' numbers of segments << 8, 4 | both tiles take it << 1 | parity in the segment
   int pad;
 };
 
@@ -356,14 +361,15 @@ __device__ __forceinline__ bool walk(const SharedParams& p, const CUtensorMap* m
         set = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
         if (++next_set < plan.sets) ask();
       }
-      const int work = unit_work(set.steps, set.both), unit = (at - set.start) / work, start = set.start + unit * work, to = min(last, start + work);
-      s.lo = step_of(at, start, set.both, set.steps), s.hi = step_of(to, start, set.both, set.steps);
-      fresh = unit + 1 == set.units && to == start + work;
+      const int unit = unit_at(at - set.start, set.full, set.steps), both = unit < set.full;
+      const int start = set.start + unit_start(unit, set.full, set.steps), end = start + unit_work(set.steps, both), to = min(last, end);
+      s.lo = step_of(at, start, both, set.steps), s.hi = step_of(to, start, both, set.steps);
+      fresh = unit + 1 == set.units && to == end;
       at = to;
       if (s.hi <= s.lo) continue;
       s.end = set.end, s.kv = set.kv;
       s.first = (set.first & -S::N) + s.lo * S::N;
-      s.row0 = set.row0, s.queries = set.queries, s.both = set.both;
+      s.row0 = set.row0, s.queries = set.queries, s.both = both;
       s.tile = unit / p.kv_heads;
       s.head = unit - s.tile * p.kv_heads;
       const int64_t piece = int(blockIdx.x) + set.unit0 + unit;
@@ -378,7 +384,7 @@ __device__ __forceinline__ bool walk(const SharedParams& p, const CUtensorMap* m
     }
     const int left = s.hi - s.lo;
     const int sure = set.kv < 0 ? set.end : decode_entries(set.kv, p.next_n, 0, p.ratio, p.capacity);
-    const int where = s.tile << 12 | int((count - first_only) % S::NAN_SLOTS) << 8 | int(count % S::NAN_SLOTS) << 4;
+    const int where = s.tile << 12 | int((count - first_only) % S::NAN_SLOTS) << 8 | int(count % S::NAN_SLOTS) << 4 | s.both << 1;
     first_only += left == 1 && !s.both;
     const int32_t* table = p.table + set.request * p.table_stride;
     const int x = s.head * (S::RB / 4);  // in words
@@ -446,10 +452,11 @@ __device__ __noinline__ void note_nan(const Set* set, int next_n, int group, int
   using S = SharedShape<D>;
   const Set of = *set;
   for (int t = 0; t < S::TILES; ++t) {
-    if (!of.both && S::TILES == 2 && t != (where & 1)) continue;
+    const bool both = where >> 1 & 1;
+    if (!both && S::TILES == 2 && t != (where & 1)) continue;
     const int slot = where >> (t ? 8 : 4) & 15;
     for (int x = 0; x < 128; ++x) {
-      const int m = (where >> 12) * S::QUERIES + (of.both ? 128 * t : 0) + x;
+      const int m = (where >> 12) * S::QUERIES + (both ? 128 * t : 0) + x;
       const int seen = of.kv < 0 ? of.end : decode_entries(of.kv, next_n, m / group, ratio, capacity);
       if (m < of.queries && seen > e) atomicOr(&nans[(slot * S::TILES + t) * 128 + x], blocks);
     }
@@ -933,9 +940,9 @@ __global__ void __launch_bounds__(SharedShape<D>::THREADS, 1) shared_kernel(Shar
 }
 
 // ------------------------------------------------------------------------------------------------ the join
-constexpr int JOIN_ROWS = 16, JOIN_SHARED_THREADS = 256;         // queries and threads of a CTA
-constexpr int JOIN_WIDTH = JOIN_SHARED_THREADS / JOIN_ROWS * 4;  // its dimensions
-constexpr int JOIN_AT_ONCE = 8;                                  // pieces under way
+constexpr int JOIN_ROWS = 16, JOIN_SHARED_THREADS = 256;  // queries and threads of a CTA
+constexpr int JOIN_AT_ONCE = 8;                           // pieces under way
+__host__ __device__ constexpr int join_width(int split) { return JOIN_SHARED_THREADS / JOIN_ROWS / split * 4; }  // dimensions of a CTA
 
 // A piece, for the CTA's queries.
 struct Listed {
@@ -947,10 +954,10 @@ struct Listed {
 __host__ __device__ constexpr int join_pieces(int grid) { return 2 * (grid + 3); }
 __host__ __device__ constexpr int join_smem(int grid) { return join_pieces(grid) * (JOIN_ROWS * 8 + int(sizeof(Listed))); }
 
-// blockIdx.x: requests x KV heads; y: JOIN_ROWS of the request's queries; z: JOIN_WIDTH dimensions, four a thread.  Neighbouring
+// blockIdx.x: requests x KV heads; y: JOIN_ROWS of the request's queries; z: dimensions, four a thread.  Neighbouring
 // threads have neighbouring queries, as they lie in a piece.  The pieces of the CTA's queries are listed first, and each one's
-// factor found, once for all dimensions; then a thread adds up its values, JOIN_AT_ONCE loads under way.
-template <int D>
+// factor found, once for all dimensions; then a thread adds up its values of every SPLIT-th piece, JOIN_AT_ONCE loads under way.
+template <int D, int SPLIT>
 __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(SharedParams p) {
   using S = SharedShape<D>;
   extern __shared__ __align__(16) uint8_t join_memory[];
@@ -959,6 +966,7 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
   float* sums = factors + most * JOIN_ROWS;                // [most][JOIN_ROWS]
   Listed* list = reinterpret_cast<Listed*>(sums + most * JOIN_ROWS);
   __shared__ float tops[JOIN_ROWS], totals[JOIN_ROWS];
+  __shared__ float4 parts[SPLIT == 1 ? 1 : JOIN_SHARED_THREADS];
   const int tid = threadIdx.x, lane = tid & 31, r = blockIdx.x / p.kv_heads, head = blockIdx.x - r * p.kv_heads;
   // queries of the request (the last one may have fewer rows: their units and pieces end with them)
   const int members = int(min(int64_t(p.next_n), p.num_rows - int64_t(r) * p.next_n)) * p.group, m0 = blockIdx.y * JOIN_ROWS;
@@ -981,17 +989,18 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
       const int tile = (offset + m0) / S::QUERIES + (part == 1);
       if (part == 0) border = (tile + 1) * S::QUERIES - offset;
       if (part != 1 || border < min(m0 + JOIN_ROWS, members)) {
-        const int unit = tile * p.kv_heads + head, work = unit_work(set.steps, set.both), start = set.start + unit * work;
+        const int unit = tile * p.kv_heads + head, both = unit < set.full;
+        const int start = set.start + unit_start(unit, set.full, set.steps), work = unit_work(set.steps, both);
         const int c0 = share_of(start, plan.ctas, plan.total), c1 = share_of(start + work - 1, plan.ctas, plan.total);
         const int rows = part < 2 ? 128 : p.suffix_rows, height = S::TILES * rows;
         const int64_t floats = part < 2 ? S::PIECE : height * (D + 2);
-        const int twice = S::TILES == 2 && !set.both;  // even steps in one tile, odd ones in the other
+        const int twice = S::TILES == 2 && !both;  // even steps in one tile, odd ones in the other
         const float* pieces = (part < 2 ? p.prefix_pieces : p.suffix_pieces) + int64_t(set.unit0 + unit) * floats;
         const int here = (c1 - c0 + 1) << twice;
         for (int x = tid; x < here; x += JOIN_SHARED_THREADS) {
           const int cta = c0 + (x >> twice), second = twice ? x & 1 : 0;
-          const int lo = step_of(share_start(cta, plan.ctas, plan.total), start, set.both, set.steps);
-          const int hi = step_of(share_start(cta + 1, plan.ctas, plan.total), start, set.both, set.steps);
+          const int lo = step_of(share_start(cta, plan.ctas, plan.total), start, both, set.steps);
+          const int hi = step_of(share_start(cta + 1, plan.ctas, plan.total), start, both, set.steps);
           list[count + x] = {hi - lo > second ? pieces + int64_t(cta) * floats : nullptr, height, offset + m0 - tile * S::QUERIES + second * rows};
         }
         count += here;
@@ -1000,15 +1009,22 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
     ends[part] = count;
   }
   __syncthreads();
-  for (int i = tid; i < count * JOIN_ROWS; i += JOIN_SHARED_THREADS) {
-    const int k = i / JOIN_ROWS, row = i % JOIN_ROWS, m = m0 + row;
-    const bool own = m < members && (k >= ends[1] || (k >= ends[0]) == (m >= border));
-    float top = NO_TOP, sum = 0.f;
-    if (own && list[k].piece) {
-      const float* at = list[k].piece + int64_t(list[k].height) * D + list[k].at + row;
-      top = at[0], sum = at[list[k].height];
+  for (int i0 = tid; i0 < count * JOIN_ROWS; i0 += JOIN_AT_ONCE * JOIN_SHARED_THREADS) {
+    float top[JOIN_AT_ONCE], sum[JOIN_AT_ONCE];
+#pragma unroll
+    for (int j = 0; j < JOIN_AT_ONCE; ++j) {
+      const int i = i0 + j * JOIN_SHARED_THREADS, k = i / JOIN_ROWS, row = i % JOIN_ROWS, m = m0 + row;
+      top[j] = NO_TOP, sum[j] = 0.f;
+      if (k < count && m < members && (k >= ends[1] || (k >= ends[0]) == (m >= border)) && list[k].piece) {
+        const float* at = list[k].piece + int64_t(list[k].height) * D + list[k].at + row;
+        top[j] = at[0], sum[j] = at[list[k].height];
+      }
     }
-    factors[i] = top, sums[i] = sum;
+#pragma unroll
+    for (int j = 0; j < JOIN_AT_ONCE; ++j) {
+      const int i = i0 + j * JOIN_SHARED_THREADS;
+      if (i < count * JOIN_ROWS) factors[i] = top[j], sums[i] = sum[j];
+    }
   }
   __syncthreads();
   // ---- each query's base, factors and sum, by a warp, two queries each
@@ -1030,18 +1046,18 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
   }
   __syncthreads();
   // ---- the values
-  const int row = tid % JOIN_ROWS, m = m0 + row, d4 = blockIdx.z * (JOIN_WIDTH / 4) + tid / JOIN_ROWS, rel = m / p.group;
-  const int64_t row_at = int64_t(r) * p.next_n + rel;
-  if (m >= members) return;
+  constexpr int WIDTH4 = join_width(SPLIT) / 4;
+  const int row = tid % JOIN_ROWS, m = m0 + row, d4 = blockIdx.z * WIDTH4 + tid / JOIN_ROWS % WIDTH4, first = tid / (JOIN_ROWS * WIDTH4);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < count; k0 += JOIN_AT_ONCE) {
+  for (int k0 = first; k0 < count; k0 += SPLIT * JOIN_AT_ONCE) {
     float4 v[JOIN_AT_ONCE];
     float f[JOIN_AT_ONCE];
 #pragma unroll
     for (int i = 0; i < JOIN_AT_ONCE; ++i) {
-      f[i] = k0 + i < count ? factors[(k0 + i) * JOIN_ROWS + row] : -1.f;
+      const int k = k0 + i * SPLIT;
+      f[i] = k < count ? factors[k * JOIN_ROWS + row] : -1.f;  // (a query behind the last one has none)
       if (f[i] >= 0.f) {
-        const Listed l = list[k0 + i];
+        const Listed l = list[k];
         v[i] = *reinterpret_cast<const float4*>(l.piece + (int64_t(d4) * l.height + l.at + row) * 4);
       }
     }
@@ -1049,6 +1065,19 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
     for (int i = 0; i < JOIN_AT_ONCE; ++i)
       if (f[i] >= 0.f) acc[0] += f[i] * v[i].x, acc[1] += f[i] * v[i].y, acc[2] += f[i] * v[i].z, acc[3] += f[i] * v[i].w;
   }
+  if (SPLIT > 1) {
+    parts[tid] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    if (first > 0) return;
+#pragma unroll
+    for (int i = 1; i < SPLIT; ++i) {
+      const float4 v = parts[tid + i * (JOIN_ROWS * WIDTH4)];
+      acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
+    }
+  }
+  if (m >= members) return;
+  const int rel = m / p.group;
+  const int64_t row_at = int64_t(r) * p.next_n + rel;
   const float total = plan.failed ? NAN : totals[row], norm = total == 0.f ? 0.f : 1.f / total;
   uint32_t packed[2];
 #pragma unroll
@@ -1065,14 +1094,15 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
 
 // What the host needs to know of a head dimension's kernels.
 struct SharedInfo {
-  const void *plan, *kernel, *join;
+  const void *plan, *kernel, *join[3];  // joins: of split 1, 4 and 16
   int threads, smem, queries, tiles, step, piece_floats;
 };
 template <int D>
 SharedInfo shared_info() {
   using S = SharedShape<D>;
   return {reinterpret_cast<const void*>(shared_plan_kernel<D>), reinterpret_cast<const void*>(shared_kernel<D>),
-          reinterpret_cast<const void*>(shared_join_kernel<D>), S::THREADS, S::SMEM, S::QUERIES, S::TILES, S::N, S::PIECE};
+          {reinterpret_cast<const void*>(shared_join_kernel<D, 1>), reinterpret_cast<const void*>(shared_join_kernel<D, 4>),
+           reinterpret_cast<const void*>(shared_join_kernel<D, 16>)}, S::THREADS, S::SMEM, S::QUERIES, S::TILES, S::N, S::PIECE};
 }
 SharedInfo shared_64();
 SharedInfo shared_128();

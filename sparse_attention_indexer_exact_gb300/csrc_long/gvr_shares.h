@@ -14,6 +14,17 @@ constexpr int UNIT_WORK = 4;
 // The work of a unit of `steps` steps, each taken by one tile or by both.
 GVRC_FN int unit_work(int steps, int both) { return UNIT_WORK + (steps << both); }
 
+// Of a set's units, whose steps are as many, the first `full` are taken by both tiles.  Where a unit begins in the set's work,
+// and the unit that lies at a place of it.
+GVRC_FN int unit_start(int unit, int full, int steps) {
+  const int wide = unit < full ? unit : full;
+  return wide * unit_work(steps, 1) + (unit - wide) * unit_work(steps, 0);
+}
+GVRC_FN int unit_at(int at, int full, int steps) {
+  const int wide = full * unit_work(steps, 1);
+  return at < wide ? at / unit_work(steps, 1) : full + (at - wide) / unit_work(steps, 0);
+}
+
 // Where share c begins, of `total` work cut into `ctas` shares.
 GVRC_FN int share_start(int c, int ctas, int total) { return int(int64_t(c) * total / ctas); }
 

@@ -147,11 +147,21 @@ def test_every_kernel_waits_for_the_one_before_it():
 
 SHARES = r"""
 #include <cstdio>
+#include <initializer_list>
 #include "gvr_shares.h"
 using namespace gvrc;
 int main() {
   // lines: steps, both of each unit, then -1 and the CTAs.  Walks every share as the kernel does, and joins as it does.
   int steps[4096], both[4096], start[4097], n = 0, ctas;
+  for (int units = 1; units < 7; ++units)  // of a set: its units one behind the other
+    for (int full = 0; full <= units; ++full)
+      for (int s : {1, 2, 5, 70})
+        for (int u = 0, at = 0; u < units; ++u) {
+          if (unit_start(u, full, s) != at) return 2;
+          for (int end = at + unit_work(s, u < full); at < end; ++at)
+            if (unit_at(at, full, s) != u) return 3;
+          if (u + 1 == units && unit_start(units, full, s) != at) return 4;
+        }
   while (std::scanf("%d", &steps[n]) == 1) {
     if (steps[n] >= 0) { if (std::scanf("%d", &both[n]) != 1) return 1; ++n; continue; }
     if (std::scanf("%d", &ctas) != 1) return 1;

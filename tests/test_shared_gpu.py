@@ -128,6 +128,13 @@ def test_many_queries_a_request(gvr, next_n, group):
     check(gvr, next_n, [(256, [150, 200 + next_n]), (100, [next_n, 300, 131])], group=group, kv_heads=1, dim=128, next_n=next_n, cut_rows=1)
 
 
+def test_most_requests_and_groups(gvr):
+    """8192 of both: what the plan holds in shared memory at most."""
+    groups = [(2, [1, 2])] * 2000 + [(1, [0])] * 4192
+    check(gvr, 31, groups, dim=64, group=1, kv_heads=1, ps=2, given=(list(range(0, 4002, 2)) + list(range(4001, 8193)) + [8192] * 2000,
+                                                                       [2] * 2000 + [1] * 4192 + [5] * 2000))
+
+
 @pytest.mark.parametrize("next_n,group,left", [(300, 1, 10), (40, 8, 3), (1000, 1, 1), (130, 2, 129)])
 @pytest.mark.parametrize("dim", [64, 256])
 def test_a_last_request_of_fewer_rows(gvr, next_n, group, left, dim):
@@ -194,6 +201,19 @@ def test_nan_stays_with_those_who_see_it(gvr, dim):
         check(gvr, 7, [(prefix, [40, 31, 77, 128]), (100, [29, 41])], dim=dim, next_n=4, change=change)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [70, 96, 130])
+def test_nan_with_more_queries_than_two_tiles(gvr, dim, group):
+    """Queries that fill tiles and those left over, in steps of either kind."""
+    def change(cache, table, kv, starts, prefixes):
+        ps = cache.shape[1]
+        for r, back in ((0, 2), (1, 1)):
+            e = kv[r] - back  # seen by the last rows of four
+            cache[table[r, e // ps], e % ps, 0, dim + dim // 16 + 2] = 127
+
+    check(gvr, 17, [(300, [140, 31])], dim=dim, next_n=4, group=group, kv_heads=1, change=change)
+
+
 def test_nan_in_a_prefix_is_seen_by_all(gvr):
     def change(cache, table, kv, starts, prefixes):
         cache[table[0, 2], 5, 1, 128 + 8 + 3] = 127
@@ -229,6 +249,13 @@ def test_long_prefixes(gvr, dim, kv_heads, requests, prefix):
     """More steps than the device's SMs: units are cut within and between them."""
     rng = np.random.default_rng(12)
     check(gvr, 12, [(prefix, [int(x) for x in rng.integers(1, 90, requests)]), (prefix // 3, [4, 200])], dim=dim, kv_heads=kv_heads, group=2, ps=64)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("requests,next_n,cut_rows", [(2, 1, 0), (3, 3, 2)])
+def test_few_queries_of_many_pieces(gvr, dim, requests, next_n, cut_rows):
+    """Values whose pieces many threads join, beside short requests that have few."""
+    check(gvr, 16, [(20000, [17] * requests), (0, [3])], dim=dim, kv_heads=1, group=2, next_n=next_n, cut_rows=cut_rows)
 
 
 def test_many_requests(gvr):
