@@ -3,11 +3,17 @@
 //
 // Two kernels.  The first, a cluster of CTAs a request, finds the M = keep - recent heaviest of the n - recent older
 // entries: an exact radix selection over order-preserving 32-bit keys, three digits of 11, 11 and 10 bits from the top, each
-// from a histogram in shared memory that the cluster adds up; the keys stay in shared memory after the first pass.  Then one
+// from a histogram in shared memory that the cluster adds up, until all of the crossing bin stays; the keys stay in shared memory
+// after the first pass.  Then one
 // ordered pass writes the chosen entries' numbers, slots and weights: a position is the number of chosen entries
 // before it, so the result does not depend on the order of execution.  The second kernel, CTAs over all requests' new
 // entries, copies rows into the new pages and rewrites weights, tables and lists.  Nothing is moved in place: old pages
 // are only read, so copies need no order among each other, and pages that other requests hold stay what they are.
+//
+// What bounds them.  64 requests of up to 5200 entries cut to 4096 (8 heads of 128): 85 to 90 us, of which 67 copy 490 MB in and out
+// at 5.7 TB/s under the profiler (0.85 of the copy rate back to back); the selection's 16 are a chain of barriers, cluster
+// round trips and scans.  One request of 9000: 25 us, 15 and 8.  Five of up to 131072 cut to 20000: 55 to 59, 31 and 23
+// (eight CTAs a request hold 16384 keys each; 40 us before the cluster's histograms were read at once).
 #include <algorithm>
 #include <mutex>
 
@@ -88,14 +94,13 @@ __device__ __forceinline__ uint2 scan_before(uint2 v, uint2* sums, uint2& total)
   return make_uint2(x.x - v.x + (warp ? bx : 0), x.y - v.y + (warp ? by : 0));
 }
 
-// Bound by its chain of barriers and round trips, not by its bytes: 16 us for 64 requests of up to 5200 entries.
 template <int SELECT_THREADS>
 __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_select_kernel(EvictParams p) {
   constexpr int WARPS = SELECT_THREADS / 32, OWN = BINS / SELECT_THREADS;  // bins of a thread
   extern __shared__ __align__(16) uint32_t keys[];  // [min(slice, MAX_KEYS)]
   __shared__ __align__(16) uint32_t hist[3][BINS];
   __shared__ uint2 sums[32];
-  __shared__ uint32_t found[2];    // the crossing bin, and what is still wanted of it
+  __shared__ uint32_t found[3];    // the crossing bin, what is still wanted of it, and what it holds
   __shared__ uint32_t mine_of[4];  // of this CTA: entries above the threshold, equal to it; first entry that goes; a missing page
   const int tid = threadIdx.x;
   const int rank = int(gvr::cluster_rank()), cs = int(gvr::cluster_size()), r = int(cs == 1 ? blockIdx.x : gvr::cluster_id_x());
@@ -124,6 +129,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_s
 
   // ---- the threshold: the want-th largest key, digit by digit
   uint32_t prefix = 0;  // digits found
+  int drop = 0;         // bits below them, which do not matter
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t mask = pass == 2 ? 1023 : 2047;
@@ -165,16 +171,17 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_s
     uint32_t above = scan_before<WARPS>(make_uint2(sum, 0), sums, total).x;
 #pragma unroll
     for (int j = OWN - 1; j >= 0; --j) {
-      if (above < want && want <= above + own[j]) found[0] = bin + j, found[1] = want - above;
+      if (above < want && want <= above + own[j]) found[0] = bin + j, found[1] = want - above, found[2] = own[j];
       above += own[j];
     }
-    if (tid == 0 && want == 0) found[0] = 0, found[1] = 0;  // nothing is wanted, whatever the threshold
+    if (tid == 0 && want == 0) found[0] = found[1] = found[2] = 0;  // nothing is wanted, whatever the threshold
     __syncthreads();
     prefix = pass == 0 ? found[0] : prefix << (pass == 1 ? 11 : 10) | found[0];
-    want = found[1];
-    __syncthreads();  // both are read before the next pass finds its own
+    want = found[1], drop = shift;
+    if (want == found[2]) break;  // all of the bin stays
+    __syncthreads();  // they are read before the next pass finds its own
   }
-  const uint32_t threshold = prefix, ties = want;  // `ties` entries that equal the threshold stay, those with the lowest numbers
+  const uint32_t threshold = prefix, ties = want;  // `ties` entries that equal it stay, those with the lowest numbers
   const bool none = p.keep == p.recent;
 
   // ---- what lies in the CTAs before this one
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_s
   {
     uint2 own = make_uint2(0, 0);
     for (int i = from + tid; i < old_to; i += SELECT_THREADS) {
-      const uint32_t k = key_at(i);
+      const uint32_t k = key_at(i) >> drop;
       own.x += k > threshold, own.y += k == threshold;
     }
     scan_before<WARPS>(own, sums, total);
@@ -211,7 +218,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_s
     for (int j = 0; j < 4; ++j) {
       const int i = i0 + 4 * tid + j;
       if (i < old_to) page[j] = table[i >> p.page_shift], weight[j] = weights[i];  // on their way beside the scan
-      const uint32_t k = i < old_to && !none ? key_at(i) : 0;
+      const uint32_t k = i < old_to && !none ? key_at(i) >> drop : 0;
       is[j] = i >= old_to ? 3 : none ? 2 : k > threshold ? 0 : k == threshold ? 1 : 2;
       own.x += is[j] == 0, own.y += is[j] == 1;
     }
