@@ -11,13 +11,28 @@
 //
 // A CTA.  One warp walks over the share: it notes the segments for the others and starts the copies of their rows, a
 // page's rows of a head (up to a step's) a bulk tensor copy.  Four warps expand K and four V (e2m1 times e4m3 is exact
-// in f16), from there into matrix operands in shared memory.  One thread issues the products
+// in f16), from there into matrix operands in shared memory.  One lane of a warp issues the products
 // S = Q K^T and O += P V on the fifth-generation tensor cores, 128 queries a tile: S and O lie in tensor memory.  Eight warps a
 // tile take S, two threads a query, each half of the step's entries, and write P, in f16, over it; P is read from there as an
 // operand.  Two tiles take turns: while one's P is made, the other's products run.  Where a unit
 // has up to 128 queries both tiles hold them, one taking the even steps, one the odd ones.
-// The joining kernel is not let start early: its CTAs, few of which read most, would gather on the SMs that are through first
-// (66 us became 80 where 128 queries share 131071 entries).
+//
+// What bounds it (64 requests of 2 rows behind 32000 entries, 64 heads over 8 of 128: 175 us, 0.40 of the tensor cores' measured
+// rate; the plan takes 5 us of it, the shares 157, the join 12).  A step of a unit of 256 queries takes 2.2 us, of 128 queries
+// 1.25 (head_dim 64: 1.8 and 1.0; 256, 64 entries and 128 queries: 1.25).  No pipe is busy: the tensor pipe 46 %, issue 50 %, the
+// ALU 37 %, FMA 23 %, DRAM 11 %.  What counts is the way of a tile through
+// its step, scores -> maximum -> exponentials -> P -> products -> scores, about 3400 clocks of which the other tile's hide half.
+// Tensor memory has no room for more tiles: at head_dim 128 two times O and S take all of its columns.
+//
+// Tried, with times of that call at their time: a lone thread as issuer instead of a converged warp's elected lane (367 us against 325), loops
+// unrolled (260 against 213: code beyond the instruction caches), counters of barriers in arrays (185 against 175: they
+// lie in memory), copies by warps instead of tensor copies (+8 us), one thread a query (slower), three of eight exponentials by a
+// polynomial (slower), a pass without the maximum of the step (spills), the first scores kept in registers from the
+// maximum's pass to the exponentials' (+2.5), P handed over by halves (+3), V waited for by halves (+4) or quarters (+13), an issuer
+// a tile (+32: their products interleave, and each tile's are through later).  Without exponentials, expansions and
+// maxima, and with one product for eight, 140 of then 194 us were left.  The joining kernel is not let start early: its CTAs, few of
+// which read most, would gather on the SMs that are through first (66 us became 80 where 640 queries of one KV head share
+// 131071 entries).
 #pragma once
 
 #include <cuda.h>
