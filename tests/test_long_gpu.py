@@ -366,3 +366,71 @@ def test_attention_after_eviction(gvr):
     ref = cachecheck.attend(q.double().numpy(), cache, table, lens, range(3), listed, 1 / np.sqrt(dim))
     tol, tol_lse = cachecheck.attend_tolerance(ref, 2.0 ** -7, np.abs(cachecheck.unpack(cache, dim)[1]).max())
     assert (np.abs(out.double().cpu().numpy() - ref[0]) <= tol).all() and (np.abs(host(lse) - ref[1]) <= tol_lse).all()
+
+
+def test_a_run_of_all_three(gvr):
+    """Requests behind a common prompt: attention and what it draws over some steps, eviction, and the prefix that is left of it."""
+    rng = np.random.default_rng(24)
+    prefix, lens, keep, recent, heads, kv_heads, dim, ps, next_n = 150, [260, 190, 333, 177], 160, 30, 8, 2, 64, 16, 2
+    table, spare = paged(rng, lens, ps, extra=60)
+    cache = random_cache(rng, int(max(table.max(), spare.max())) + 1, ps, kv_heads, dim)
+    table[1:, :prefix // ps] = table[0, :prefix // ps]
+    for r in (1, 2, 3):
+        cache[table[r, prefix // ps], :prefix % ps] = cache[table[0, prefix // ps], :prefix % ps]
+    cd, td, ld = dev(cache), dev(table), dev(np.array(lens, np.int32))
+    starts, w = dev(np.array([0, 4], np.int32)), torch.zeros(4, table.shape[1] * ps, device="cuda")
+
+    def step(given, entries, pages, common):
+        q = torch.from_numpy(rng.standard_normal((4 * next_n, heads, dim)).astype(np.float32)).half()
+        out, lse = gvr.attend_shared(q.cuda(), cd, td, given, next_n, 1, starts, dev(np.array([common], np.int32)), want_lse=True)
+        before = host(w).copy()
+        gvr.attend_weights(q.cuda(), cd, td, given, next_n, 1, lse, w)
+        seen = cachecheck.row_entries(entries, next_n, 1, 4 * next_n, pages.shape[1] * ps)
+        now = host(cd)
+        ref = cachecheck.attend(q.double().numpy(), now, pages, seen, [r // next_n for r in range(4 * next_n)], None, 1 / np.sqrt(dim))
+        tol, tol_lse = cachecheck.attend_tolerance(ref, 2.0 ** -10, np.abs(cachecheck.unpack(now, dim)[1]).max())
+        assert (np.abs(out.double().cpu().numpy() - ref[0]) <= tol).all() and (np.abs(host(lse) - ref[1]) <= tol_lse).all()
+        after, off = longcheck.weights(q.double().numpy(), now, pages, entries, next_n, 1, host(lse), 1 / np.sqrt(dim), before)
+        assert (np.abs(host(w) - after) <= off).all()
+
+    for _ in range(3):
+        step(ld, lens, table, prefix)
+    drawn, held = host(w).copy(), table[table >= 0]
+    kept, new, _, counts = gvr.cache_evict(w, cd, td, ld, dev(spare), keep, recent)
+    assert new.tolist() == [keep] * 4 and counts[2] == 0 and np.array_equal(host(cd)[held], cache[held])
+    for r in range(4):
+        assert host(kept)[r].tolist() == longcheck.chosen(drawn[r], lens[r], keep, recent)
+    # entries that all requests kept in the same places
+    same = (host(kept) == host(kept)[0]).all(0) & (host(kept)[0] < prefix)
+    common = int(same.argmin())
+    step(new, [keep] * 4, host(td), common)
+
+
+@pytest.mark.parametrize("ps", [4, 64])
+def test_pages_beyond_32_bits(gvr, ps):
+    """A cache of 5 GB, of which the last pages are read and written."""
+    rng = np.random.default_rng(25)
+    heads, kv_heads, dim, lens, keep, recent = 4, 2, 128, [300, 210], 100, 20
+    table, spare = paged(rng, lens, ps, extra=2 * -(-keep // ps))
+    few = int(max(table.max(), spare.max())) + 1
+    cache = random_cache(rng, few, ps, kv_heads, dim)
+    table[1, :96 // ps] = table[0, :96 // ps]
+    pages = 5 * 2 ** 30 // (ps * kv_heads * 144)
+    first = pages - few
+    assert first * ps * kv_heads * 144 > 2 ** 32
+    big = gvr.cache_alloc(pages, ps, kv_heads, dim)
+    big[first:] = dev(cache)
+    far = np.where(table >= 0, table + first, table)
+    td, ld = dev(far), dev(np.array(lens, np.int32))
+    q = torch.from_numpy(rng.standard_normal((2, heads, dim)).astype(np.float32)).to(torch.bfloat16)
+    groups = dev(np.array([0, 2], np.int32)), dev(np.array([64], np.int32))
+    out, lse = gvr.attend_shared(q.cuda(), big, td, ld, 1, 1, *groups, want_lse=True)
+    near = gvr.attend_shared(q.cuda(), dev(cache), dev(table), ld, 1, 1, *groups, want_lse=True)
+    assert torch.equal(out, near[0]) and torch.equal(lse, near[1])
+    w = gvr.attend_weights(q.cuda(), big, td, ld, 1, 1, lse)
+    assert torch.equal(w, gvr.attend_weights(q.cuda(), dev(cache), dev(table), ld, 1, 1, lse))
+    want = longcheck.evict(host(w), cache, table, lens, 1, spare, keep, recent, 200)
+    kept, new, released, counts = gvr.cache_evict(w, big, td, ld, dev(spare + np.int32(first)), keep, recent, 1, 200)
+    assert np.array_equal(host(kept), want[3]) and np.array_equal(host(big[first:]), want[1]) and np.array_equal(host(counts), want[6])
+    assert np.array_equal(host(td), np.where(want[2] >= 0, want[2] + first, want[2]))
+    assert np.array_equal(host(released), np.where(want[5] >= 0, np.array(want[5]) + first, want[5]))
