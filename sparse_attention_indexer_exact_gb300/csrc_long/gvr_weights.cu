@@ -13,12 +13,14 @@
 // Matrix products by mma.sync, as in gvr_attend.cuh and for its reason: a KV head's queries are few, the 4-bit operand
 // expands in registers straight into that layout.
 //
-// What bounds it.  64 requests of up to 16384 entries, 64 heads over 8 of 128: 116 us cold, 110 to 124 among others.  K is half of a row, but its 64
+// What bounds it.  64 requests of up to 16384 entries, 64 heads over 8 of 128: 111 us, 121 over other inputs each time.  K is half of a row, but its 64
 // bytes of codes and 8 of scales, rows being 144 bytes, touch 17 of 18 blocks of 64 bytes, which is what DRAM gives at least:
-// 598 MB, at 5.2 TB/s (0.77 of the measured copy rate).  16 rows a request of 6 heads over 4 of 64 (19 requests up to 12345
-// entries): 43 to 50 us, products and exponentials.  One row of 8192 entries: 10.5 to 12 us, latency.
+// 598 MB, at 5.2 TB/s under the profiler (0.77 of the measured copy rate).  16 rows a request of 6 heads over 4 of 64 (19 requests up to 12345
+// entries): 34.5 us, no pipe busy (before its last step: issue 47 %, tensor 29 %): a CTA has
+// three turns of its warps, each a chain of copy, expansion, products and exponentials, behind its queries' way into shared memory.  One row of 8192 entries: 9.2 us, latency.
 // Steps of 16 entries for few warps took one row from 14.4 to 11 us; the queries fetched a turn ahead and two chains of products the
-// batch from 113 to 106; no limits where all rows see an entry the 16 rows from 51 to 43.
+// batch from 113 to 106; no limits where all rows see an entry the 16 rows from 51 to 43, requests
+// weighed with what they cost beside their steps from 41 to 36.
 #include <algorithm>
 #include <mutex>
 
@@ -32,6 +34,8 @@ constexpr int WEIGHT_WARPS = 8, WEIGHT_THREADS = 32 * WEIGHT_WARPS;
 constexpr int AHEAD = 3;              // stages of a warp's ring
 constexpr int QUERY_BYTES = 1 << 16;  // of queries in shared memory, at most
 constexpr int MANY = 4;               // steps of 32 entries a warp
+constexpr int REQUEST_WORK = 8;       // what a request costs beside its steps, in steps: its queries, and a last turn of some warps (0, 2, 4, 8, 14:
+                                      // 118, 113, 111, 112, 112 us for 64 requests of one row, 41, 41, 39, 36, 36 for 19 of 16 rows)
 
 struct WeightParams {
   const uint8_t* data;
@@ -78,7 +82,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
   uint4* operands = reinterpret_cast<uint4*>(smem + WEIGHT_WARPS * S::RING);  // [part][D / 32][32 lanes]
   Queries* queries = reinterpret_cast<Queries*>(smem + WEIGHT_WARPS * S::RING + part * S::TILE);  // [part][4]
   int2* limits = reinterpret_cast<int2*>(queries + part * 4);  // [part][4]
-  int* start = reinterpret_cast<int*>(limits + part * 4);  // [requests + 1]: the steps before each request
+  int* start = reinterpret_cast<int*>(limits + part * 4);  // [requests + 1]: the work before each request, in steps
   __shared__ int sums[WEIGHT_WARPS];
 
   begin();
@@ -91,6 +95,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
   for (int r0 = 0; r0 < p.requests; r0 += WEIGHT_THREADS) {
     const int r = r0 + tid;
     int x = r < p.requests ? (entries(r) + STEP - 1) / STEP : 0;
+    if (x > 0) x += REQUEST_WORK;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -124,8 +129,9 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
   const int members = p.next_n * p.group;
   const uint32_t ring_at = gvr::smem_u32(ring);
   for (; at < last; ++request) {
-    const int segment = min(last, start[request + 1]) - at, first = at - start[request];
-    at += max(segment, 0);
+    const int begins = start[request] + REQUEST_WORK, to = min(last, start[request + 1]);
+    const int first = max(at - begins, 0), segment = to - begins - first;
+    at = max(at, to);
     if (segment <= 0) continue;
     const int kv = p.lens[request], n = entries(request), sure = decode_entries(kv, p.next_n, 0, p.ratio, p.capacity);
     const int32_t* table = p.table + request * p.table_stride;
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(WEIGHT_THREADS, 2) weights_kernel(WeightParams
                 for (int j = 0; j < 4; ++j) a[2 * w + j / 2][j % 2 * 2] = hmul2(x[j], x0), a[2 * w + j / 2][j % 2 * 2 + 1] = hmul2(y[j], y0);
               }
               auto add_up = [&](auto bordering) {
-                constexpr int AT_ONCE = D == 64 && !decltype(bordering)::value ? 2 : 1;
+                constexpr int AT_ONCE = D == 64 ? 2 : 1;
 #pragma unroll AT_ONCE
                 for (int t = 0; t < tiles; ++t) {
                   const int tile = h * tiles + t;
@@ -411,7 +417,7 @@ gvr_status attend_weights(const gvr_cache* cache, const void* q, int64_t q_row_s
   p.requests = int32_t((num_rows + next_n - 1) / next_n);
   // steps are counted in 32 bits
   const int64_t halves = (int64_t(p.capacity) + 15) / 16;
-  if (halves * p.requests > kIntMax) return GVR_ERR_ARG;
+  if ((halves + REQUEST_WORK) * p.requests > kIntMax) return GVR_ERR_ARG;
   // steps of 32 entries, or of 16 where a warp has fewer than MANY of those, by the table's width
   const int64_t warps = int64_t(2) * sms * WEIGHT_WARPS;
   const int mt = halves * p.requests < 2 * MANY * warps ? 1 : 2;
