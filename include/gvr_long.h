@@ -4,7 +4,7 @@
  * entry draws, and eviction of the entries that draw least.
  *
  * Entries, cache, block tables, conventions and statuses are those of gvr_cache.h, with three differences.  A call
- * enqueues two or three kernels (attend_weights: one).  A row of the block table has at most 2^31 - 2^16 entries
+ * enqueues up to four kernels (attend_weights: one).  A row of the block table has at most 2^31 - 2^16 entries
  * (table_width * page_size).  Workspaces, where there are any, are required; their content is not kept between calls:
  * calls that can overlap on the GPU, or graphs whose replays can, need one each.
  */
@@ -26,11 +26,12 @@ extern "C" {
  *                   Requests before the first and behind the last are in no group.  A start below one before it
  *                   counts as that one, a negative one as 0, one beyond the requests as their number.
  *   prefix_entries  int32 [num_groups]: the first prefix_entries[g] entries of all requests of the group
- *                   are the same.  The caller vouches for it; they are read through the block table of the
- *                   group's first request that has that many.  (Usually its full pages are the very same pages.  The
- *                   page in which a prefix ends may be each request's own copy.)  Negative counts as 0.
+ *                   are the same.  The caller vouches for it, and each of their block tables has them: they are read through
+ *                   that of one of the requests, or of each.  (Usually full pages are the very same pages.  The page
+ *                   in which a prefix ends may be each request's own copy.)  Negative counts as 0.
  * A request whose rows do not all see the whole prefix, and a request alone in its group, is attended as one in no
  * group.  num_groups 0 to GVR_LONG_MAX_REQUESTS (0: the pointers may be NULL), and as many requests.
+ * Where the block table is so narrow, or the requests so few, that sharing is not expected to pay, attend_decode's kernels run.
  * Result, roundings and everything else are as in attend_decode without indices; next_n times num_heads /
  * num_kv_heads is at most 2^19, and num_rows times that quotient at most 2^26.
  *   workspace       16-byte aligned, attend_shared_workspace's bytes.

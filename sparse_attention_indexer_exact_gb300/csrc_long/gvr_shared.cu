@@ -19,12 +19,17 @@ struct SharedDevice {
 };
 SharedDevice g_shared_devices[kMaxDevices];
 
+// Tails: at most so many entries, as one CTA walks over them, and so many tiles of queries, as each expands them anew; by a kernel
+// of its own, which few requests are not worth.  128 requests over 3200 entries, 2880 of them common: 107 -> 74 us with 8 KV
+// heads of 128 and 4 queries each, 77 -> 50 with 8 of 64 and one; 32 requests over 12800: 69 -> 57; 64 of 2 rows behind 32000, 10 to
+// 2000 of their own: 176 -> 179; 27 requests under 2 KV heads of 256 50 -> 67, were they let.
+constexpr int TAIL_ENTRIES = 2048, TAIL_TILES = 4, LEAST_TAILS = 256;
 constexpr int64_t MAX_QUERIES = 1 << 26;  // of a KV head: their tiles' numbers share words with flags
 
 // Where everything lies in the workspace.
 struct Layout {
-  int64_t plan, sets, joined, cta_set, cta_start, prefix, suffix, bytes;
-  int32_t suffix_rows;
+  int64_t plan, sets, joined, cta_set, cta_start, prefix, suffix, tails, bytes;
+  int32_t suffix_rows, tail_tiles, tail_height;
 };
 
 int64_t align16(int64_t x) { return (x + 15) / 16 * 16; }
@@ -69,8 +74,35 @@ gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group,
   l->cta_start = l->cta_set + align16(grid * 4);
   l->prefix = l->cta_start + align16((grid + 1) * 4);
   l->suffix = l->prefix + (groups > 0 ? (grid + prefix_units) * k.piece_floats * 4 : 0);
-  l->bytes = l->suffix + (grid + suffix_units) * suffix_floats * 4;
+  l->tails = l->suffix + (grid + suffix_units) * suffix_floats * 4;
+  const int32_t tail_queries = k.tails(members).queries;
+  l->tail_tiles = int32_t((members + tail_queries - 1) / tail_queries);
+  if (l->tail_tiles > TAIL_TILES || requests * kv_heads < LEAST_TAILS) l->tail_tiles = 0;
+  l->tail_height = l->tail_tiles * tail_queries;
+  l->bytes = l->tails + align16(requests * kv_heads * l->tail_height * (dim + 2) * 4);
   return GVR_OK;
+}
+
+// Whether attend_decode, which reads each request's entries by themselves, is expected to take less time, by the table's width, as the
+// lengths are on the device.  Measured apart and together: 2 requests of 800 entries (8 KV heads of 128, 4 queries each) 8.5 and
+// 19 us, 32 of 800 14 and 35, 128 of 3200 91 and 72, 32 of 12800 90 and 57; of 2 heads of 256, 32 of 3200 25 and 34, of 12800 64 and 47.
+struct Expected {
+  float rows[3];  // apart: us a million rows, for jobs of 8, 16 and 32 queries
+  float step[2];  // together: us a step of a unit of one tile, of two
+};
+bool better_apart(const SharedInfo& k, int dim, const SharedParams& p, int64_t members, int64_t groups, int sms) {
+  const Expected x = dim == 64    ? Expected{{17.f, 24.f, 38.f}, {1.f, 1.85f}}
+                     : dim == 128 ? Expected{{25.f, 37.f, 37.f}, {1.25f, 2.2f}}
+                                  : Expected{{66.f, 66.f, 66.f}, {1.27f, 1.27f}};
+  const int job = members <= 8 || dim == 256 ? 0 : members <= 16 || dim == 128 ? 1 : 2;  // as attend_decode chooses
+  const int64_t tiles = (members + (8 << job) - 1) / (8 << job);
+  if (p.kv_heads * tiles > 65535) return false;  // attend_decode refuses them
+  const double apart = 8. + 1e-6 * x.rows[job] * double(p.requests) * double(p.kv_heads * tiles) * double(p.capacity);
+  const int64_t sets = groups > 0 ? std::min<int64_t>(groups, p.requests) : p.requests, queries = (p.num_rows * p.group + sets - 1) / sets;
+  const double units = double(sets) * double(p.kv_heads) * double((queries + k.queries - 1) / k.queries);
+  const double steps = double((int64_t(p.capacity) + k.step - 1) / k.step);
+  const double together = 20. + 0.05 * double(p.requests) * double(p.kv_heads) + units * steps * x.step[queries > 128] / sms;
+  return apart <= together;
 }
 
 }  // namespace
@@ -126,6 +158,10 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   const gvr_status fits = layout(k, dim, p.kv_heads, p.group, num_rows, next_n, num_groups, sms, &l);
   if (fits != GVR_OK) return fits;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < size_t(l.bytes)) return GVR_ERR_WORKSPACE;
+  p.num_rows = num_rows;
+  if (better_apart(k, dim, p, members, num_groups, sms))
+    return attend_decode(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table, table_stride, table_width, kv_lens, next_n,
+                         compress_ratio, nullptr, 1, scale, out, lse, workspace, workspace_bytes, stream);
   SharedDevice& d = g_shared_devices[dev];  // sm_count has checked dev
   std::call_once(d.once, [&d, sms]() {
     for (int each : {64, 128, 256}) {
@@ -133,6 +169,10 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
       if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(i.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, i.smem);
       for (const void* join : i.join)
         if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, join_smem(sms));
+      for (int64_t members : {8, 16, 32}) {
+        const TailInfo t = i.tails(members);
+        if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(t.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, t.smem);
+      }
       if (d.err == cudaSuccess)
         d.err = cudaFuncSetAttribute(i.plan, cudaFuncAttributeMaxDynamicSharedMemorySize, (7 * GVR_LONG_MAX_REQUESTS + 1) * 4);
     }
@@ -154,11 +194,13 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   p.cta_start = reinterpret_cast<int32_t*>(ws + l.cta_start);
   p.prefix_pieces = reinterpret_cast<float*>(ws + l.prefix);
   p.suffix_pieces = reinterpret_cast<float*>(ws + l.suffix);
+  p.tail_pieces = reinterpret_cast<float*>(ws + l.tails);
   p.suffix_rows = l.suffix_rows;
+  p.tail_height = l.tail_height;
+  p.tail_entries = l.tail_tiles > 0 ? TAIL_ENTRIES : 0;
   p.q_row = q_row_stride;
   p.q_head = q_head_stride;
   p.table_stride = table_stride;
-  p.num_rows = num_rows;
   p.unit = unit_bytes(cache->page_stride, row);
   p.page_units = uint32_t(cache->page_stride / p.unit);
   p.row_units = row / p.unit;
@@ -178,9 +220,22 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   void* args[] = {&p, &map};
   const int plan_smem = int(5 * num_groups + 1 + 2 * p.requests) * 4;
   cudaError_t e = launch(k.plan, dim3(1), PLAN_THREADS, plan_smem, 1, args, stream);
+  const int64_t tasks = int64_t(p.requests) * p.kv_heads;
+  if (e == cudaSuccess && l.tail_tiles > 0) {
+    AttendParams a = {};
+    a.data = p.data, a.q = q, a.table = block_table, a.lens = kv_lens;
+    a.q_row = p.q_row, a.q_head = p.q_head, a.table_stride = p.table_stride, a.num_rows = p.num_rows;
+    a.unit = p.unit, a.page_units = p.page_units, a.entry_units = p.entry_units, a.row_units = p.row_units;
+    a.num_pages = p.num_pages, a.page_shift = p.page_shift, a.kv_heads = p.kv_heads, a.group = p.group, a.fold = next_n, a.capacity = p.capacity;
+    a.next_n = next_n, a.ratio = p.ratio, a.bf16 = p.bf16, a.scale_log2 = p.scale_log2, a.q_sign = p.q_sign;
+    TailParams t = {p.joined, p.tail_pieces, p.tail_height};
+    void* tail_args[] = {&a, &t};
+    const TailInfo i = k.tails(members);
+    e = launch(i.kernel, dim3(uint32_t(tasks), uint32_t(l.tail_tiles)), i.threads, i.smem, 1, tail_args, stream);
+  }
   if (e == cudaSuccess) e = launch(k.kernel, dim3(uint32_t(sms)), k.threads, k.smem, 1, args, stream);
   if (e == cudaSuccess) {
-    const int64_t tasks = int64_t(p.requests) * p.kv_heads, blocks = (members + JOIN_ROWS - 1) / JOIN_ROWS;
+    const int64_t blocks = (members + JOIN_ROWS - 1) / JOIN_ROWS;
     // A value's pieces are shared out among 4 threads where CTAs are fewer than SMs (640 queries of one KV head behind 131071
     // entries 65.0 -> 61.5 us, two requests of 700 entries 20.0 -> 19.0; 196 and 216 CTAs took 3 us more), among 16 where
     // they are very few and the pieces can be many (8 queries of one KV head over 194560 entries 49 -> 40 us; with few pieces 2 us more).

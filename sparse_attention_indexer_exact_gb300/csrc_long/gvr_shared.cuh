@@ -40,6 +40,7 @@
 #include "../csrc_cache/gvr_attend.cuh"
 #include "gvr_long_common.h"
 #include "gvr_shares.h"
+#include "gvr_tails.cuh"
 #include "gvr_tcgen05.cuh"
 
 namespace gvrc {
@@ -67,12 +68,6 @@ struct Plan {
   int32_t failed;  // a wait gave up
 };
 
-// What a request's rows join.
-struct Joined {
-  int32_t suffix;  // its set, -1: none
-  int32_t prefix;  // its group's, -1: none
-};
-
 struct SharedParams {
   const uint8_t* data;
   const uint16_t* q;
@@ -89,10 +84,12 @@ struct SharedParams {
   int32_t* cta_start;  // [grid + 1]: where it begins
   float* prefix_pieces;
   float* suffix_pieces;
+  float* tail_pieces;
   int64_t q_row, q_head, table_stride, num_rows;
   uint32_t unit, page_units, entry_units, row_units;  // as in AttendParams
   int32_t num_pages, page_shift, kv_heads, group, capacity, next_n, ratio, bf16, requests, groups, grid;
   int32_t suffix_rows;  // rows of a tile in a suffix piece (a multiple of 8)
+  int32_t tail_entries, tail_height;  // requests with at most so many entries behind their prefix have a tail in place of a set (0: none)
   float scale_log2, q_sign, v_scale;
 };
 
@@ -170,7 +167,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
   for (int i0 = 0; i0 <= p.groups && p.groups > 0; i0 += PLAN_THREADS) {
     const int i = i0 + tid;
     int x = i <= p.groups ? min(max(p.group_starts[i], 0), p.requests) : 0;
-    const int prefix = i < p.groups ? min(max(p.prefix_entries[i], 0), p.capacity) : 0;
+    const int prefix = i < p.groups ? min(max(p.prefix_entries[i], 0), p.capacity) & -STEP : 0;  // tails begin where their steps do
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -243,7 +240,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
   for (int r0 = 0; r0 < p.requests; r0 += PLAN_THREADS) {
     const int r = r0 + tid;
     Set set = {};
-    Joined join = {-1, -1};
+    Joined join = {-1, -1, 0, 0};
     if (r < p.requests) {
       set.kv = max(lens[r], 0);
       const int g = group_of(r, lens[r]);
@@ -255,7 +252,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 1) shared_plan_kernel(SharedPara
       set.queries = int(min(int64_t(p.next_n), p.num_rows - set.row0)) * p.group;
       set.unit0 = r * (p.kv_heads * ((p.next_n * p.group + S::QUERIES - 1) / S::QUERIES));
     }
-    join.suffix = place(r < p.requests, set);
+    const bool tail = set.end > set.first && set.end - set.first <= p.tail_entries;
+    if (tail) join.tail_first = set.first / STEP, join.tail_steps = (set.end - set.first + STEP - 1) / STEP;
+    join.suffix = place(r < p.requests && !tail, set);
     if (r < p.requests) p.joined[r] = join;
   }
   __syncthreads();
@@ -1023,6 +1022,10 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
     }
     ends[part] = count;
   }
+  if (join.tail_steps > 0) {
+    if (tid == 0) list[count] = {p.tail_pieces + int64_t(blockIdx.x) * p.tail_height * (D + 2), p.tail_height, m0};
+    ++count;
+  }
   __syncthreads();
   for (int i0 = tid; i0 < count * JOIN_ROWS; i0 += JOIN_AT_ONCE * JOIN_SHARED_THREADS) {
     float top[JOIN_AT_ONCE], sum[JOIN_AT_ONCE];
@@ -1111,13 +1114,14 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
 struct SharedInfo {
   const void *plan, *kernel, *join[3];  // joins: of split 1, 4 and 16
   int threads, smem, queries, tiles, step, piece_floats;
+  TailInfo (*tails)(int64_t members);
 };
 template <int D>
 SharedInfo shared_info() {
   using S = SharedShape<D>;
   return {reinterpret_cast<const void*>(shared_plan_kernel<D>), reinterpret_cast<const void*>(shared_kernel<D>),
           {reinterpret_cast<const void*>(shared_join_kernel<D, 1>), reinterpret_cast<const void*>(shared_join_kernel<D, 4>),
-           reinterpret_cast<const void*>(shared_join_kernel<D, 16>)}, S::THREADS, S::SMEM, S::QUERIES, S::TILES, S::N, S::PIECE};
+           reinterpret_cast<const void*>(shared_join_kernel<D, 16>)}, S::THREADS, S::SMEM, S::QUERIES, S::TILES, S::N, S::PIECE, tails_of<D>};
 }
 SharedInfo shared_64();
 SharedInfo shared_128();

@@ -74,22 +74,28 @@ def check(gvr, seed, groups, *, dim=128, dtype=torch.bfloat16, next_n=1, group=4
     s = 1 / np.sqrt(dim) if scale is None else scale
     if given is not None:
         starts, prefixes = (np.array(x, np.int32) for x in given)
-    args = (qd, dev(cache), dev(table), dev(np.array(kv, np.int32)), next_n, cr, dev(starts), dev(prefixes))
     more = dict(scale=scale, want_lse=True, k_scale=k_scale, v_scale=v_scale)
-    out, lse = gvr.attend_shared(*args, **more)
-    assert out.dtype == dtype and out.shape == (rows, heads, dim) and lse.shape == (rows, heads)
-    seen = cachecheck.row_entries(kv, next_n, cr, rows, table.shape[1] * ps)
+    capacity = table.shape[1] * ps
+    seen = cachecheck.row_entries(kv, next_n, cr, rows, capacity)
     ref = cachecheck.attend(q.double().numpy(), cache, table, seen, [r // next_n for r in range(rows)], None, s, k_scale, v_scale)
     v_max = np.nanmax(np.abs(cachecheck.unpack(cache, dim, k_scale, v_scale)[1]))
     tol, tol_lse = cachecheck.attend_tolerance(ref, EPS[dtype], v_max)
-    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
-    for got, want, most, name in ((o, ref[0], tol, "out"), (l, ref[1], tol_lse, "lse")):
-        assert np.array_equal(np.isnan(got), np.isnan(want)), (name, np.argwhere(np.isnan(got) != np.isnan(want))[:5])
-        with np.errstate(invalid="ignore"):
-            bad = (np.abs(got - want) > most) & (got != want)
-        assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:5], got[bad][:5], want[bad][:5], np.broadcast_to(most, got.shape)[bad][:5])
-    again, lse2 = gvr.attend_shared(*args, **more)
-    assert torch.equal(again.view(torch.int16), out.view(torch.int16)) and torch.equal(lse2.view(torch.int32), lse.view(torch.int32))  # the same bits
+    # a table as narrow as it is, for which attend_decode's kernels may run, then one as wide as it takes for those of attend_shared
+    wide = np.pad(table, ((0, 0), (0, -(-(1 << 25) // (requests * kv_heads * ps)))), constant_values=-1)
+    for t in (table, wide):
+        if t is wide and max(kv) // cr > capacity:
+            continue  # it would show entries that the other one does not
+        args = (qd, dev(cache), dev(t), dev(np.array(kv, np.int32)), next_n, cr, dev(starts), dev(prefixes))
+        out, lse = gvr.attend_shared(*args, **more)
+        assert out.dtype == dtype and out.shape == (rows, heads, dim) and lse.shape == (rows, heads)
+        o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for got, want, most, name in ((o, ref[0], tol, "out"), (l, ref[1], tol_lse, "lse")):
+            assert np.array_equal(np.isnan(got), np.isnan(want)), (name, np.argwhere(np.isnan(got) != np.isnan(want))[:5])
+            with np.errstate(invalid="ignore"):
+                bad = (np.abs(got - want) > most) & (got != want)
+            assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:5], got[bad][:5], want[bad][:5], np.broadcast_to(most, got.shape)[bad][:5])
+        again, lse2 = gvr.attend_shared(*args, **more)
+        assert torch.equal(again.view(torch.int16), out.view(torch.int16)) and torch.equal(lse2.view(torch.int32), lse.view(torch.int32))  # the same bits
     return args, out, lse
 
 
@@ -128,11 +134,11 @@ def test_many_queries_a_request(gvr, next_n, group):
     check(gvr, next_n, [(256, [150, 200 + next_n]), (100, [next_n, 300, 131])], group=group, kv_heads=1, dim=128, next_n=next_n, cut_rows=1)
 
 
-def test_most_requests_and_groups(gvr):
-    """8192 of both: what the plan holds in shared memory at most."""
-    groups = [(2, [1, 2])] * 2000 + [(1, [0])] * 4192
-    check(gvr, 31, groups, dim=64, group=1, kv_heads=1, ps=2, given=(list(range(0, 4002, 2)) + list(range(4001, 8193)) + [8192] * 2000,
-                                                                       [2] * 2000 + [1] * 4192 + [5] * 2000))
+def test_most_groups(gvr):
+    """8192 groups, most of them empty, of requests whose many queries want the kernels of attend_shared all the same."""
+    groups = [(70, [1, 2])] * 500 + [(1, [0])] * 24
+    starts = list(range(0, 1002, 2)) + list(range(1001, 1025)) + [1024] * 7668
+    check(gvr, 31, groups, dim=64, group=33, kv_heads=1, ps=2, given=(starts, [70] * 500 + [1] * 24 + [5] * 7668))
 
 
 @pytest.mark.parametrize("next_n,group,left", [(300, 1, 10), (40, 8, 3), (1000, 1, 1), (130, 2, 129)])
@@ -256,6 +262,15 @@ def test_long_prefixes(gvr, dim, kv_heads, requests, prefix):
 def test_few_queries_of_many_pieces(gvr, dim, requests, next_n, cut_rows):
     """Values whose pieces many threads join, beside short requests that have few."""
     check(gvr, 16, [(20000, [17] * requests), (0, [3])], dim=dim, kv_heads=1, group=2, next_n=next_n, cut_rows=cut_rows)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("next_n,group", [(1, 2), (3, 5), (1, 33)])
+def test_few_and_many_entries_behind_a_prefix(gvr, dim, next_n, group):
+    """On both sides of the 2048 that one CTA takes, with and without a prefix, which may end within a step of 32."""
+    check(gvr, 18, [(0, [2047 + next_n]), (0, [2048]), (0, [2049]), (100, [1948 + next_n, 2041, 2049, 2148, 2149, 5, 31, 33, 1])], dim=dim,
+          kv_heads=1, group=group, next_n=next_n)
+    check(gvr, 19, [(0, [300, 2500, 31, 4000])], dim=dim, kv_heads=2, group=group, next_n=next_n, ps=8)
 
 
 def test_many_requests(gvr):
