@@ -19,11 +19,11 @@ struct SharedDevice {
 };
 SharedDevice g_shared_devices[kMaxDevices];
 
-// Tails: at most so many entries, as one CTA walks over them, and so many tiles of queries, as each expands them anew; by a kernel
-// of its own, which few requests are not worth.  128 requests over 3200 entries, 2880 of them common: 107 -> 74 us with 8 KV
-// heads of 128 and 4 queries each, 77 -> 50 with 8 of 64 and one; 32 requests over 12800: 69 -> 57; 64 of 2 rows behind 32000, 10 to
-// 2000 of their own: 176 -> 179; 27 requests under 2 KV heads of 256 50 -> 67, were they let.
-constexpr int TAIL_ENTRIES = 2048, TAIL_TILES = 4, LEAST_TAILS = 256;
+// Tails: at most so many tiles of queries, as each expands their entries anew; by a kernel of its own, which few requests are
+// not worth.  128 requests over 3200 entries, 2880 of them common: 107 -> 73 us with 8 KV heads of 128 and 4 queries each,
+// 77 -> 50 with 8 of 64 and one; 32 requests over 12800: 69 -> 56; 64 of 2 rows behind 32000, 10 to 2000 of their own: 176 -> 177;
+// 27 requests under 2 KV heads of 256 50 -> 67, were they let.
+constexpr int TAIL_TILES = 4, LEAST_TAILS = 256;
 constexpr int64_t MAX_QUERIES = 1 << 26;  // of a KV head: their tiles' numbers share words with flags
 
 // Where everything lies in the workspace.
@@ -79,7 +79,7 @@ gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group,
   l->tail_tiles = int32_t((members + tail_queries - 1) / tail_queries);
   if (l->tail_tiles > TAIL_TILES || requests * kv_heads < LEAST_TAILS) l->tail_tiles = 0;
   l->tail_height = l->tail_tiles * tail_queries;
-  l->bytes = l->tails + align16(requests * kv_heads * l->tail_height * (dim + 2) * 4);
+  l->bytes = l->tails + align16(requests * kv_heads * TAIL_CHUNKS * l->tail_height * (dim + 2) * 4);
   return GVR_OK;
 }
 
@@ -90,7 +90,7 @@ struct Expected {
   float rows[3];  // apart: us a million rows, for jobs of 8, 16 and 32 queries
   float step[2];  // together: us a step of a unit of one tile, of two
 };
-bool better_apart(const SharedInfo& k, int dim, const SharedParams& p, int64_t members, int64_t groups, int sms) {
+bool better_apart(const SharedInfo& k, int dim, const SharedParams& p, int64_t members, int64_t groups, bool tails, int sms) {
   const Expected x = dim == 64    ? Expected{{17.f, 24.f, 38.f}, {1.f, 1.85f}}
                      : dim == 128 ? Expected{{25.f, 37.f, 37.f}, {1.25f, 2.2f}}
                                   : Expected{{66.f, 66.f, 66.f}, {1.27f, 1.27f}};
@@ -101,7 +101,7 @@ bool better_apart(const SharedInfo& k, int dim, const SharedParams& p, int64_t m
   const int64_t sets = groups > 0 ? std::min<int64_t>(groups, p.requests) : p.requests, queries = (p.num_rows * p.group + sets - 1) / sets;
   const double units = double(sets) * double(p.kv_heads) * double((queries + k.queries - 1) / k.queries);
   const double steps = double((int64_t(p.capacity) + k.step - 1) / k.step);
-  const double together = 20. + 0.05 * double(p.requests) * double(p.kv_heads) + units * steps * x.step[queries > 128] / sms;
+  const double together = 20. + (tails ? 0.03 : 0.06) * double(p.requests) * double(p.kv_heads) + units * steps * x.step[queries > 128] / sms;
   return apart <= together;
 }
 
@@ -159,7 +159,7 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   if (fits != GVR_OK) return fits;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < size_t(l.bytes)) return GVR_ERR_WORKSPACE;
   p.num_rows = num_rows;
-  if (better_apart(k, dim, p, members, num_groups, sms))
+  if (better_apart(k, dim, p, members, num_groups, l.tail_tiles > 0, sms))
     return attend_decode(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table, table_stride, table_width, kv_lens, next_n,
                          compress_ratio, nullptr, 1, scale, out, lse, workspace, workspace_bytes, stream);
   SharedDevice& d = g_shared_devices[dev];  // sm_count has checked dev
@@ -231,7 +231,7 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
     TailParams t = {p.joined, p.tail_pieces, p.tail_height};
     void* tail_args[] = {&a, &t};
     const TailInfo i = k.tails(members);
-    e = launch(i.kernel, dim3(uint32_t(tasks), uint32_t(l.tail_tiles)), i.threads, i.smem, 1, tail_args, stream);
+    e = launch(i.kernel, dim3(uint32_t(tasks), uint32_t(l.tail_tiles), TAIL_CHUNKS), i.threads, i.smem, 1, tail_args, stream);
   }
   if (e == cudaSuccess) e = launch(k.kernel, dim3(uint32_t(sms)), k.threads, k.smem, 1, args, stream);
   if (e == cudaSuccess) {

@@ -8,6 +8,8 @@
 // head it has units of 256 queries (head_dim 256: 128).  The steps of N entries of all units, one behind the other, are cut
 // into equal ranges, one a CTA of an SM.  A CTA walks over its range, unit by unit, and leaves a piece for each: sums over
 // exp2(score - base) v, base and sum.  A last kernel joins the pieces of every query.  Every sum has a fixed order.
+// (Of many requests with few entries behind their prefix, these are no sets: gvr_tails.cuh leaves pieces of them.  A set of few
+// queries costs 10 us of an SM beside its steps.)
 //
 // A CTA.  One warp walks over the share: it notes the segments for the others and starts the copies of their rows, a
 // page's rows of a head (up to a step's) a bulk tensor copy.  Four warps expand K and four V (e2m1 times e4m3 is exact
@@ -17,8 +19,8 @@
 // operand.  Two tiles take turns: while one's P is made, the other's products run.  Where a unit
 // has up to 128 queries both tiles hold them, one taking the even steps, one the odd ones.
 //
-// What bounds it (64 requests of 2 rows behind 32000 entries, 64 heads over 8 of 128: 175 us, 0.40 of the tensor cores' measured
-// rate; the plan takes 5 us of it, the shares 157, the join 12).  A step of a unit of 256 queries takes 2.2 us, of 128 queries
+// What bounds it (64 requests of 2 rows behind 32000 entries, 64 heads over 8 of 128: 177 us, 0.40 of the tensor cores' measured
+// rate; the plan takes 5 us of it, the tails 35, the shares 123, the join 12; without tails the shares took 157).  A step of a unit of 256 queries takes 2.2 us, of 128 queries
 // 1.25 (head_dim 64: 1.8 and 1.0; 256, 64 entries and 128 queries: 1.25).  No pipe is busy: the tensor pipe 46 %, issue 50 %, the
 // ALU 37 %, FMA 23 %, DRAM 11 %.  What counts is the way of a tile through
 // its step, scores -> maximum -> exponentials -> P -> products -> scores, about 3400 clocks of which the other tile's hide half.
@@ -965,7 +967,7 @@ struct Listed {
 };
 
 // Pieces of a query at most: the units that it is in are cut where CTAs' shares end, and of each CTA it has up to two.
-__host__ __device__ constexpr int join_pieces(int grid) { return 2 * (grid + 3); }
+__host__ __device__ constexpr int join_pieces(int grid) { return 2 * (grid + 3) + TAIL_CHUNKS; }
 __host__ __device__ constexpr int join_smem(int grid) { return join_pieces(grid) * (JOIN_ROWS * 8 + int(sizeof(Listed))); }
 
 // blockIdx.x: requests x KV heads; y: JOIN_ROWS of the request's queries; z: dimensions, four a thread.  Neighbouring
@@ -1022,10 +1024,9 @@ __global__ void __launch_bounds__(JOIN_SHARED_THREADS) shared_join_kernel(Shared
     }
     ends[part] = count;
   }
-  if (join.tail_steps > 0) {
-    if (tid == 0) list[count] = {p.tail_pieces + int64_t(blockIdx.x) * p.tail_height * (D + 2), p.tail_height, m0};
-    ++count;
-  }
+  const int chunks = (join.tail_steps + TAIL_CHUNK - 1) / TAIL_CHUNK;
+  if (tid < chunks) list[count + tid] = {p.tail_pieces + (int64_t(blockIdx.x) * TAIL_CHUNKS + tid) * p.tail_height * (D + 2), p.tail_height, m0};
+  count += chunks;
   __syncthreads();
   for (int i0 = tid; i0 < count * JOIN_ROWS; i0 += JOIN_AT_ONCE * JOIN_SHARED_THREADS) {
     float top[JOIN_AT_ONCE], sum[JOIN_AT_ONCE];

@@ -1,7 +1,7 @@
 // gvr_tails.cuh -- the entries behind a prefix, of attend_shared's requests that have few of them and few queries: what
 // gvr_attend.cuh's walk does to a request's rows, from an entry on.
 //
-// A CTA has a request's queries of a KV head (up to Q of them: a tile) and all of its entries; its warps take steps of 32 in
+// A CTA has a request's queries of a KV head (up to Q of them: a tile) and a chunk of its entries; its warps take steps of 32 in
 // turn, and their sums join in shared memory to one piece.  Products are mma.sync ones, 8 queries wide, as the queries are few.
 #pragma once
 
@@ -16,9 +16,13 @@ struct __align__(16) Joined {
   int32_t tail_first, tail_steps;  // its tail, in steps of 32 entries; 0: none
 };
 
+// Entries of a chunk, in steps, and chunks of a tail.  (64 requests of 2 rows, 8 KV heads of 128, 10 to 2000 entries each behind a
+// prefix: 177 us with two chunks of 32 steps, 179 with one of 64, 185 with four of 16, 200 with eight of 8.)
+constexpr int TAIL_CHUNK = 32, TAIL_CHUNKS = 2, TAIL_ENTRIES = TAIL_CHUNKS * TAIL_CHUNK * STEP;
+
 struct TailParams {
   const Joined* joined;
-  float* pieces;  // [requests][KV heads][D / 4][height][4], then bases and sums [height]
+  float* pieces;  // [requests][KV heads][TAIL_CHUNKS][D / 4][height][4], then bases and sums [height]
   int32_t height;  // queries, up to whole tiles
 };
 
@@ -31,7 +35,7 @@ struct TailShape {
   static constexpr int SMEM = WARPS * (S::WALK > JOIN ? S::WALK : JOIN);
 };
 
-// blockIdx.x: requests x KV heads; y: tiles.
+// blockIdx.x: requests x KV heads; y: tiles; z: chunks.
 template <int D, int NT>
 __global__ void __launch_bounds__(TailShape<D, NT>::THREADS, Shape<D, NT>::FOLD_BLOCKS) tails_kernel(AttendParams p, TailParams t) {
   using S = Shape<D, NT>;
@@ -43,8 +47,8 @@ __global__ void __launch_bounds__(TailShape<D, NT>::THREADS, Shape<D, NT>::FOLD_
   const int r = blockIdx.x / p.kv_heads, h = blockIdx.x - r * p.kv_heads, m0 = blockIdx.y * S::Q;
   begin();
   const int4 held = *reinterpret_cast<const int4*>(t.joined + r);
-  const int first = held.z, steps = held.w;
-  if (steps == 0) return;
+  const int first = held.z + int(blockIdx.z) * TAIL_CHUNK, steps = min(held.w - int(blockIdx.z) * TAIL_CHUNK, TAIL_CHUNK);
+  if (steps <= 0) return;
   uint32_t raw[NT][D / 8];
   load_queries<D, NT, true>(p, r, h, m0, p.fold * p.group, raw);
   const Unit u = load_unit<true>(p, r);
@@ -68,7 +72,7 @@ __global__ void __launch_bounds__(TailShape<D, NT>::THREADS, Shape<D, NT>::FOLD_
       if (g == 0) tops[warp * S::Q + qi] = top[n][j], sums[warp * S::Q + qi] = total[n][j];
     }
   __syncthreads();
-  float* piece = t.pieces + int64_t(blockIdx.x) * t.height * (D + 2);
+  float* piece = t.pieces + (int64_t(blockIdx.x) * TAIL_CHUNKS + blockIdx.z) * t.height * (D + 2);
   for (int i = tid; i < S::Q * D / 4; i += T::THREADS) {
     const int qi = i % S::Q, d4 = i / S::Q;
     float all = NO_TOP, sum = 0.f;

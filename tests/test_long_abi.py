@@ -142,7 +142,7 @@ def test_every_kernel_waits_for_the_one_before_it():
         for body in re.split(r"__global__", code(path))[1:]:
             kernels += 1
             assert re.search(r"\bbegin\(\);", body.split("\n}\n")[0])
-    assert kernels == 6
+    assert kernels == 7
 
 
 SHARES = r"""
