@@ -75,7 +75,8 @@ def attend_shared(q, cache, block_table, kv_lens, next_n: int, compress_ratio: i
 
     ``group_starts`` (int32 [groups + 1]) cuts the requests into groups: group g is requests group_starts[g] up to
     group_starts[g + 1].  The first ``prefix_entries[g]`` entries (int32 [groups]) of all its requests are the same, as
-    they are behind one prompt: they are read once for the whole group.  The result is that of ``attend_decode``.
+    they are behind one prompt, and each request's table has them: they are read once for the whole group, where the
+    tables are wide and the requests many enough for that to pay.  The result is that of ``attend_decode``.
     """
     if stream is not None:
         with _current(stream, q):
