@@ -718,31 +718,50 @@ __device__ __forceinline__ bool soften(const SharedParams& p, SharedBars* bars, 
     x.piece = g.piece + x.at;
     if (x.tasks == 0) return;
     if (x.warp) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * p.q_row + int64_t(g.head * p.group + m - rel * p.group) * p.q_head);
+      // half of the query's values, in one go as far as registers have room
+      constexpr int PARTS = D / 16, HELD = PARTS < 8 ? PARTS : 8;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + at * p.q_row + int64_t(g.head * p.group + m - rel * p.group) * p.q_head) + half * PARTS;
+      uint4 v[HELD];
+      auto load = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) v[j] = live ? src[j0 + j] : make_uint4(0, 0, 0, 0);
+      };
       float mul = p.q_sign, back = 1.f;
       if (p.bf16) {  // exactly to f16 by a power of two per query (gvr_attend.cuh)
         uint32_t big = 0;
-#pragma unroll 8
-        for (int j = 0; j < D / 8; ++j) {
-          const uint4 v = live ? src[j] : make_uint4(0, 0, 0, 0);
-          big = __vmaxu2(__vmaxu2(big, v.x & 0x7fff7fffu), v.y & 0x7fff7fffu);
-          big = __vmaxu2(__vmaxu2(big, v.z & 0x7fff7fffu), v.w & 0x7fff7fffu);
+#pragma unroll 1
+        for (int j0 = PARTS - HELD; j0 >= 0; j0 -= HELD) {  // the first ones last: they stay
+          load(j0);
+#pragma unroll
+          for (int j = 0; j < HELD; ++j) {
+            big = __vmaxu2(__vmaxu2(big, v[j].x & 0x7fff7fffu), v[j].y & 0x7fff7fffu);
+            big = __vmaxu2(__vmaxu2(big, v[j].z & 0x7fff7fffu), v[j].w & 0x7fff7fffu);
+          }
         }
         big = max(big & 0xffffu, big >> 16);
+        *mine = __uint_as_float(big);
+        meet(pair, false);
+        big = max(big, *reinterpret_cast<const volatile uint32_t*>(other));
         const int exponent = int(big >> 7), up = big == 0 || exponent == 255 ? 0 : min(14 - (exponent - 127), 126);
         mul = p.q_sign * __uint_as_float(uint32_t(127 + up) << 23);
         back = __uint_as_float(uint32_t(127 - up) << 23);
+      } else {
+        load(0);
       }
       const uint32_t sign = pack_f16(p.q_sign, p.q_sign);
-#pragma unroll 4
-      for (int j = half * (D / 16); j < (half + 1) * (D / 16); ++j) {  // half of the query's values
-        const uint4 v = live ? src[j] : make_uint4(0, 0, 0, 0);
-        uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+      for (int j0 = 0; j0 < PARTS; j0 += HELD) {
+        if (j0 > 0) load(j0);
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
-          h[y] = p.bf16 ? pack_f16(__uint_as_float(h[y] << 16) * mul, __uint_as_float(h[y] & 0xffff0000u) * mul) : hmul2(h[y], sign);
-        const uint32_t dst = q_row_at + j / 8 * (128 * 128) + ((j % 8) ^ (row & 7)) * 16;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+        for (int j = 0; j < HELD; ++j) {
+          uint32_t h[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            h[y] = p.bf16 ? pack_f16(__uint_as_float(h[y] << 16) * mul, __uint_as_float(h[y] & 0xffff0000u) * mul) : hmul2(h[y], sign);
+          const int part = half * PARTS + j0 + j;
+          const uint32_t dst = q_row_at + part / 8 * (128 * 128) + ((part % 8) ^ (row & 7)) * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+        }
       }
       x.factor = fmaxf(back * p.scale_log2, 1.17549435e-38f);
     }
