@@ -8,8 +8,7 @@
 // head it has units of 256 queries (head_dim 256: 128).  The steps of N entries of all units, one behind the other, are cut
 // into equal ranges, one a CTA of an SM.  A CTA walks over its range, unit by unit, and leaves a piece for each: sums over
 // exp2(score - base) v, base and sum.  A last kernel joins the pieces of every query.  Every sum has a fixed order.
-// (Of many requests with few entries behind their prefix, these are no sets: gvr_tails.cuh leaves pieces of them.  A set of few
-// queries costs 10 us of an SM beside its steps.)
+// (Of many requests with few entries behind their prefix, these are no sets: gvr_tails.cuh leaves pieces of them.)
 //
 // A CTA.  One warp walks over the share: it notes the segments for the others and starts the copies of their rows, a
 // page's rows of a head (up to a step's) a bulk tensor copy.  Four warps expand K and four V (e2m1 times e4m3 is exact
@@ -19,8 +18,8 @@
 // operand.  Two tiles take turns: while one's P is made, the other's products run.  Where a unit
 // has up to 128 queries both tiles hold them, one taking the even steps, one the odd ones.
 //
-// What bounds it (64 requests of 2 rows behind 32000 entries, 64 heads over 8 of 128: 177 us, 0.40 of the tensor cores' measured
-// rate; the plan takes 5 us of it, the tails 35, the shares 123, the join 12; without tails the shares took 157).  A step of a unit of 256 queries takes 2.2 us, of 128 queries
+// What bounds it (64 requests of 2 rows behind 32000 entries, 64 heads over 8 of 128: 165 us, 0.42 of the tensor cores' measured
+// rate; the plan takes 5 us of it, the tails 35, the shares about 112, the join 12; without tails as much in all).  A step of a unit of 256 queries takes 2.2 us, of 128 queries
 // 1.25 (head_dim 64: 1.8 and 1.0; 256, 64 entries and 128 queries: 1.25).  No pipe is busy: the tensor pipe 49 %, issue 54 %, the
 // ALU 39 %, FMA 25 %, DRAM 4 %.  What counts is the way of a tile through
 // its step, scores -> maximum -> exponentials -> P -> products -> scores, about 3400 clocks of which the other tile's hide half.
@@ -30,7 +29,7 @@
 // unrolled (260 against 213: code beyond the instruction caches), counters of barriers in arrays (185 against 175: they
 // lie in memory), copies by warps instead of tensor copies (+8 us), one thread a query (slower), three of eight exponentials by a
 // polynomial (slower), a pass without the maximum of the step (spills), the first scores kept in registers from the
-// maximum's pass to the exponentials' (+2.5), P handed over by halves (+3), V waited for by halves (+4) or quarters (+13), an issuer
+// maximum's pass to the exponentials' (+2.5), queries read twice, for their largest and to convert them (+12), P handed over by halves (+3), V waited for by halves (+4) or quarters (+13), an issuer
 // a tile (+32: their products interleave, and each tile's are through later).  Without exponentials, expansions and
 // maxima, and with one product for eight, 140 of then 194 us were left.  The joining kernel is not let start early: its CTAs, few of
 // which read most, would gather on the SMs that are through first (66 us became 80 where 640 queries of one KV head share

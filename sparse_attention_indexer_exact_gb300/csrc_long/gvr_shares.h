@@ -7,9 +7,10 @@
 
 namespace gvrc {
 
-// What a unit costs beside its steps (queries, first pages, its piece), in tile steps.  With 2, 4, 7 and 10 the benchmark's
-// batch of long prompts took 210, 175, 182 and 188 us, its small groups 41, 43, 46 and 50 us.
-constexpr int UNIT_WORK = 4;
+// What a unit costs beside its steps (queries, first pages, its piece), in tile steps.  With 2, 3, 4 and 6 the benchmark's
+// small groups took 40.9, 41.2, 42.3 and 44.9 us, its document 65, 62.1, 61.8 and 61.9; too little lets those who have
+// several units end last, too much those who have none.
+constexpr int UNIT_WORK = 3;
 
 // The work of a unit of `steps` steps, each taken by one tile or by both.
 GVRC_FN int unit_work(int steps, int both) { return UNIT_WORK + (steps << both); }

@@ -18,6 +18,7 @@ PKG = os.path.join(ROOT, "sparse_attention_indexer_exact_gb300")
 HEADER = os.path.join(ROOT, "include", "gvr_long.h")
 WORKSPACE = 7
 NO_GPU = 6  # where the answer depends on the device's SMs
+UNIT_WORK = 3  # of gvr_shares.h
 
 
 def test_library_exports_what_the_header_declares(gvr, lib):
@@ -202,7 +203,7 @@ def test_shares_are_joined_as_they_are_walked(tmp_path):
     cases = [([(1, 0)], 1), ([(1, 0)], 2), ([(1, 1)], 3), ([(10 ** 8, 1), (1, 0), (10 ** 8, 1)], 152), ([(1, 0)] * 1000, 152)]
     for _ in range(300):
         units = [(rng.choice([1, 2, 3, 7, 64, 513]), rng.randrange(2)) for _ in range(rng.randrange(1, 60))]
-        total = sum(4 + (s << b) for s, b in units)
+        total = sum(UNIT_WORK + (s << b) for s, b in units)
         cases.append((units, max(1, min(rng.choice([1, 3, 132, 152]), total // 2))))
     text = "\n".join(" ".join(f"{s} {b}" for s, b in units) + f" -1 {ctas}" for units, ctas in cases)
     r = subprocess.run([str(exe)], input=text, capture_output=True, text=True)
@@ -213,7 +214,7 @@ def test_shares_are_joined_as_they_are_walked(tmp_path):
         for line in at:
             kind, *x = line.split()
             if kind == "end":
-                assert int(x[0]) == sum(4 + (s << b) for s, b in units)
+                assert int(x[0]) == sum(UNIT_WORK + (s << b) for s, b in units)
                 break
             c, u, lo, hi = map(int, x)
             assert 0 <= c < ctas
