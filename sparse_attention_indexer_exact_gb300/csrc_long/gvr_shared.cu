@@ -20,9 +20,9 @@ struct SharedDevice {
 SharedDevice g_shared_devices[kMaxDevices];
 
 // Tails: at most so many tiles of queries, as each expands their entries anew; by a kernel of its own, which few requests are
-// not worth.  128 requests over 3200 entries, 2880 of them common: 107 -> 73 us with 8 KV heads of 128 and 4 queries each,
-// 77 -> 50 with 8 of 64 and one; 32 requests over 12800: 69 -> 56; 64 of 2 rows behind 32000, 10 to 2000 of their own: 176 -> 177;
-// 27 requests under 2 KV heads of 256 50 -> 67, were they let.
+// not worth.  128 requests over 3200 entries, 2880 of them common: 96 -> 69 us with 8 KV heads of 128 and 4 queries each,
+// 48 -> 43 with 4 of 64 and 12; 32 requests over 12800: 60 -> 53; 64 of 2 rows behind 32000, 10 to 2000 of their own: 166 -> 165;
+// 27 requests under 2 KV heads of 256 took 17 us more with them.
 constexpr int TAIL_TILES = 4, LEAST_TAILS = 256;
 constexpr int64_t MAX_QUERIES = 1 << 26;  // of a KV head: their tiles' numbers share words with flags
 
@@ -85,7 +85,7 @@ gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group,
 
 // Whether attend_decode, which reads each request's entries by themselves, is expected to take less time, by the table's width, as the
 // lengths are on the device.  Measured apart and together: 2 requests of 800 entries (8 KV heads of 128, 4 queries each) 8.5 and
-// 19 us, 32 of 800 14 and 35, 128 of 3200 91 and 72, 32 of 12800 90 and 57; of 2 heads of 256, 32 of 3200 25 and 34, of 12800 64 and 47.
+// 19 us, 32 of 800 14 and 35, 128 of 3200 91 and 69, 32 of 12800 90 and 53; of 2 heads of 256, 32 of 3200 25 and 34, of 12800 64 and 47.
 struct Expected {
   float rows[3];  // apart: us a million rows, for jobs of 8, 16 and 32 queries
   float step[2];  // together: us a step of a unit of one tile, of two
