@@ -500,15 +500,18 @@ __device__ __forceinline__ bool bring(const SharedParams& p, SharedBars* bars, c
     if (!(note.there[row / 32] >> (row % 32) & 1)) {
 #pragma unroll
       for (int j = 0; j < VALUES / 64; ++j) scales[j] = 0;  // P is 0 there, and 0 x NaN is not
-    } else if (is_v && border >= 0) {
+    }
+    const int slot = is_v ? 0 : int(step & 1);
+    if (!__all_sync(0xffffffffu, bar_wait(is_v ? &bars->v_free[half] : &bars->k_free[slot], (is_v ? step & 1 : step >> 1 & 1) ^ 1))) return false;
+    // Behind the wait: the products of the step before this one are complete, so that each tile's takers have written P of
+    // a later segment than the one that had this segment's slot, and that one's notes are read and cleared.
+    if (is_v && border >= 0) {
       uint32_t blocks = 0;
 #pragma unroll
       for (int j = 0; j < VALUES / 16; ++j)
         if ((scales[j / 4] >> (8 * (j % 4)) & 0x7f) == 0x7f) blocks |= 1u << (part * (VALUES / 16) + j), scales[j / 4] &= ~(0xffu << (8 * (j % 4)));
       if (blocks) note_nan<D>(p.sets + note.set, p.next_n, p.group, p.ratio, p.capacity, note.where, border + row, blocks, nans);
     }
-    const int slot = is_v ? 0 : int(step & 1);
-    if (!__all_sync(0xffffffffu, bar_wait(is_v ? &bars->v_free[half] : &bars->k_free[slot], (is_v ? step & 1 : step >> 1 & 1) ^ 1))) return false;
     const uint8_t* at = from + stage * S::RAW;
     uint32_t dst = to + slot * S::KV_BYTES;
 #pragma unroll 1
