@@ -461,9 +461,11 @@ __device__ __forceinline__ bool walk(const SharedParams& p, const CUtensorMap* m
 }
 
 // A NaN that only some rows of a unit see is taken out of V, and put into those rows' results: `blocks` of 16 values of
-// entry e, which the rows whose limit lies behind it note.
+// entry e, which the rows whose limit lies behind it note.  Of a prefix's rows only those of requests that share it: a
+// warp that takes scores neither reads nor clears the notes of rows that are all without one.
 template <int D>
-__device__ __noinline__ void note_nan(const Set* set, int next_n, int group, int ratio, int capacity, int where, int e, uint32_t blocks, uint32_t* nans) {
+__device__ __noinline__ void note_nan(const Set* set, const Joined* joined, int next_n, int group, int ratio, int capacity, int where, int e, uint32_t blocks,
+                                      uint32_t* nans) {
   using S = SharedShape<D>;
   const Set of = *set;
   for (int t = 0; t < S::TILES; ++t) {
@@ -472,8 +474,10 @@ __device__ __noinline__ void note_nan(const Set* set, int next_n, int group, int
     const int slot = where >> (t ? 8 : 4) & 15;
     for (int x = 0; x < 128; ++x) {
       const int m = (where >> 12) * S::QUERIES + (both ? 128 * t : 0) + x;
-      const int seen = of.kv < 0 ? of.end : decode_entries(of.kv, next_n, m / group, ratio, capacity);
-      if (m < of.queries && seen > e) atomicOr(&nans[(slot * S::TILES + t) * 128 + x], blocks);
+      if (m >= of.queries) break;
+      const int rel = m / group;
+      const bool sees = of.kv < 0 ? joined[(of.row0 + rel) / next_n].prefix >= 0 && of.end > e : decode_entries(of.kv, next_n, rel, ratio, capacity) > e;
+      if (sees) atomicOr(&nans[(slot * S::TILES + t) * 128 + x], blocks);
     }
   }
 }
@@ -510,7 +514,7 @@ __device__ __forceinline__ bool bring(const SharedParams& p, SharedBars* bars, c
 #pragma unroll
       for (int j = 0; j < VALUES / 16; ++j)
         if ((scales[j / 4] >> (8 * (j % 4)) & 0x7f) == 0x7f) blocks |= 1u << (part * (VALUES / 16) + j), scales[j / 4] &= ~(0xffu << (8 * (j % 4)));
-      if (blocks) note_nan<D>(p.sets + note.set, p.next_n, p.group, p.ratio, p.capacity, note.where, border + row, blocks, nans);
+      if (blocks) note_nan<D>(p.sets + note.set, p.joined, p.next_n, p.group, p.ratio, p.capacity, note.where, border + row, blocks, nans);
     }
     const uint8_t* at = from + stage * S::RAW;
     uint32_t dst = to + slot * S::KV_BYTES;

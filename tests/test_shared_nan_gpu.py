@@ -36,3 +36,19 @@ def test_nan_in_short_prefixes_one_after_the_other(gvr, dim):  # noqa: F811
 
     _, out, _ = check(gvr, 42, [(96, [1, 5, 2, 9, 1, 30, 3, 4])] * 150, dim=dim, group=1, kv_heads=8, change=change)
     assert out.isnan().any(-1).any(-1).tolist() == [r // 8 % 3 == 0 for r in range(1200)]
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 64), (128, 40), (256, 64)])
+def test_nan_in_a_prefix_with_idle_requests(gvr, dim, group):  # noqa: F811
+    """Idle requests of so many queries that whole warps have none that is live, in groups whose prefix has a NaN; the groups after
+    them have none, and all of their requests are live."""
+    idle = {g: g % 3 for g in range(0, 200, 2)}
+    groups = [(96, [-1 if idle.get(g) == i else 3 + i for i in range(4)]) for g in range(200)]
+
+    def change(cache, table, kv, starts, prefixes):
+        for g in idle:
+            r = 4 * g + (g % 3 == 0)
+            nan_in_v(cache, table[r, 5], 9, g // 2 % 2, dim, g % (dim // 16))
+
+    _, out, _ = check(gvr, 43, groups, dim=dim, group=group, change=change)
+    assert out.isnan().any(-1).any(-1).tolist() == [g in idle and idle[g] != i for g in range(200) for i in range(4)]
