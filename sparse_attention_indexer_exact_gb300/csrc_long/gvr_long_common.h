@@ -1,4 +1,4 @@
-// gvr_long_common.h -- what the host code of include/gvr_long.h shares: the checks of a call's rows.
+// gvr_long_common.h -- what the host code of include/gvr_long.h shares: the checks of a call's rows, and the ways of attend_shared.
 #pragma once
 
 #include <cmath>
@@ -31,4 +31,16 @@ inline gvr_status check_rows(const gvr_cache* cache, const void* q, int64_t q_ro
   return GVR_OK;
 }
 
+// Which kernels attend_shared takes: those of its rule, its own, or attend_decode's.
+enum { WAY_BY_RULE = 0, WAY_TOGETHER = 1, WAY_APART = 2 };
+
 }  // namespace gvrc
+
+// attend_shared with the choice between the kernels made by the caller.  Exported for the tests alone, which run every case
+// both ways: the rule goes by the table's width and would send most small cases to attend_decode's kernels.
+extern "C" gvr_status attend_shared_way(int32_t way, const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                                        int32_t dtype, int64_t num_rows, int32_t num_heads, const int32_t* block_table,
+                                        int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int32_t next_n,
+                                        int32_t compress_ratio, const int32_t* group_starts, const int32_t* prefix_entries,
+                                        int64_t num_groups, float scale, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream);

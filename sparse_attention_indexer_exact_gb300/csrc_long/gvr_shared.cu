@@ -127,12 +127,12 @@ gvr_status attend_shared_workspace(int32_t num_kv_heads, int32_t head_dim, int64
   return s;
 }
 
-gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
-                         int32_t dtype, int64_t num_rows, int32_t num_heads, const int32_t* block_table,
-                         int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int32_t next_n,
-                         int32_t compress_ratio, const int32_t* group_starts, const int32_t* prefix_entries,
-                         int64_t num_groups, float scale, void* out, float* lse, void* workspace,
-                         size_t workspace_bytes, void* stream) {
+gvr_status attend_shared_way(int32_t way, const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                             int32_t dtype, int64_t num_rows, int32_t num_heads, const int32_t* block_table,
+                             int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int32_t next_n,
+                             int32_t compress_ratio, const int32_t* group_starts, const int32_t* prefix_entries,
+                             int64_t num_groups, float scale, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   using namespace gvrc;
   const gvr_status s = check_rows(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table, table_stride, table_width,
                                   kv_lens, next_n, compress_ratio, scale);
@@ -159,7 +159,7 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
   if (fits != GVR_OK) return fits;
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < size_t(l.bytes)) return GVR_ERR_WORKSPACE;
   p.num_rows = num_rows;
-  if (better_apart(k, dim, p, members, num_groups, l.tail_tiles > 0, sms))
+  if (way == WAY_APART || (way == WAY_BY_RULE && better_apart(k, dim, p, members, num_groups, l.tail_tiles > 0, sms)))
     return attend_decode(cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table, table_stride, table_width, kv_lens, next_n,
                          compress_ratio, nullptr, 1, scale, out, lse, workspace, workspace_bytes, stream);
   SharedDevice& d = g_shared_devices[dev];  // sm_count has checked dev
@@ -245,6 +245,17 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
     e = launch(k.join[which], grid, JOIN_SHARED_THREADS, join_smem(sms), 1, args, stream);
   }
   return e == cudaSuccess ? GVR_OK : GVR_ERR_LAUNCH;
+}
+
+gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                         int32_t dtype, int64_t num_rows, int32_t num_heads, const int32_t* block_table,
+                         int64_t table_stride, int64_t table_width, const int32_t* kv_lens, int32_t next_n,
+                         int32_t compress_ratio, const int32_t* group_starts, const int32_t* prefix_entries,
+                         int64_t num_groups, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return attend_shared_way(gvrc::WAY_BY_RULE, cache, q, q_row_stride, q_head_stride, dtype, num_rows, num_heads, block_table, table_stride,
+                           table_width, kv_lens, next_n, compress_ratio, group_starts, prefix_entries, num_groups, scale, out, lse,
+                           workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
