@@ -58,11 +58,14 @@ bool tensor_map(const gvr_cache* c, int step, CUtensorMap* map) {
                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Groups whose prefix is shared, at most: each has two requests.  (Callers may list many more, most of them empty.)
+int64_t sharing_groups(int64_t groups, int64_t requests) { return std::min(groups, requests / 2); }
+
 gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group, int64_t num_rows, int64_t next_n, int64_t groups, int64_t grid, Layout* l) {
   const int64_t requests = (num_rows + next_n - 1) / next_n, members = next_n * group;
-  const int64_t tiles = (members + k.queries - 1) / k.queries;
+  const int64_t tiles = (members + k.queries - 1) / k.queries, sharing = sharing_groups(groups, requests);
   // a group has its queries / k.queries tiles and at most one more
-  const int64_t prefix_units = groups > 0 ? kv_heads * (num_rows * group / k.queries + groups) : 0;
+  const int64_t prefix_units = sharing > 0 ? kv_heads * (num_rows * group / k.queries + sharing) : 0;
   const int64_t suffix_units = requests * kv_heads * tiles;
   if (prefix_units > kIntMax / 2 || suffix_units > kIntMax / 2) return GVR_ERR_ARG;
   l->suffix_rows = int32_t(std::min<int64_t>(128, (members + 7) / 8 * 8));
@@ -73,7 +76,7 @@ gvr_status layout(const SharedInfo& k, int dim, int64_t kv_heads, int64_t group,
   l->cta_set = l->joined + align16(requests * int64_t(sizeof(Joined)));
   l->cta_start = l->cta_set + align16(grid * 4);
   l->prefix = l->cta_start + align16((grid + 1) * 4);
-  l->suffix = l->prefix + (groups > 0 ? (grid + prefix_units) * k.piece_floats * 4 : 0);
+  l->suffix = l->prefix + (sharing > 0 ? (grid + prefix_units) * k.piece_floats * 4 : 0);
   l->tails = l->suffix + (grid + suffix_units) * suffix_floats * 4;
   const int32_t tail_queries = k.tails(members).queries;
   l->tail_tiles = int32_t((members + tail_queries - 1) / tail_queries);
@@ -150,7 +153,7 @@ gvr_status attend_shared_way(int32_t way, const gvr_cache* cache, const void* q,
   p.requests = int32_t((num_rows + next_n - 1) / next_n);
   // work is counted in 32 bits: each unit's steps, twice where two tiles take them, and what it costs beside
   const int64_t steps = (int64_t(p.capacity) + k.step - 1) / k.step + UNIT_WORK, members = int64_t(next_n) * p.group;
-  const int64_t units = int64_t(p.kv_heads) * (num_rows * p.group / k.queries + num_groups + p.requests * ((members + k.queries - 1) / k.queries));
+  const int64_t units = int64_t(p.kv_heads) * (num_rows * p.group / k.queries + sharing_groups(num_groups, p.requests) + p.requests * ((members + k.queries - 1) / k.queries));
   if (units > kIntMax / 2 || (steps > 0 && units > kIntMax / 2 / steps)) return GVR_ERR_ARG;
   int sms = 0, dev = 0;
   if (sm_count(&sms) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return GVR_ERR_LAUNCH;
