@@ -330,11 +330,13 @@ PyObject* evict(PyObject* const* a) {
   const gvr_cache c = cache_of(w, tensor(a[1]), 1.f, 1.f);
   const Tensor &lens = tensor(a[3]), &free_pages = tensor(a[4]);
   need(lens.dim() == 1);
-  const int64_t requests = lens.size(0), most = integer(a[8]);
+  const int64_t requests = lens.size(0);
   const int32_t *lens_at = int32s(w, lens, 0), *free_at = int32s(w, free_pages, 0);
   const int32_t keep = integer32(a[5]), recent = integer32(a[6]), ratio = integer32(a[7]);
   const Table t = table_of(w, tensor(a[2]), requests);
   const Weights x = weights_of(w, tensor(a[0]), requests, t.width * c.page_size);
+  // max_released None: as many as the given list holds, else every page of the table
+  const int64_t most = a[8] != Py_None ? integer(a[8]) : a[11] != Py_None ? tensor(a[11]).numel() : requests * t.width;
   size_t bytes = 0;
   need(most >= 0 && most <= INT32_MAX && cache_evict_workspace(requests, keep, &bytes) == GVR_OK);
   const Tensor out[4] = {ints(w, a[9], {requests, keep}), ints(w, a[10], {requests}), ints(w, a[11], {most}), ints(w, a[12], {3})};

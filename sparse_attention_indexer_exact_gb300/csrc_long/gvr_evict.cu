@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1024 / SELECT_THREADS) evict_s
   for (int i = tid; i < 3 * BINS; i += SELECT_THREADS) (&hist[0][0])[i] = 0;
   if (tid == 0) mine_of[2] = 0xffffffffu, mine_of[3] = 0;
   begin();
+  // the list of released pages, which may be as long as the table; the pages come in with the next kernel
+  for (int64_t i = int64_t(blockIdx.x) * SELECT_THREADS + tid; i < p.max_released; i += int64_t(gridDim.x) * SELECT_THREADS) p.released[i] = -1;
   const int n = entries_of(p, r);
   int32_t* kept = p.kept + int64_t(r) * p.keep;
   if (n <= p.keep) {  // by all CTAs of the cluster alike
@@ -317,7 +319,6 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictParams p)
     }
     taken = sum_all(taken, sums), back = sum_all(back, sums), left = sum_all(left, sums);
     if (tid == 0) p.counts[0] = int(taken), p.counts[1] = int(back), p.counts[2] = int(left);
-    for (int64_t i = back + tid; i < p.max_released; i += MOVE_THREADS) p.released[i] = -1;
   }
   if (!served) {
     if (cut.state != WHOLE) {

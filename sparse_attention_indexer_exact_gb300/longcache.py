@@ -149,7 +149,7 @@ def attend_weights(q, cache, block_table, kv_lens, next_n: int, compress_ratio: 
     return weights
 
 
-def cache_evict(weights, cache, block_table, kv_lens, free_pages, keep: int, recent: int, compress_ratio: int = 1, max_released: int = 0,
+def cache_evict(weights, cache, block_table, kv_lens, free_pages, keep: int, recent: int, compress_ratio: int = 1, max_released: int | None = None,
                 kept=None, new_lens=None, released=None, counts=None, *, stream=None):
     """Cut each request's cache to ``keep`` entries: its ``recent`` last ones, and of the others those of largest weight.
 
@@ -160,7 +160,8 @@ def cache_evict(weights, cache, block_table, kv_lens, free_pages, keep: int, rec
     written.  ``block_table`` and ``weights`` are rewritten in place.  Returns ``kept`` (int32 [requests, keep]: the entries' old numbers, -1
     behind them), ``new_lens`` (int32 [requests]), ``released`` (int32 [max_released]: the pages given up, -1 behind
     them) and ``counts`` (int32 [3]: pages taken, pages released, requests left as they were for want of pages, whose row of
-    ``kept`` is -1).
+    ``kept`` is -1).  Without ``max_released`` the list holds as many as ``released`` does where that is given, else every page
+    of the table; a shorter one loses the numbers of those that it has no room for.
     """
     if stream is not None:
         with _current(stream, cache):
@@ -172,7 +173,7 @@ def cache_evict(weights, cache, block_table, kv_lens, free_pages, keep: int, rec
         return done
     import torch
     keep, recent, compress_ratio = _int32_value(keep, "keep"), _int32_value(recent, "recent"), _int32_value(compress_ratio, "compress_ratio")
-    if keep < 1 or not 0 <= recent <= keep or max_released < 0:
+    if keep < 1 or not 0 <= recent <= keep or (max_released is not None and max_released < 0):
         raise ValueError(f"keep must be at least 1, recent 0 to keep and max_released at least 0: got {keep}, {recent} and {max_released}")
     c = _cache_struct(cache, 1.0, 1.0)
     device = cache.get_device()
@@ -181,6 +182,8 @@ def cache_evict(weights, cache, block_table, kv_lens, free_pages, keep: int, rec
     table, table_stride, width = _table_2d(block_table, device, requests)
     w, w_stride = _weights_2d(weights, device, requests, width * cache.shape[1])
     free = _int32(free_pages, device, "free_pages")
+    if max_released is None:
+        max_released = requests * width if released is None else released.numel()
 
     def ints(t, name, *shape):
         if t is None:
