@@ -31,7 +31,8 @@ extern "C" {
  *                   in which a prefix ends may be each request's own copy.)  Negative counts as 0.
  * A request whose rows do not all see the whole prefix, and a request alone in its group, is attended as one in no
  * group.  num_groups 0 to GVR_LONG_MAX_REQUESTS (0: the pointers may be NULL), and as many requests.
- * Where the block table is so narrow, or the requests so few, that sharing is not expected to pay, attend_decode's kernels run.
+ * Where the block table is so narrow, or the requests so few, that sharing is not expected to pay, attend_decode's kernels run.  (By the
+ * table's width and the groups listed, as lengths are on the device: a table no wider than the longest request needs is the best one.)
  * Result, roundings and everything else are as in attend_decode without indices; next_n times num_heads /
  * num_kv_heads is at most 2^19, and num_rows times that quotient at most 2^26.
  *   workspace       16-byte aligned, attend_shared_workspace's bytes.
@@ -45,7 +46,8 @@ gvr_status attend_shared(const gvr_cache* cache, const void* q, int64_t q_row_st
                          int64_t num_groups, float scale, void* out, float* lse, void* workspace,
                          size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that attend_shared needs on the current device for a cache of num_kv_heads heads of head_dim. */
+/* Bytes of workspace that attend_shared needs on the current device for a cache of num_kv_heads heads of head_dim.  Of groups beyond half the
+ * requests, which cannot all share, only a line of the plan each, 48 bytes. */
 gvr_status attend_shared_workspace(int32_t num_kv_heads, int32_t head_dim, int64_t num_rows, int32_t num_heads,
                                    int32_t next_n, int64_t num_groups, size_t* bytes);
 

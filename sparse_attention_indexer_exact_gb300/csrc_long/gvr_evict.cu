@@ -10,9 +10,9 @@
 // entries, copies rows into the new pages and rewrites weights, tables and lists.  Nothing is moved in place: old pages
 // are only read, so copies need no order among each other, and pages that other requests hold stay what they are.
 //
-// What bounds them.  64 requests of up to 5200 entries cut to 4096 (8 heads of 128): 85 to 90 us, of which 67 copy 490 MB in and out
-// at 5.7 TB/s under the profiler (0.85 of the copy rate back to back); the selection's 16 are a chain of barriers, cluster
-// round trips and scans.  One request of 9000: 25 us, 15 and 8.  Five of up to 131072 cut to 20000: 55 to 59, 31 and 23
+// What bounds them.  64 requests of up to 5200 entries cut to 4096 (8 heads of 128): 90 to 93 us, of which 67 to 70 copy 490 MB in and out
+// at 5.7 to 5.8 TB/s under the profiler (0.85 of the copy rate back to back); the selection's 16 are a chain of barriers, cluster
+// round trips and scans.  One request of 9000: 24 to 28 us, 15 and 8.  Five of up to 131072 cut to 20000: 55 to 59, 31 and 23
 // (eight CTAs a request hold 16384 keys each; 40 us before the cluster's histograms were read at once).
 #include <algorithm>
 #include <mutex>

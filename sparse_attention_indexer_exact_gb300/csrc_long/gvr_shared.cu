@@ -22,7 +22,8 @@ SharedDevice g_shared_devices[kMaxDevices];
 // Tails: at most so many tiles of queries, as each expands their entries anew; by a kernel of its own, which few requests are
 // not worth.  128 requests over 3200 entries, 2880 of them common: 96 -> 69 us with 8 KV heads of 128 and 4 queries each,
 // 48 -> 43 with 4 of 64 and 12; 32 requests over 12800: 60 -> 53; 64 of 2 rows behind 32000, 10 to 2000 of their own: 166 -> 165;
-// 27 requests under 2 KV heads of 256 took 17 us more with them.
+// By requests x KV heads, with and without tails: 54 (27 requests, heads of 256) 64 and 43 us, 96 (12, 128) 65 and 56, 100 (25, 64) 35 and 28,
+// 192 (24, 128) 86 and 83, 196 (49, 64) 43.7 and 40.5, 256 (32, 128) 99 and 95, 256 (64, 64) 46 and 46, 512 (64, 128) 167 and 174.
 constexpr int TAIL_TILES = 4, LEAST_TAILS = 256;
 constexpr int64_t MAX_QUERIES = 1 << 26;  // of a KV head: their tiles' numbers share words with flags
 

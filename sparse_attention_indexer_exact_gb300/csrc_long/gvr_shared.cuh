@@ -20,8 +20,8 @@
 //
 // What bounds it (64 requests of 2 rows behind 32000 entries, 64 heads over 8 of 128: 165 us, 0.42 of the tensor cores' measured
 // rate; the plan takes 5 us of it, the tails 35, the shares 112, the join 12; without tails as much in all).  A step of a unit of 256 queries takes 2.2 us, of 128 queries
-// 1.25 (head_dim 64: 1.8 and 1.0; 256, 64 entries and 128 queries: 1.25).  No pipe is busy: the tensor pipe about 55 %, issue
-// 55 %, DRAM 4 %.  What counts is the way of a tile through
+// 1.25 (head_dim 64: 1.8 and 1.0; 256, 64 entries and 128 queries: 1.25).  No pipe is busy: the tensor pipe 52 %, issue
+// 57 %, DRAM 5 %.  What counts is the way of a tile through
 // its step, scores -> maximum -> exponentials -> P -> products -> scores, about 3400 clocks of which the other tile's hide half.
 // Tensor memory has no room for more tiles: at head_dim 128 two times O and S take all of its columns.
 //

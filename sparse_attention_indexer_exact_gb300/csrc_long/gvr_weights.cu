@@ -13,13 +13,13 @@
 // Matrix products by mma.sync, as in gvr_attend.cuh and for its reason: a KV head's queries are few, the 4-bit operand
 // expands in registers straight into that layout.
 //
-// What bounds it.  64 requests of up to 16384 entries, 64 heads over 8 of 128: 103 us under the profiler, 111 over the same
-// inputs again, 121 over other ones each time.  K is half of a row, but its 64
+// What bounds it.  64 requests of up to 16384 entries, 64 heads over 8 of 128: 103 us under the profiler, 107 over the same
+// inputs again, 109 over other ones each time.  K is half of a row, but its 64
 // bytes of codes and 8 of scales, rows being 144 bytes, touch 17 of 18 blocks of 64 bytes, which is what DRAM gives at least:
 // 598 MB, at 5.8 TB/s under the profiler (0.87 of the measured copy rate).  16 rows a request of 6 heads over 4 of 64 (19 requests up to 12345
-// entries): 34.5 us, no pipe busy (before its last step: issue 47 %, tensor 29 %): a CTA has
-// three turns of its warps, each a chain of copy, expansion, products and exponentials, behind its queries' way into shared memory.  One row of 8192 entries: 9.2 us, latency.
-// Steps of 16 entries for few warps took one row from 14.4 to 11 us; the queries fetched a turn ahead and two chains of products the
+// entries): 34.5 to 35.6 us, no pipe busy (before its last step: issue 47 %, tensor 29 %): a CTA has
+// three turns of its warps, each a chain of copy, expansion, products and exponentials, behind its queries' way into shared memory.  One row of 8192 entries: 7.7 us, latency.
+// With the copy of its weights that the benchmark's call makes (1 to 12 us), steps of 16 entries for few warps took one row from 14.4 to 11 us; the queries fetched a turn ahead and two chains of products the
 // batch from 113 to 106; no limits where all rows see an entry the 16 rows from 51 to 43, requests
 // weighed with what they cost beside their steps from 41 to 36.
 #include <algorithm>
